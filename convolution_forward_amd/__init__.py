@@ -11,6 +11,8 @@ GPU, the call raises.
         strides free), F [KH,KW,Cin/groups,Cout] contiguous -> Y [N,Ho,Wo,Cout].
     conv_depthwise(x, w, bias=None, stride=1, padding=0, dilation=1, exact=True)
         Depthwise, X [N,C,H,W], w [C*mult,KH,KW] -> Y [N,C*mult,Ho,Wo].
+    rms_norm_q8, matmul_q8, causal_conv1d, gated_delta_rule
+        The operators of a token mixer round a short causal convolution (mixer.py).
 
 padding is an int (all sides), a pair (rows, columns; the same before and
 after), or four values (top, bottom, left, right).
@@ -36,6 +38,8 @@ CONV_ERR_HIP = 8
 
 CONV_F32 = 0
 CONV_BF16 = 1
+CONV_I8 = 2
+CONV_E4M3 = 3
 CONV_DW_EXACT = 0
 CONV_DW_FAST = 1
 VARIANT_AUTO = 0
@@ -46,7 +50,8 @@ EXPORTED = ("conv2d_nhwc_fwd", "conv2d_nhwc_fwd_variant", "conv2d_nhwc_fwd_windo
             "conv_depthwise_fwd_variant", "conv_depthwise_fwd_window", "conv2d_nhwc_auto_variant",
             "conv2d_nhwc_window_auto_variant", "conv_depthwise_auto_variant", "conv_depthwise_window_auto_variant",
             "conv_out_size", "conv_out_size_window", "conv_status_str", "conv_copy_bytes", "conv_copy_bytes_wide",
-            "conv_im2col_nhwc")
+            "conv_im2col_nhwc", "conv_rms_norm_q8_fwd", "conv_matmul_q8_fwd", "conv_causal1d_fwd",
+            "conv_delta_rule_fwd", "conv_delta_rule_workspace")
 
 
 class ConvWindow(ctypes.Structure):
@@ -114,6 +119,17 @@ def load_library():
     lib.conv_copy_bytes.argtypes = [p, p, i64, p]
     lib.conv_copy_bytes_wide.restype = i
     lib.conv_copy_bytes_wide.argtypes = [p, p, i64, p]
+    f32 = ctypes.c_float
+    lib.conv_rms_norm_q8_fwd.restype = i
+    lib.conv_rms_norm_q8_fwd.argtypes = [p, i64, p, i64, p, p, i64, p, i64, p, i64, i, f32, i, i, p]
+    lib.conv_matmul_q8_fwd.restype = i
+    lib.conv_matmul_q8_fwd.argtypes = [p, i64, p, p, i64, p, p, p, i64, i64, i, i, i, i, i, p]
+    lib.conv_causal1d_fwd.restype = i
+    lib.conv_causal1d_fwd.argtypes = [p, i64, p, p, p, i64, p, p, p, p, i, i64, i, i, i, i, i, p]
+    lib.conv_delta_rule_fwd.restype = i
+    lib.conv_delta_rule_fwd.argtypes = [p] * 12 + [i, p, p, p, i64, i64] + [i] * 5 + [f32] + [i] * 3 + [p]
+    lib.conv_delta_rule_workspace.restype = i64
+    lib.conv_delta_rule_workspace.argtypes = [i64] + [i] * 7
     _lib = lib
     return lib
 
@@ -344,3 +360,6 @@ def copy_bytes(src, dst, nbytes: int | None = None, wide: bool = False):
     _check(fn(src.data_ptr(), dst.data_ptr(), n, _stream_ptr(src.device)),
            "conv_copy_bytes_wide" if wide else "conv_copy_bytes")
     return dst
+
+
+from .mixer import causal_conv1d, delta_rule_workspace, gated_delta_rule, matmul_q8, rms_norm_q8  # noqa: E402,F401

@@ -5,6 +5,7 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include "checks.h"
 #include "internal.h"
 
 using namespace convfwd;
@@ -14,17 +15,6 @@ namespace {
 bool dtype_known(conv_dtype d) { return d == CONV_F32 || d == CONV_BF16; }
 
 int64_t dtype_size(conv_dtype d) { return d == CONV_BF16 ? 2 : 4; }
-
-// Half-open byte range [lo, hi) touched by a strided 4-D tensor with
-// non-negative strides.
-struct Range {
-    uintptr_t lo, hi;
-};
-
-// Largest byte extent of a tensor the library addresses. Kernels form
-// element and byte offsets as int64 sums of index * stride terms, each no
-// larger than the extent, so every such sum stays far from overflow.
-constexpr int64_t MAX_EXTENT_BYTES = int64_t(1) << 60;
 
 // Bytes from the first to one past the last element of a strided 4-D
 // tensor (sizes >= 1, strides >= 0), or -1 when that exceeds
@@ -60,14 +50,6 @@ int64_t flat_bytes4(int64_t a, int64_t b, int64_t c, int64_t d)
         return -1;
     return n;
 }
-
-Range flat_range(const void *base, int64_t bytes)
-{
-    uintptr_t lo = (uintptr_t)base;
-    return Range{lo, lo + (uintptr_t)bytes};
-}
-
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
 // Products of sizes must stay far from int64 overflow; every size here is an
 // int, so four of them fit, but stride arithmetic is checked separately.
@@ -299,13 +281,6 @@ conv_status validate_dw(const float *X, const float *w, const float *bias, float
 }
 
 int dw_auto(const DwProblem &p) { return dw_tiled_supports(p) ? CONV_VARIANT_TILED : CONV_VARIANT_DIRECT; }
-
-conv_status launched(hipError_t e)
-{
-    if (e != hipSuccess)
-        return CONV_ERR_HIP;
-    return hipGetLastError() == hipSuccess ? CONV_OK : CONV_ERR_HIP;
-}
 
 }  // namespace
 

@@ -1,0 +1,165 @@
+// Short causal depthwise convolution over packed sequences, channels
+// adjacent, with a carried state ("Convolution Is Wx+b Moving Across a
+// Signal", section "Where this shows up in models I work with": a causal
+// Conv1D pads only before the signal; here the padding is the state).
+//
+//   y[t,c] = act(bias[c] + sum_j w[c,j] * xx[t - taps + 1 + j, c])
+//
+// A workgroup takes TT tokens of one sequence (tiles never cross sequences)
+// and 256 channel vectors; a thread slides the taps-1 previous rows of its
+// channels along the tile in registers, so each row is read once plus taps-1
+// rows a tile. The first tile of a sequence also writes the sequence's state,
+// after it has read the old one: the two may be the same memory.
+#include "common.h"
+#include "internal.h"
+#include "sequences.h"
+
+namespace convfwd {
+namespace {
+
+constexpr int NT = 256;
+constexpr int TT = 16;
+
+template <class T, int V>
+struct Vec {
+    T v[V];
+};
+
+template <class T, int V>
+__device__ __forceinline__ void load_vec(const T *p, float (&f)[V])
+{
+    Vec<T, V> t;
+    if constexpr (V > 1)
+        t = *reinterpret_cast<const Vec<T, V> *>(__builtin_assume_aligned(p, V * sizeof(T)));
+    else
+        t.v[0] = *p;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        f[i] = load_as_f32(&t.v[i]);
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_vec(T *p, const float (&f)[V])
+{
+    Vec<T, V> t;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        store_from_f32(&t.v[i], f[i]);
+    if constexpr (V > 1)
+        *reinterpret_cast<Vec<T, V> *>(__builtin_assume_aligned(p, V * sizeof(T))) = t;
+    else
+        *p = t.v[0];
+}
+
+template <class T, int V, int K>
+__global__ __launch_bounds__(NT) void causal_conv1d_kernel(Causal1dProblem p)
+{
+    const int c = ((int)blockIdx.y * NT + (int)threadIdx.x) * V;
+    const SeqTile tile = seq_tile(p.seq, TT, (int)blockIdx.x);
+    if (c >= p.channels)
+        return;
+    const int64_t C = p.channels;
+    const T *x = static_cast<const T *>(p.x) + tile.begin * p.xs + c;
+    T *y = static_cast<T *>(p.y) + tile.begin * p.ys + c;
+    const int64_t t0 = (int64_t)tile.index * TT;
+    const bool first = tile.index == 0;
+    if (t0 >= tile.len && !first)
+        return;
+    const int slot = p.state_in || p.state_out ? seq_slot(p.seq, tile.n) : -1;
+    const T *si = p.state_in && slot >= 0 ? static_cast<const T *>(p.state_in) + (int64_t)slot * (K - 1) * C + c : nullptr;
+    // Row t of the sequence; the K-1 before it are the carried ones.
+    auto row = [&](int64_t t, float(&f)[V]) {
+        if (t >= 0)
+            load_vec<T, V>(x + t * p.xs, f);
+        else if (si)
+            load_vec<T, V>(si + (t + K - 1) * C, f);
+        else
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                f[i] = 0.f;
+    };
+    float w[K][V], b[V], win[K][V];
+    const T *wp = static_cast<const T *>(p.w) + (int64_t)c * K;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            w[j][i] = load_as_f32(wp + i * K + j);
+        b[i] = p.bias ? p.bias[c + i] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+        row(t0 - (K - 1) + j, win[j]);
+    const int64_t end = tile.len - t0 < TT ? tile.len - t0 : TT;
+    for (int t = 0; t < end; ++t) {
+        row(t0 + t, win[K - 1]);
+        float f[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float a = b[i];
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                a = fmaf(w[j][i], win[j][i], a);
+            f[i] = p.silu ? a / (1.f + __expf(-a)) : a;
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+                win[j][i] = win[j + 1][i];
+        }
+        store_vec<T, V>(y + (t0 + t) * p.ys, f);
+    }
+    if (first && p.state_out && slot >= 0) {
+        // Ascending: row r of the new state is row len + r of (old state, x),
+        // never an old row that has been overwritten.
+        T *so = static_cast<T *>(p.state_out) + (int64_t)slot * (K - 1) * C + c;
+#pragma unroll
+        for (int r = 0; r < K - 1; ++r) {
+            float f[V];
+            row(tile.len - (K - 1) + r, f);
+            store_vec<T, V>(so + r * C, f);
+        }
+    }
+}
+
+template <class T, int V>
+void launch_taps(const Causal1dProblem &p, hipStream_t s)
+{
+    const int vecs = (p.channels + V - 1) / V;
+    const dim3 grid((unsigned)seq_tiles(p.seq, TT), (unsigned)((vecs + NT - 1) / NT));
+    switch (p.taps) {
+    case 2: hipLaunchKernelGGL((causal_conv1d_kernel<T, V, 2>), grid, dim3(NT), 0, s, p); break;
+    case 3: hipLaunchKernelGGL((causal_conv1d_kernel<T, V, 3>), grid, dim3(NT), 0, s, p); break;
+    case 4: hipLaunchKernelGGL((causal_conv1d_kernel<T, V, 4>), grid, dim3(NT), 0, s, p); break;
+    case 5: hipLaunchKernelGGL((causal_conv1d_kernel<T, V, 5>), grid, dim3(NT), 0, s, p); break;
+    case 6: hipLaunchKernelGGL((causal_conv1d_kernel<T, V, 6>), grid, dim3(NT), 0, s, p); break;
+    case 7: hipLaunchKernelGGL((causal_conv1d_kernel<T, V, 7>), grid, dim3(NT), 0, s, p); break;
+    default: hipLaunchKernelGGL((causal_conv1d_kernel<T, V, 8>), grid, dim3(NT), 0, s, p); break;
+    }
+}
+
+template <class T>
+void launch(const Causal1dProblem &p, hipStream_t s)
+{
+    constexpr int V = 16 / sizeof(T);
+    const uintptr_t bits = (uintptr_t)p.x | (uintptr_t)p.y | (uintptr_t)p.state_in | (uintptr_t)p.state_out |
+                           (uintptr_t)(p.xs * sizeof(T)) | (uintptr_t)(p.ys * sizeof(T)) |
+                           (uintptr_t)(p.channels * sizeof(T));
+    if (bits % 16 == 0)
+        launch_taps<T, V>(p, s);
+    else
+        launch_taps<T, 1>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_causal1d(const Causal1dProblem &p, hipStream_t s)
+{
+    if (seq_tiles(p.seq, TT) > (int64_t(1) << 30) || p.channels > (1 << 23))
+        return hipErrorInvalidValue;
+    if (p.dtype == CONV_BF16)
+        launch<uint16_t>(p, s);
+    else
+        launch<float>(p, s);
+    return hipGetLastError();
+}
+
+}  // namespace convfwd

@@ -87,6 +87,79 @@ struct Im2colProblem {
 
 hipError_t launch_im2col(const Im2colProblem &p, hipStream_t s);
 
+// ---- Token-mixer operators (mixer_api.cpp validates, one file each) --------
+
+// A validated RMS norm with 8-bit output.
+struct NormProblem {
+    const void *x, *residual, *weight;
+    void *h, *q;
+    float *scale;
+    int64_t xs, rs, hs, qs;     // row strides in elements
+    int64_t rows;
+    int width;
+    float eps;
+    conv_dtype dtype, qdt;
+};
+
+hipError_t launch_rms_norm_q8(const NormProblem &p, hipStream_t s);
+
+// A validated product of 8-bit operands.
+struct MatmulQ8Problem {
+    const void *x, *w;
+    const float *xscale, *wscale, *bias;
+    void *y;
+    int64_t xs, ws, ys;         // row strides in elements
+    int64_t M;
+    int N, K;
+    conv_dtype qdt, ydt;
+};
+
+hipError_t launch_matmul_q8_direct(const MatmulQ8Problem &p, hipStream_t s);
+
+// Packed sequences and their state slots (device arrays; seq_offsets NULL =
+// equal lengths, slots NULL = slot n for sequence n).
+struct Sequences {
+    const int32_t *offsets;
+    const int32_t *slots;
+    int num_slots;
+    int num_seqs;
+    int64_t tokens;
+    int64_t each;               // tokens / num_seqs, the length of each where offsets is NULL
+};
+
+// A validated causal convolution over packed sequences.
+struct Causal1dProblem {
+    const void *x, *w;
+    const float *bias;
+    void *y;
+    int64_t xs, ys;             // row strides in elements
+    const void *state_in;
+    void *state_out;
+    Sequences seq;
+    int channels, taps, silu;
+    conv_dtype dtype;
+};
+
+hipError_t launch_causal1d(const Causal1dProblem &p, hipStream_t s);
+
+// A validated gated delta rule.
+struct DeltaProblem {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    void *o;
+    int64_t qst, qsh, kst, ksh, vst, vsh, ost, osh;     // token and head strides in elements
+    const float *state_in;
+    float *state_out;
+    Sequences seq;
+    void *workspace;
+    int Hk, Hv, Dk, Dv;
+    float scale;
+    int normalize;
+    conv_dtype dtype;
+};
+
+hipError_t launch_delta_direct(const DeltaProblem &p, hipStream_t s);
+
 // Streaming copies used for bandwidth / counter calibration.
 hipError_t launch_copy_bytes(const void *src, void *dst, int64_t bytes, hipStream_t s);
 hipError_t launch_copy_wide(const void *src, void *dst, int64_t bytes, hipStream_t s);

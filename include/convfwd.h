@@ -9,7 +9,9 @@
  * dynamic LDS limit has been raised (hipFuncSetAttribute, done on the first
  * launch there and remembered only once it succeeds); calls are thread-safe.
  *
- * Two operators:
+ * Two convolution operators, and at the end of this file the four operators
+ * of a token mixer built round a short causal convolution (norm, 8-bit
+ * product, causal convolution, gated delta rule):
  *
  *  - Dense NHWC cross-correlation, as fixed by "CMU DLSys Lecture 14:
  *    Convolutional Network Implementation", section 1 (the index contract):
@@ -58,7 +60,9 @@ typedef enum conv_status {
 
 typedef enum conv_dtype {
     CONV_F32 = 0,   /* IEEE binary32 */
-    CONV_BF16 = 1   /* bfloat16 (upper half of a binary32) */
+    CONV_BF16 = 1,  /* bfloat16 (upper half of a binary32) */
+    CONV_I8 = 2,    /* signed 8-bit integer, -127 .. 127 (quantised operands only) */
+    CONV_E4M3 = 3   /* 8-bit float, 4 exponent and 3 mantissa bits, no infinities, largest 448 (quantised operands only) */
 } conv_dtype;
 
 typedef enum conv_dw_mode {
@@ -297,6 +301,146 @@ CONVFWD_API conv_status conv_copy_bytes(const void *src, void *dst, int64_t byte
  * CONV_ERR_NULL, CONV_ERR_NONPOSITIVE, CONV_ERR_ALIAS, CONV_ERR_HIP as
  * conv_copy_bytes. */
 CONVFWD_API conv_status conv_copy_bytes_wide(const void *src, void *dst, int64_t bytes, void *stream);
+
+/*
+ * ---- Operators of a token mixer round a short causal convolution ----------
+ *
+ * A mixer layer of a language model normalises its input, projects it (a 1x1
+ * convolution, here with 8-bit operands), runs the causal depthwise Conv1D
+ * that "Convolution Is Wx+b Moving Across a Signal" names (section "Where
+ * this shows up in models I work with") over each sequence, and moves a
+ * per-head state along the sequence. These four calls are that layer. They
+ * are forward operators; each has one form for prompts and for single tokens.
+ *
+ * Rules they share:
+ *  - Tokens are rows, channels are adjacent. Strides are in elements.
+ *  - Packed sequences: `tokens` rows hold num_seqs sequences one after the
+ *    other. seq_offsets is a device array of num_seqs + 1 int32 values,
+ *    sequence n holding rows [seq_offsets[n], seq_offsets[n+1]); empty
+ *    sequences are allowed. NULL means sequences of equal length
+ *    tokens / num_seqs (CONV_ERR_SHAPE when that does not divide). Offsets are
+ *    read on the device; values outside [0, tokens] are clamped to it and
+ *    never lead outside a buffer, but offsets that do not ascend from 0 to
+ *    tokens give unspecified outputs.
+ *  - States: state_in (NULL: every sequence starts from zeros) and state_out
+ *    (NULL: not wanted) hold num_slots states. Sequence n uses slot slots[n]
+ *    (device int32 array of num_seqs values), or slot n where slots is NULL
+ *    (then num_slots >= num_seqs, CONV_ERR_SHAPE otherwise). A slot outside
+ *    [0, num_slots) means: start from zeros, keep nothing. state_out may be
+ *    state_in (updated in place); otherwise the two must not overlap. Slots
+ *    that no sequence names are not touched, and no slot may be named twice.
+ *  - tokens == 0 is allowed: outputs are empty, state_out is still written.
+ *  - Errors: CONV_ERR_NULL (a required pointer), CONV_ERR_NONPOSITIVE (a size
+ *    <= 0 other than tokens or rows, which may be 0), CONV_ERR_SHAPE,
+ *    CONV_ERR_DTYPE, CONV_ERR_LAYOUT (strides below the row they step over, a
+ *    pointer not aligned to its elements, or extents past 2^60 bytes),
+ *    CONV_ERR_ALIAS (an output overlaps an input or another output, except
+ *    as said), CONV_ERR_UNSUPPORTED, CONV_ERR_HIP.
+ */
+
+/*
+ * conv_rms_norm_q8_fwd -- RMS norm with the residual's addition and an
+ * output in 8 bits with one scale a row.
+ *
+ *   h = x + residual, rounded to `dtype` (h = x without a residual)
+ *   y_j = h_j * rsqrt(mean_j(h_j^2) + eps) * weight_j          in fp32
+ *   scale = max_j |y_j| / QMAX,  QMAX = 127 (CONV_I8) or 448 (CONV_E4M3)
+ *   q_j = y_j / scale rounded to nearest, ties to even
+ * A row of zeros has scale 0 and q 0. A row whose mean square or largest
+ * value is not finite has scale NaN and q 0, so it reads back as NaN.
+ *
+ *   x         device [rows, width], row stride x_stride, dtype CONV_F32 or CONV_BF16.
+ *   residual  device [rows, width], row stride r_stride, `dtype`, or NULL.
+ *   weight    device [width], `dtype`.
+ *   h         device [rows, width], row stride h_stride, `dtype`; the sum.
+ *             Required with a residual, and NULL without (CONV_ERR_NULL /
+ *             CONV_ERR_UNSUPPORTED). May be x or residual itself (same
+ *             pointer and stride).
+ *   q         device [rows, width], row stride q_stride, q_dtype.
+ *   scale     device [rows] fp32.
+ */
+CONVFWD_API conv_status conv_rms_norm_q8_fwd(const void *x, int64_t x_stride, const void *residual, int64_t r_stride,
+                                             const void *weight, void *h, int64_t h_stride, void *q,
+                                             int64_t q_stride, float *scale, int64_t rows, int width, float eps,
+                                             conv_dtype dtype, conv_dtype q_dtype, void *stream);
+
+/*
+ * conv_matmul_q8_fwd -- matrix product of 8-bit operands with a scale for
+ * each token and each output channel: a 1x1 convolution in 8 bits.
+ *
+ *   y[m,n] = x_scale[m] * w_scale[n] * sum_{k<K} x[m,k] * w[n,k] + bias[n]
+ *
+ * Sums are exact in 32-bit integers (CONV_I8; K <= 131071, CONV_ERR_UNSUPPORTED
+ * past that) or fp32 (CONV_E4M3, products exact); the scales and the bias are
+ * applied in fp32 and y is rounded once.
+ *
+ *   x        device [M,K], row stride x_stride >= K, q_dtype (CONV_I8 or CONV_E4M3).
+ *   w        device [N,K], row stride w_stride >= K, q_dtype: one row an output channel.
+ *   x_scale  device [M] fp32.   w_scale  device [N] fp32.   bias  device [N] fp32 or NULL.
+ *   y        device [M,N], row stride y_stride >= N, y_dtype (CONV_F32 or CONV_BF16).
+ *   variant  CONV_VARIANT_AUTO or _TILED (matrix cores), or _DIRECT (one
+ *            thread per output); every variant takes every shape.
+ */
+CONVFWD_API conv_status conv_matmul_q8_fwd(const void *x, int64_t x_stride, const float *x_scale, const void *w,
+                                           int64_t w_stride, const float *w_scale, const float *bias, void *y,
+                                           int64_t y_stride, int64_t M, int N, int K, conv_dtype q_dtype,
+                                           conv_dtype y_dtype, int variant, void *stream);
+
+/*
+ * conv_causal1d_fwd -- short causal depthwise convolution over packed
+ * sequences, channels adjacent, with a carried state.
+ *
+ *   y[t,c] = act(bias[c] + sum_{j<taps} w[c,j] * xx[t - taps + 1 + j, c])
+ * where xx is the sequence's taps-1 carried rows (state_in, or zeros)
+ * followed by its tokens; state_out holds the last taps-1 rows of xx. act is
+ * the identity or SiLU, v / (1 + exp(-v)). Sums are fp32, y is rounded once.
+ *
+ *   x, y       device [tokens, channels], row strides x_stride, y_stride, dtype CONV_F32 or CONV_BF16.
+ *   w          device, contiguous [channels, taps], `dtype`; 2 <= taps <= 8 (CONV_ERR_UNSUPPORTED otherwise).
+ *   bias       device [channels] fp32 or NULL.
+ *   state_in, state_out  device, contiguous [num_slots, taps-1, channels], `dtype`.
+ */
+CONVFWD_API conv_status conv_causal1d_fwd(const void *x, int64_t x_stride, const void *w, const float *bias, void *y,
+                                          int64_t y_stride, const int32_t *seq_offsets, const void *state_in,
+                                          void *state_out, const int32_t *slots, int num_slots, int64_t tokens,
+                                          int num_seqs, int channels, int taps, int silu, conv_dtype dtype,
+                                          void *stream);
+
+/*
+ * conv_delta_rule_fwd -- the gated delta rule over packed sequences.
+ *
+ * For each sequence and value head, S [Dk,Dv] in fp32 and token by token:
+ *   S = exp(g_t) S;  u = beta_t (v_t - S^T k_t);  S = S + k_t u^T;  o_t = scale * S^T q_t
+ * Value head h reads query and key head h / (Hv/Hk). With normalize != 0,
+ * q_t and k_t are first divided by sqrt(sum of squares + 1e-6), in fp32.
+ *
+ *   q, k       device [tokens, Hk, Dk], `dtype`; strides: host arrays (token,
+ *              head) in elements, NULL = contiguous. Channels are adjacent.
+ *   v          device [tokens, Hv, Dv], `dtype`, strides likewise.
+ *   g, beta    device, contiguous [tokens, Hv] fp32. g <= 0 is the rule's
+ *              use; g = -inf forgets everything before its token.
+ *   state_in, state_out  device, contiguous [num_slots, Hv, Dk, Dv] fp32.
+ *   o          device [tokens, Hv, Dv], `dtype`, strides likewise.
+ *   workspace  device memory of at least conv_delta_rule_workspace bytes,
+ *              256-byte aligned, used during the call only (NULL when that is 0).
+ *   variant    CONV_VARIANT_DIRECT: token by token, any sizes with Dk <= 256.
+ *              CONV_VARIANT_TILED: by chunks of 64 tokens on the matrix
+ *              cores, bf16 with Dk <= 128. CONV_VARIANT_AUTO picks by the sizes.
+ *              Both compute in fp32 precision.
+ */
+CONVFWD_API conv_status conv_delta_rule_fwd(const void *q, const int64_t *q_strides, const void *k,
+                                            const int64_t *k_strides, const void *v, const int64_t *v_strides,
+                                            const float *g, const float *beta, const int32_t *seq_offsets,
+                                            const float *state_in, float *state_out, const int32_t *slots,
+                                            int num_slots, void *o, const int64_t *o_strides, void *workspace,
+                                            int64_t workspace_bytes, int64_t tokens, int num_seqs, int Hk, int Hv,
+                                            int Dk, int Dv, float scale, int normalize, conv_dtype dtype,
+                                            int variant, void *stream);
+
+/* Bytes of workspace conv_delta_rule_fwd needs for these sizes (0: none), or
+ * -1 where the sizes themselves are an error. Host-only. */
+CONVFWD_API int64_t conv_delta_rule_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, int Dv,
+                                              conv_dtype dtype, int variant);
 
 #ifdef __cplusplus
 }
