@@ -115,6 +115,8 @@ struct MatmulQ8Problem {
 };
 
 hipError_t launch_matmul_q8_direct(const MatmulQ8Problem &p, hipStream_t s);
+bool matmul_q8_tiled_supports(const MatmulQ8Problem &p);
+hipError_t launch_matmul_q8(const MatmulQ8Problem &p, hipStream_t s);
 
 // Packed sequences and their state slots (device arrays; seq_offsets NULL =
 // equal lengths, slots NULL = slot n for sequence n).

@@ -1,0 +1,511 @@
+// Product of 8-bit operands on the matrix cores: a 1x1 convolution in 8 bits.
+//
+//   y[m,n] = xs[m] ws[n] sum_k x[m,k] w[n,k] + b[n]
+//
+// Both operands have K adjacent, so both are staged in LDS as rows of 128
+// bytes (one stage = 128 of K) and a lane's MFMA fragment is 16
+// adjacent bytes of a row; the order of K inside a stage is the same for
+// both, which is all the sum needs.
+//
+// Work decomposition: a workgroup takes TM tokens x TN output channels, its
+// waves 16*MB x 64 pieces of that. Every wave issues its share of a stage's
+// loads (straight into LDS, 1 KB a wave instruction: 8 rows of 128 bytes, one
+// whole line each) NS - 1 stages ahead, into a ring of NS stages: at the top
+// of stage t it waits for its own loads of that stage, and the barrier then
+// says both that everyone's have landed and that everyone has read stage
+// t - 1, whose place stage t + NS - 1 takes.
+//
+// w is the MFMA's row operand, so a lane holds four adjacent channels of one
+// token. The channel that row 4g + i of block nb stands for is chosen as
+// 32 (nb/2) + 8g + 4 (nb%2) + i: two blocks then hold eight adjacent channels
+// a lane, and a wave's 16-byte stores fill 64-byte runs of a token's row.
+#include <type_traits>
+
+#include "common.h"
+#include "eight_bit.h"
+#include "internal.h"
+
+namespace convfwd {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int KS = 128;                 // K bytes of a stage
+constexpr uint32_t OOB = 0x80000000u;
+constexpr int BUF_WORD3 = 0x00020000;
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <bool E4M3>
+struct Acc {
+    using type = f32x4;
+};
+template <>
+struct Acc<false> {
+    using type = i32x4;
+};
+
+// One lane's 16 bytes of an operand as the matrix instructions take them.
+// int8: as they are. e4m3: as 16 bf16 values, exactly. The 8-bit float
+// instructions keep only some 13 bits of a product's place while they add
+// (measured against 64 bits: up to 2^-12.5 of the sum of magnitudes, with
+// either instruction), so their sums are not fp32 sums; the bf16 ones add as
+// fp32 does.
+template <bool E4M3>
+struct Frag {
+    i32x4 v;
+};
+template <>
+struct Frag<true> {
+    bf16x8 v[2];
+};
+
+template <bool E4M3>
+__device__ __forceinline__ Frag<E4M3> frag(i32x4 raw)
+{
+    Frag<E4M3> f;
+    if constexpr (E4M3) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)raw[i], 1.f, false);
+            const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)raw[i], 1.f, true);
+            f.v[i >> 1][4 * (i & 1)] = lo[0];
+            f.v[i >> 1][4 * (i & 1) + 1] = lo[1];
+            f.v[i >> 1][4 * (i & 1) + 2] = hi[0];
+            f.v[i >> 1][4 * (i & 1) + 3] = hi[1];
+        }
+    } else {
+        f.v = raw;
+    }
+    return f;
+}
+
+template <bool E4M3>
+__device__ __forceinline__ typename Acc<E4M3>::type mma(const Frag<E4M3> &a, const Frag<E4M3> &b, typename Acc<E4M3>::type c)
+{
+    if constexpr (E4M3) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[0], b.v[0], c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[1], b.v[1], c, 0, 0, 0);
+    } else {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(a.v, b.v, c, 0, 0, 0);
+    }
+}
+
+// Stored place of 16-byte chunk c of a staged row: the rows of a fragment
+// read must fall in distinct 16-byte columns of the 256 bytes that the banks
+// span (two rows). x reads 16 adjacent rows; w reads rows 8 (r/4) + r%4 + const.
+__device__ __forceinline__ int xswz(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int wswz(int row) { return ((row >> 1) & 1) | (((row >> 3) & 3) << 1); }
+
+struct Q8Args {
+    const uint8_t *x, *w;
+    const float *xscale, *wscale, *bias;
+    void *y;
+    int64_t xs, ws, ys;
+    int M, N, K;
+    int mt, nt;             // tiles
+    int group;              // token tiles that one strip of the tile order spans
+    int stages;
+    int vec;                // y rows take 16-byte stores
+};
+
+// 16 bytes at any address, zeros past the first `left` of them.
+__device__ __forceinline__ i32x4 load16_any(const uint8_t *p, int left)
+{
+    i32x4 v = {0, 0, 0, 0};
+    if (left >= 16) {
+        __builtin_memcpy(&v, p, 16);
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < left; ++i)
+            v[i >> 2] |= (int)((uint32_t)p[i] << (8 * (i & 3)));
+    }
+    return v;
+}
+
+// Where tile number i lies: strips of `group` token tiles, inside a strip
+// channel tile by channel tile, so the tiles in flight on an XCD (consecutive
+// numbers) share a few rows of each operand in its L2.
+__device__ __forceinline__ void place(const Q8Args &a, int i, int &mi, int &ni)
+{
+    const int strip = i / (a.group * a.nt);
+    const int left = a.mt - strip * a.group;
+    const int g = left < a.group ? left : a.group;
+    const int at = i - strip * a.group * a.nt;
+    ni = at / g;
+    mi = strip * a.group + at - ni * g;
+}
+
+template <int V>
+__device__ __forceinline__ void channel_scales(const Q8Args &a, int n, float (&ws)[V], float (&bias)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        ws[i] = n + i < a.N ? a.wscale[n + i] : 0.f;
+        bias[i] = n + i < a.N && a.bias ? a.bias[n + i] : 0.f;
+    }
+}
+
+// V adjacent channels of token m from channel n on: 16-byte stores (8-byte
+// ones for four bf16) where y's rows allow them, else one by one.
+template <int V, bool OUT_BF16>
+__device__ __forceinline__ void store_channels(const Q8Args &a, int m, int n, const float (&v)[V])
+{
+    using T = std::conditional_t<OUT_BF16, uint16_t, float>;
+    T *y = static_cast<T *>(a.y) + (int64_t)m * a.ys + n;
+    T o[V] __attribute__((aligned(16)));
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if constexpr (OUT_BF16)
+            o[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);
+        else
+            o[i] = v[i];
+    if (a.vec && n + V <= a.N) {
+        typedef uint32_t words __attribute__((ext_vector_type(sizeof(T) * V >= 16 ? 4 : 2)));
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) * V / sizeof(words)); ++i)
+            __builtin_nontemporal_store(reinterpret_cast<const words *>(o)[i], reinterpret_cast<words *>(y) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (n + i < a.N)
+                y[i] = o[i];
+    }
+}
+
+template <int MB, int WM, int WN, int NS, bool E4M3, bool OUT_BF16, bool ALIGNED>
+__global__ __launch_bounds__(64 * WM * WN) void matmul_q8_kernel(Q8Args a)
+{
+    using A = typename Acc<E4M3>::type;
+    constexpr int NB = 4;
+    constexpr int TM = 16 * MB * WM, TN = 64 * WN, W = WM * WN;
+    constexpr int XB = TM * KS, STAGE = (TM + TN) * KS;
+    constexpr int LOADS = (TM + TN) / 8 / W;        // wave loads a stage: 8 rows each
+    static_assert(LOADS * 8 * W == TM + TN, "whole loads");
+    extern __shared__ __align__(16) uint8_t ring[];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int g = lane >> 4, r = lane & 15;
+    const int bid = with_args_loaded((int)blockIdx.x, a);
+    // Workgroup i runs on XCD i % 8: give each XCD consecutive tiles.
+    const int tile = (bid & 7) * (int)(gridDim.x >> 3) + (bid >> 3);
+    if (tile >= a.mt * a.nt)
+        return;
+    int mi, ni;
+    place(a, tile, mi, ni);
+    const int m0 = mi * TM, n0 = ni * TN;
+
+    const uint8_t *xbase = a.x + (int64_t)m0 * a.xs;
+    const uint8_t *wbase = a.w + (int64_t)n0 * a.ws;
+    const int xrows = min(TM, a.M - m0), wrows = min(TN, a.N - n0);
+
+    // Load v of this wave fills staged rows 8 (W v + wave) .. + 7 (x's TM
+    // rows, then w's TN); lane L row + L/8, stored chunk L%8.
+    static_assert(TM % (8 * W) == 0, "a load belongs to one operand");
+    auto row_of = [&](int v) __attribute__((always_inline)) { return 8 * (W * v + wave) + (lane >> 3); };
+    auto is_x = [](int v) __attribute__((always_inline)) { return 8 * W * (v + 1) <= TM; };
+    auto k_of = [&](int v) __attribute__((always_inline)) {
+        const int row = row_of(v);
+        return 16 * ((lane & 7) ^ (is_x(v) ? xswz(row) : wswz(row - TM)));
+    };
+
+    // Aligned operands go straight into LDS. Rows past the operand and
+    // chunks past K read zeros (the range check of the buffer).
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(xbase), 0, (int)((xrows - 1) * a.xs + a.K), BUF_WORD3);
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(wbase), 0, (int)((wrows - 1) * a.ws + a.K), BUF_WORD3);
+    uint32_t off[ALIGNED ? LOADS : 1];
+    if constexpr (ALIGNED) {
+#pragma unroll
+        for (int v = 0; v < LOADS; ++v) {
+            const int row = is_x(v) ? row_of(v) : row_of(v) - TM;
+            off[v] = row < (is_x(v) ? xrows : wrows) ? (uint32_t)(row * (int)(is_x(v) ? a.xs : a.ws) + k_of(v)) : OOB;
+        }
+    }
+    auto issue = [&](int t) __attribute__((always_inline)) {
+        uint8_t *dst = ring + (t % NS) * STAGE;
+#pragma unroll
+        for (int v = 0; v < LOADS; ++v) {
+            const uint32_t o = t * KS + k_of(v) < a.K ? off[v] + (uint32_t)(t * KS) : OOB;
+            const auto to = (__attribute__((address_space(3))) void *)(dst + 1024 * (W * v + wave));
+            if (is_x(v))
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, to, 16, o, 0, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, o, 0, 0, 0);
+        }
+    };
+    // Others go through registers, a stage ahead, and are masked byte by byte at the end of K.
+    i32x4 held[ALIGNED ? 1 : LOADS];
+    auto fetch = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+        for (int v = 0; v < LOADS; ++v) {
+            const int row = is_x(v) ? row_of(v) : row_of(v) - TM;
+            const int k = t * KS + k_of(v);
+            held[v] = row < (is_x(v) ? xrows : wrows)
+                          ? load16_any((is_x(v) ? xbase : wbase) + row * (is_x(v) ? a.xs : a.ws) + k, a.K - k)
+                          : i32x4{0, 0, 0, 0};
+        }
+    };
+    auto put = [&](int t) __attribute__((always_inline)) {
+        uint8_t *dst = ring + (t % NS) * STAGE;
+#pragma unroll
+        for (int v = 0; v < LOADS; ++v)
+            *reinterpret_cast<i32x4 *>(dst + 1024 * (W * v + wave) + 16 * lane) = held[v];
+    };
+
+    const int wm = wave / WN, wn = wave % WN;
+    // Fragment addresses within a stage.
+    int xat[2], wat[NB][2];
+    const int xrow = wm * 16 * MB + r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        xat[h] = xrow * KS + 16 * ((4 * h + g) ^ xswz(xrow));
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int row = wn * 64 + 32 * (nb >> 1) + 8 * (r >> 2) + 4 * (nb & 1) + (r & 3);
+            wat[nb][h] = XB + row * KS + 16 * ((4 * h + g) ^ wswz(row));
+        }
+    }
+
+    A acc[MB][NB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+            acc[b][nb] = A{0, 0, 0, 0};
+
+    if constexpr (ALIGNED) {
+#pragma unroll
+        for (int t = 0; t < NS - 1; ++t)
+            issue(t);
+    } else {
+        fetch(0);
+        put(0);
+    }
+    for (int t = 0; t < a.stages; ++t) {
+        if constexpr (ALIGNED)
+            wait_vmcnt<(NS - 2) * LOADS>();
+        lds_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (ALIGNED)
+            issue(t + NS - 1);
+        else
+            fetch(t + 1);
+        const uint8_t *s = ring + (t % NS) * STAGE;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            Frag<E4M3> wf[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+                wf[nb] = frag<E4M3>(*reinterpret_cast<const i32x4 *>(s + wat[nb][h]));
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                const Frag<E4M3> xf = frag<E4M3>(*reinterpret_cast<const i32x4 *>(s + xat[h] + b * 16 * KS));
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    acc[b][nb] = mma<E4M3>(wf[nb], xf, acc[b][nb]);
+            }
+        }
+        if constexpr (!ALIGNED)
+            put(t + 1);
+    }
+    // The stages past the end (zeros) land before the workgroup's LDS is let go.
+    wait_vmcnt<0>();
+
+    // Lane (g, r) holds, of token 16 b + r of the wave's, channels 32 p + 8 g .. + 7 in blocks 2p and 2p + 1.
+    const int nw = n0 + wn * 64 + 8 * g;
+    float ws[2][8], bias[2][8];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+        channel_scales<8>(a, nw + 32 * p, ws[p], bias[p]);
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        const int m = m0 + wm * 16 * MB + 16 * b + r;
+        if (m >= a.M)
+            continue;
+        const float xsc = a.xscale[m];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = (float)acc[b][2 * p + (i >> 2)][i & 3] * xsc * ws[p][i] + bias[p][i];
+            store_channels<8, OUT_BF16>(a, m, nw + 32 * p, v);
+        }
+    }
+}
+
+// Few tokens (at most 16 MB a workgroup): w's bytes are the time, so w goes
+// straight from memory into MFMA fragments, and K is split over the
+// workgroup's eight waves to have as many loads in flight as there is w.
+// Wave i takes K pieces i, i + 8, ... of 128 bytes, four (two at 64 tokens) at a time, and the
+// eight partial sums of a 16-channel block meet in LDS (in a fixed order).
+constexpr int SW = 8;
+
+template <int MB, bool E4M3, bool OUT_BF16, bool ALIGNED>
+__global__ __launch_bounds__(64 * SW) void matmul_q8_few_kernel(Q8Args a)
+{
+    using A = typename Acc<E4M3>::type;
+    __shared__ A part[SW][MB][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int g = lane >> 4, r = lane & 15;
+    const int n0 = with_args_loaded((int)blockIdx.x, a) * 16;
+    const int m0 = (int)blockIdx.y * 16 * MB;
+    // Rows past the operand read its last row; their outputs are not stored.
+    const uint8_t *wrow = a.w + (int64_t)min(n0 + r, a.N - 1) * a.ws + 16 * g;
+    const uint8_t *xrow[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+        xrow[b] = a.x + (int64_t)min(m0 + 16 * b + r, a.M - 1) * a.xs + 16 * g;
+    A acc[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+        acc[b] = A{0, 0, 0, 0};
+    auto load = [&](const uint8_t *row, int k) __attribute__((always_inline)) {
+        if constexpr (ALIGNED)
+            return k + 16 * g < a.K ? *reinterpret_cast<const i32x4 *>(row + k) : i32x4{0, 0, 0, 0};
+        else
+            return load16_any(row + k, a.K - k - 16 * g);
+    };
+    constexpr int U = MB == 4 ? 2 : 4;
+    for (int t = wave; t < a.stages; t += SW * U) {
+        i32x4 wf[U][2], xf[U][MB][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = (t + SW * u) * KS + 64 * h;
+                wf[u][h] = load(wrow, k);
+#pragma unroll
+                for (int b = 0; b < MB; ++b)
+                    xf[u][b][h] = load(xrow[b], k);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const Frag<E4M3> w = frag<E4M3>(wf[u][h]);
+#pragma unroll
+                for (int b = 0; b < MB; ++b)
+                    acc[b] = mma<E4M3>(w, frag<E4M3>(xf[u][b][h]), acc[b]);
+            }
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+        part[wave][b][lane] = acc[b];
+    __syncthreads();
+    // Wave b joins token block b; lane (g, r) has channels 4g .. 4g + 3 of token r.
+    if (wave >= MB)
+        return;
+    A sum = part[0][wave][lane];
+#pragma unroll
+    for (int i = 1; i < SW; ++i)
+        sum += part[i][wave][lane];
+    const int m = m0 + 16 * wave + r, n = n0 + 4 * g;
+    if (m >= a.M)
+        return;
+    float ws[4], bias[4], v[4];
+    channel_scales<4>(a, n, ws, bias);
+    const float xsc = a.xscale[m];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (float)sum[i] * xsc * ws[i] + bias[i];
+    store_channels<4, OUT_BF16>(a, m, n, v);
+}
+
+template <int MB, int WM, int WN, int NS, bool E4M3, bool OB, bool ALIGNED>
+hipError_t launch_tiles(Q8Args &a, hipStream_t s)
+{
+    constexpr int TM = 16 * MB * WM, TN = 64 * WN;
+    constexpr int lds = NS * (TM + TN) * KS;
+    static_assert(lds <= 160 * 1024, "LDS");
+    a.mt = (a.M + TM - 1) / TM;
+    a.nt = (a.N + TN - 1) / TN;
+    a.group = 8;
+    const int64_t tiles = (int64_t)a.mt * a.nt;
+    if (tiles > (int64_t(1) << 30))
+        return hipErrorInvalidValue;
+    const hipError_t attr = allow_lds<matmul_q8_kernel<MB, WM, WN, NS, E4M3, OB, ALIGNED>>(lds);
+    if (attr != hipSuccess)
+        return attr;
+    hipLaunchKernelGGL((matmul_q8_kernel<MB, WM, WN, NS, E4M3, OB, ALIGNED>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                       dim3(64 * WM * WN), lds, s, a);
+    return hipGetLastError();
+}
+
+template <int MB, bool E4M3, bool OB, bool ALIGNED>
+hipError_t launch_few(const Q8Args &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.M + 16 * MB - 1) / (16 * MB)));
+    hipLaunchKernelGGL((matmul_q8_few_kernel<MB, E4M3, OB, ALIGNED>), grid, dim3(64 * SW), 0, s, a);
+    return hipGetLastError();
+}
+
+template <bool E4M3, bool OB, bool ALIGNED>
+hipError_t launch(Q8Args &a, hipStream_t s)
+{
+    if (a.M <= 16)
+        return launch_few<1, E4M3, OB, ALIGNED>(a, s);
+    if (a.M <= 32)
+        return launch_few<2, E4M3, OB, ALIGNED>(a, s);
+    if (a.M <= 64)
+        return launch_few<4, E4M3, OB, ALIGNED>(a, s);
+    const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+    const int64_t mid = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);
+    if (big >= 200)
+        return launch_tiles<8, 2, 4, 2, E4M3, OB, ALIGNED>(a, s);
+    if (mid >= 200)
+        return launch_tiles<4, 2, 2, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
+    return launch_tiles<2, 2, 2, ALIGNED ? 4 : 2, E4M3, OB, ALIGNED>(a, s);
+}
+
+}  // namespace
+
+// Every stride must let a tile's byte offsets stay below 2^31.
+bool matmul_q8_tiled_supports(const MatmulQ8Problem &p)
+{
+    return p.xs <= (1 << 22) && p.ws <= (1 << 22) && p.M <= (1 << 30);
+}
+
+hipError_t launch_matmul_q8(const MatmulQ8Problem &p, hipStream_t s)
+{
+    Q8Args a = {};
+    a.x = static_cast<const uint8_t *>(p.x);
+    a.w = static_cast<const uint8_t *>(p.w);
+    a.xscale = p.xscale;
+    a.wscale = p.wscale;
+    a.bias = p.bias;
+    a.y = p.y;
+    a.xs = p.xs;
+    a.ws = p.ws;
+    a.ys = p.ys;
+    a.M = (int)p.M;
+    a.N = p.N;
+    a.K = p.K;
+    a.stages = (p.K + KS - 1) / KS;
+    const bool bf = p.ydt == CONV_BF16, e = p.qdt == CONV_E4M3;
+    a.vec = ((uintptr_t)p.y | (uintptr_t)(p.ys * (bf ? 2 : 4))) % 16 == 0;
+    const bool aligned =
+        (((uintptr_t)p.x | (uintptr_t)p.w | (uintptr_t)p.xs | (uintptr_t)p.ws | (uintptr_t)p.K) & 15) == 0;
+    if (aligned)
+        return e ? (bf ? launch<true, true, true>(a, s) : launch<true, false, true>(a, s))
+                 : (bf ? launch<false, true, true>(a, s) : launch<false, false, true>(a, s));
+    return e ? (bf ? launch<true, true, false>(a, s) : launch<true, false, false>(a, s))
+             : (bf ? launch<false, true, false>(a, s) : launch<false, false, false>(a, s));
+}
+
+}  // namespace convfwd

@@ -186,7 +186,7 @@ conv_status conv_matmul_q8_fwd(const void *x, int64_t x_stride, const float *x_s
     // 127 * 127 * K, and one lane's -128s, must fit 32 bits: K * 2^14 < 2^31.
     if (M > MAX_ROWS || (q_dtype == CONV_I8 && K > 131071))
         return CONV_ERR_UNSUPPORTED;
-    if (variant != CONV_VARIANT_AUTO && variant != CONV_VARIANT_DIRECT)
+    if (variant != CONV_VARIANT_AUTO && variant != CONV_VARIANT_DIRECT && variant != CONV_VARIANT_TILED)
         return CONV_ERR_UNSUPPORTED;
     const int64_t e = size_of(y_dtype);
     if (x_stride < K || w_stride < K || y_stride < N || !aligned(x_scale, 4) || !aligned(w_scale, 4) ||
@@ -202,7 +202,11 @@ conv_status conv_matmul_q8_fwd(const void *x, int64_t x_stride, const float *x_s
     if (M == 0)
         return CONV_OK;
     const MatmulQ8Problem p = {x, w, x_scale, w_scale, bias, y, x_stride, w_stride, y_stride, M, N, K, q_dtype, y_dtype};
-    return launched(launch_matmul_q8_direct(p, (hipStream_t)stream));
+    const bool tiled = matmul_q8_tiled_supports(p);
+    if (variant == CONV_VARIANT_TILED && !tiled)
+        return CONV_ERR_UNSUPPORTED;
+    return launched(variant == CONV_VARIANT_DIRECT || !tiled ? launch_matmul_q8_direct(p, (hipStream_t)stream)
+                                                             : launch_matmul_q8(p, (hipStream_t)stream));
 }
 
 conv_status conv_causal1d_fwd(const void *x, int64_t x_stride, const void *w, const float *bias, void *y,
