@@ -3,12 +3,12 @@
 //   y[m,n] = xs[m] ws[n] sum_k x[m,k] w[n,k] + b[n]
 //
 // Both operands have K adjacent, so both are staged in LDS as rows of 128
-// bytes (one stage = 128 of K) and a lane's MFMA fragment is 16
+// bytes (a stage is one or two such pieces of K) and a lane's MFMA fragment is 16
 // adjacent bytes of a row; the order of K inside a stage is the same for
 // both, which is all the sum needs.
 //
 // Work decomposition: a workgroup takes TM tokens x TN output channels, its
-// waves 16*MB x 64 pieces of that. Every wave issues its share of a stage's
+// waves 16*MB x 16*NB pieces of that. Every wave issues its share of a stage's
 // loads (straight into LDS, 1 KB a wave instruction: 8 rows of 128 bytes, one
 // whole line each) NS - 1 stages ahead, into a ring of NS stages: at the top
 // of stage t it waits for its own loads of that stage, and the barrier then
@@ -34,7 +34,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int KS = 128;                 // K bytes of a stage
+constexpr int KS = 128;                 // K bytes of a piece
 constexpr uint32_t OOB = 0x80000000u;
 constexpr int BUF_WORD3 = 0x00020000;
 
@@ -116,7 +116,8 @@ struct Q8Args {
     int M, N, K;
     int mt, nt;             // tiles
     int group;              // token tiles that one strip of the tile order spans
-    int stages;
+    int pieces;             // of K
+    int stages;             // for the tiles: pieces / SUB, rounded up
     int vec;                // y rows take 16-byte stores
 };
 
@@ -184,15 +185,16 @@ __device__ __forceinline__ void store_channels(const Q8Args &a, int m, int n, co
     }
 }
 
-template <int MB, int WM, int WN, int NS, bool E4M3, bool OUT_BF16, bool ALIGNED>
+template <int MB, int NB, int WM, int WN, int SUB, int NS, bool E4M3, bool OUT_BF16, bool ALIGNED>
 __global__ __launch_bounds__(64 * WM * WN) void matmul_q8_kernel(Q8Args a)
 {
     using A = typename Acc<E4M3>::type;
-    constexpr int NB = 4;
-    constexpr int TM = 16 * MB * WM, TN = 64 * WN, W = WM * WN;
-    constexpr int XB = TM * KS, STAGE = (TM + TN) * KS;
-    constexpr int LOADS = (TM + TN) / 8 / W;        // wave loads a stage: 8 rows each
-    static_assert(LOADS * 8 * W == TM + TN, "whole loads");
+    constexpr int TM = 16 * MB * WM, TN = 16 * NB * WN, W = WM * WN;
+    constexpr int XB = TM * KS, PIECE = (TM + TN) * KS, STAGE = SUB * PIECE;
+    constexpr int LOADS1 = (TM + TN) / 8 / W;       // wave loads of a piece of K: 8 rows each
+    constexpr int LOADS = SUB * LOADS1;             // and of a stage
+    constexpr int PER = (LOADS1 + 2 * MB - 1) / (2 * MB);
+    static_assert(LOADS1 * 8 * W == TM + TN, "whole loads");
     extern __shared__ __align__(16) uint8_t ring[];
 
     const int lane = threadIdx.x & 63;
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_q8_kernel(Q8Args a)
     const int xrows = min(TM, a.M - m0), wrows = min(TN, a.N - n0);
 
     // Load v of this wave fills staged rows 8 (W v + wave) .. + 7 (x's TM
-    // rows, then w's TN); lane L row + L/8, stored chunk L%8.
+    // rows, then w's TN) of each piece; lane L row + L/8, stored chunk L%8.
     static_assert(TM % (8 * W) == 0, "a load belongs to one operand");
     auto row_of = [&](int v) __attribute__((always_inline)) { return 8 * (W * v + wave) + (lane >> 3); };
     auto is_x = [](int v) __attribute__((always_inline)) { return 8 * W * (v + 1) <= TM; };
@@ -227,43 +229,39 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_q8_kernel(Q8Args a)
         const_cast<uint8_t *>(xbase), 0, (int)((xrows - 1) * a.xs + a.K), BUF_WORD3);
     const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint8_t *>(wbase), 0, (int)((wrows - 1) * a.ws + a.K), BUF_WORD3);
-    uint32_t off[ALIGNED ? LOADS : 1];
+    uint32_t off[ALIGNED ? LOADS1 : 1];
     if constexpr (ALIGNED) {
 #pragma unroll
-        for (int v = 0; v < LOADS; ++v) {
+        for (int v = 0; v < LOADS1; ++v) {
             const int row = is_x(v) ? row_of(v) : row_of(v) - TM;
             off[v] = row < (is_x(v) ? xrows : wrows) ? (uint32_t)(row * (int)(is_x(v) ? a.xs : a.ws) + k_of(v)) : OOB;
         }
     }
-    auto issue = [&](int t) __attribute__((always_inline)) {
-        uint8_t *dst = ring + (t % NS) * STAGE;
-#pragma unroll
-        for (int v = 0; v < LOADS; ++v) {
-            const uint32_t o = t * KS + k_of(v) < a.K ? off[v] + (uint32_t)(t * KS) : OOB;
-            const auto to = (__attribute__((address_space(3))) void *)(dst + 1024 * (W * v + wave));
-            if (is_x(v))
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, to, 16, o, 0, 0, 0);
-            else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, o, 0, 0, 0);
-        }
+    // Load v of the piece that starts at k0, into its place at dst.
+    auto issue_one = [&](uint8_t *dst, int k0, int v) __attribute__((always_inline)) {
+        const uint32_t o = k0 + k_of(v) < a.K ? off[v] + (uint32_t)k0 : OOB;
+        const auto to = (__attribute__((address_space(3))) void *)(dst + 1024 * (W * v + wave));
+        if (is_x(v))
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, to, 16, o, 0, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, to, 16, o, 0, 0, 0);
     };
     // Others go through registers, a stage ahead, and are masked byte by byte at the end of K.
     i32x4 held[ALIGNED ? 1 : LOADS];
     auto fetch = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
         for (int v = 0; v < LOADS; ++v) {
-            const int row = is_x(v) ? row_of(v) : row_of(v) - TM;
-            const int k = t * KS + k_of(v);
-            held[v] = row < (is_x(v) ? xrows : wrows)
-                          ? load16_any((is_x(v) ? xbase : wbase) + row * (is_x(v) ? a.xs : a.ws) + k, a.K - k)
+            const int i = v % LOADS1, row = is_x(i) ? row_of(i) : row_of(i) - TM;
+            const int k = (t * SUB + v / LOADS1) * KS + k_of(i);
+            held[v] = row < (is_x(i) ? xrows : wrows)
+                          ? load16_any((is_x(i) ? xbase : wbase) + row * (is_x(i) ? a.xs : a.ws) + k, a.K - k)
                           : i32x4{0, 0, 0, 0};
         }
     };
-    auto put = [&](int t) __attribute__((always_inline)) {
-        uint8_t *dst = ring + (t % NS) * STAGE;
+    auto put = [&](uint8_t *dst) __attribute__((always_inline)) {
 #pragma unroll
         for (int v = 0; v < LOADS; ++v)
-            *reinterpret_cast<i32x4 *>(dst + 1024 * (W * v + wave) + 16 * lane) = held[v];
+            *reinterpret_cast<i32x4 *>(dst + v / LOADS1 * PIECE + 1024 * (W * (v % LOADS1) + wave) + 16 * lane) = held[v];
     };
 
     const int wm = wave / WN, wn = wave % WN;
@@ -275,7 +273,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_q8_kernel(Q8Args a)
         xat[h] = xrow * KS + 16 * ((4 * h + g) ^ xswz(xrow));
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int row = wn * 64 + 32 * (nb >> 1) + 8 * (r >> 2) + 4 * (nb & 1) + (r & 3);
+            const int row = wn * 16 * NB + 32 * (nb >> 1) + 8 * (r >> 2) + 4 * (nb & 1) + (r & 3);
             wat[nb][h] = XB + row * KS + 16 * ((4 * h + g) ^ wswz(row));
         }
     }
@@ -289,47 +287,62 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_q8_kernel(Q8Args a)
 
     if constexpr (ALIGNED) {
 #pragma unroll
-        for (int t = 0; t < NS - 1; ++t)
-            issue(t);
+        for (int v = 0; v < (NS - 1) * LOADS; ++v)
+            issue_one(ring + v / LOADS1 * PIECE, v / LOADS1 * KS, v % LOADS1);
     } else {
         fetch(0);
-        put(0);
+        put(ring);
     }
+    int use = 0, fill = (NS - 1) * STAGE;           // places of stage t and of stage t + NS - 1
     for (int t = 0; t < a.stages; ++t) {
         if constexpr (ALIGNED)
             wait_vmcnt<(NS - 2) * LOADS>();
         lds_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (ALIGNED)
-            issue(t + NS - 1);
-        else
+        if constexpr (!ALIGNED)
             fetch(t + 1);
-        const uint8_t *s = ring + (t % NS) * STAGE;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            Frag<E4M3> wf[NB];
+        for (int sub = 0; sub < SUB; ++sub) {
+            const uint8_t *s = ring + use + sub * PIECE;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-                wf[nb] = frag<E4M3>(*reinterpret_cast<const i32x4 *>(s + wat[nb][h]));
-#pragma unroll
-            for (int b = 0; b < MB; ++b) {
-                const Frag<E4M3> xf = frag<E4M3>(*reinterpret_cast<const i32x4 *>(s + xat[h] + b * 16 * KS));
+            for (int h = 0; h < 2; ++h) {
+                Frag<E4M3> wf[NB];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
-                    acc[b][nb] = mma<E4M3>(wf[nb], xf, acc[b][nb]);
+                    wf[nb] = frag<E4M3>(*reinterpret_cast<const i32x4 *>(s + wat[nb][h]));
+#pragma unroll
+                for (int b = 0; b < MB; ++b) {
+                    const Frag<E4M3> xf = frag<E4M3>(*reinterpret_cast<const i32x4 *>(s + xat[h] + b * 16 * KS));
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        acc[b][nb] = mma<E4M3>(wf[nb], xf, acc[b][nb]);
+                    if constexpr (ALIGNED) {
+                        // The next loads, a few between the products: a wave is held some 150 clocks for each of
+                        // them, and all at once they left the matrix cores idle (265 us against 243 at
+                        // 8192x8192x4096). Products and loads keep their order; LDS reads and VALU work may move
+                        // across.
+                        __builtin_amdgcn_sched_barrier(0x386);
+#pragma unroll
+                        for (int v = (h * MB + b) * PER; v < (h * MB + b + 1) * PER; ++v)
+                            if (v < LOADS1)
+                                issue_one(ring + fill + sub * PIECE, ((t + NS - 1) * SUB + sub) * KS, v);
+                    }
+                }
             }
         }
         if constexpr (!ALIGNED)
-            put(t + 1);
+            put(ring + fill);
+        use = use + STAGE == NS * STAGE ? 0 : use + STAGE;
+        fill = fill + STAGE == NS * STAGE ? 0 : fill + STAGE;
     }
     // The stages past the end (zeros) land before the workgroup's LDS is let go.
     wait_vmcnt<0>();
 
     // Lane (g, r) holds, of token 16 b + r of the wave's, channels 32 p + 8 g .. + 7 in blocks 2p and 2p + 1.
-    const int nw = n0 + wn * 64 + 8 * g;
-    float ws[2][8], bias[2][8];
+    const int nw = n0 + wn * 16 * NB + 8 * g;
+    float ws[NB / 2][8], bias[NB / 2][8];
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < NB / 2; ++p)
         channel_scales<8>(a, nw + 32 * p, ws[p], bias[p]);
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
@@ -338,7 +351,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_q8_kernel(Q8Args a)
             continue;
         const float xsc = a.xscale[m];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
+        for (int p = 0; p < NB / 2; ++p) {
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -351,7 +364,7 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_q8_kernel(Q8Args a)
 // Few tokens (at most 16 MB a workgroup): w's bytes are the time, so w goes
 // straight from memory into MFMA fragments, and K is split over the
 // workgroup's eight waves to have as many loads in flight as there is w.
-// Wave i takes K pieces i, i + 8, ... of 128 bytes, four (two at 64 tokens) at a time, and the
+// Wave i takes K pieces i, i + 8, ... of 128 bytes, four at a time, and the
 // eight partial sums of a 16-channel block meet in LDS (in a fixed order).
 constexpr int SW = 8;
 
@@ -381,8 +394,8 @@ __global__ __launch_bounds__(64 * SW) void matmul_q8_few_kernel(Q8Args a)
         else
             return load16_any(row + k, a.K - k - 16 * g);
     };
-    constexpr int U = MB == 4 ? 2 : 4;
-    for (int t = wave; t < a.stages; t += SW * U) {
+    constexpr int U = 4;
+    for (int t = wave; t < a.pieces; t += SW * U) {
         i32x4 wf[U][2], xf[U][MB][2];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -427,22 +440,23 @@ __global__ __launch_bounds__(64 * SW) void matmul_q8_few_kernel(Q8Args a)
     store_channels<4, OUT_BF16>(a, m, n, v);
 }
 
-template <int MB, int WM, int WN, int NS, bool E4M3, bool OB, bool ALIGNED>
+template <int MB, int NB, int WM, int WN, int SUB, int NS, bool E4M3, bool OB, bool ALIGNED>
 hipError_t launch_tiles(Q8Args &a, hipStream_t s)
 {
-    constexpr int TM = 16 * MB * WM, TN = 64 * WN;
-    constexpr int lds = NS * (TM + TN) * KS;
+    constexpr int TM = 16 * MB * WM, TN = 16 * NB * WN;
+    constexpr int lds = NS * SUB * (TM + TN) * KS;
     static_assert(lds <= 160 * 1024, "LDS");
     a.mt = (a.M + TM - 1) / TM;
     a.nt = (a.N + TN - 1) / TN;
     a.group = 8;
+    a.stages = (a.pieces + SUB - 1) / SUB;
     const int64_t tiles = (int64_t)a.mt * a.nt;
     if (tiles > (int64_t(1) << 30))
         return hipErrorInvalidValue;
-    const hipError_t attr = allow_lds<matmul_q8_kernel<MB, WM, WN, NS, E4M3, OB, ALIGNED>>(lds);
+    const hipError_t attr = allow_lds<matmul_q8_kernel<MB, NB, WM, WN, SUB, NS, E4M3, OB, ALIGNED>>(lds);
     if (attr != hipSuccess)
         return attr;
-    hipLaunchKernelGGL((matmul_q8_kernel<MB, WM, WN, NS, E4M3, OB, ALIGNED>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+    hipLaunchKernelGGL((matmul_q8_kernel<MB, NB, WM, WN, SUB, NS, E4M3, OB, ALIGNED>), dim3((unsigned)((tiles + 7) / 8 * 8)),
                        dim3(64 * WM * WN), lds, s, a);
     return hipGetLastError();
 }
@@ -458,19 +472,36 @@ hipError_t launch_few(const Q8Args &a, hipStream_t s)
 template <bool E4M3, bool OB, bool ALIGNED>
 hipError_t launch(Q8Args &a, hipStream_t s)
 {
+    // Up to 32 tokens the few-token form is the faster one (8 x 4096 x 4096:
+    // 6.5 us against 9.4 on 64x64 tiles; 32: 9.0 against 9.7), past that the
+    // tiles are (64 x 8192 x 4096: 13.9 us against 24).
     if (a.M <= 16)
         return launch_few<1, E4M3, OB, ALIGNED>(a, s);
     if (a.M <= 32)
         return launch_few<2, E4M3, OB, ALIGNED>(a, s);
-    if (a.M <= 64)
-        return launch_few<4, E4M3, OB, ALIGNED>(a, s);
-    const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
-    const int64_t mid = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);
-    if (big >= 200)
-        return launch_tiles<8, 2, 4, 2, E4M3, OB, ALIGNED>(a, s);
-    if (mid >= 200)
-        return launch_tiles<4, 2, 2, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
-    return launch_tiles<2, 2, 2, ALIGNED ? 4 : 2, E4M3, OB, ALIGNED>(a, s);
+    // The tile whose rounds over the 256 compute units cost least. A round's
+    // cost is its time at K = 4096 over the 64x64 tile's (int8: 8.9, 12.5,
+    // 17.3, 27, 43 us; e4m3 15.8, 20, 32, 49, 81): the larger a tile, the fewer
+    // bytes it loads for each product, and the longer it holds its unit. (1024
+    // x 8192 x 4096: 128x256 36 us, 128x128 45, 256x256 52; 512 x 4096 x
+    // 4096: 64x128 14.7, 64x64 17.7, 128x128 19.)
+    auto cost = [&](int tm, int tn, int each) {
+        const int64_t tiles = (int64_t)((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn);
+        return (tiles + 255) / 256 * each;
+    };
+    const int64_t costs[5] = {cost(256, 256, 48), cost(128, 256, 31), cost(128, 128, 20), cost(64, 128, 14),
+                              cost(64, 64, 10)};
+    int best = 0;
+    for (int i = 1; i < 5; ++i)
+        if (costs[i] < costs[best])
+            best = i;
+    switch (best) {
+    case 0: return launch_tiles<8, 4, 2, 4, 1, 2, E4M3, OB, ALIGNED>(a, s);
+    case 1: return launch_tiles<4, 4, 2, 4, 1, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
+    case 2: return launch_tiles<4, 2, 2, 4, 1, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
+    case 3: return launch_tiles<2, 2, 2, 4, 1, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
+    default: return launch_tiles<1, 2, 4, 2, 2, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
+    }
 }
 
 }  // namespace
@@ -496,7 +527,7 @@ hipError_t launch_matmul_q8(const MatmulQ8Problem &p, hipStream_t s)
     a.M = (int)p.M;
     a.N = p.N;
     a.K = p.K;
-    a.stages = (p.K + KS - 1) / KS;
+    a.pieces = (p.K + KS - 1) / KS;
     const bool bf = p.ydt == CONV_BF16, e = p.qdt == CONV_E4M3;
     a.vec = ((uintptr_t)p.y | (uintptr_t)(p.ys * (bf ? 2 : 4))) % 16 == 0;
     const bool aligned =
