@@ -1,0 +1,666 @@
+// The gated delta rule by chunks of 64 tokens on the matrix cores, bf16
+// operands, in fp32 precision.
+//
+// Inside a chunk let G_i be the sum of the gates up to token i, r_i the factor
+// that normalises k_i (1 without), and S the state before the chunk. With
+//   A_ij = beta_i r_i r_j exp(G_i - G_j) (k_i . k_j)   for j < i, else 0
+//   P_ij = scale rq_i r_j exp(G_i - G_j) (q_i . k_j)   for j <= i, else 0
+// the rule's 64 steps are
+//   U  = (1 + A)^-1 diag(beta) (V - diag(r exp G) K S)
+//   O  = diag(scale rq exp G) Q S + P U
+//   S' = exp(G_63) S + K^T diag(r_i exp(G_63 - G_i)) U.
+// No exponent is ever positive for gates <= 0, and differences of G are taken
+// in 64 bits, so a strong gate early in a chunk costs the later ones nothing.
+//
+// Two kernels. The first takes every chunk and key head at once and writes
+// what does not depend on S: T = (1 + A)^-1 diag(beta), P, the row factors,
+// and K, Q and K^T, all in the order in which the second one's matrix
+// instructions take them. The second carries S along each sequence. Columns
+// of S are independent, so a workgroup takes 16 CB of them; its four waves
+// share the rows.
+//
+// Precision: bf16 operands (K, Q) are exact, every other operand of a product
+// is split into bf16 parts x = hi + mid + lo (each the nearest bf16 of what is
+// left, 24 bits together), and the products of parts above 2^-24 are added in
+// fp32: three for an exact operand times a split one, six for two split ones.
+// What only o sees (bf16 for these operands) uses two parts, 2^-17.
+//
+// Values that are not finite: a zero of T or P times a NaN would carry it to
+// earlier tokens. So rows of K that hold one are read as zeros, and values of
+// V - .. that are not finite as zeros, and the token is noted; from it on the
+// outputs and the final state are set to NaN, for all columns (K, g, beta) or
+// for its own (V, S).
+#include "common.h"
+#include "internal.h"
+#include "sequences.h"
+
+namespace convfwd {
+namespace {
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int C = 64;                   // tokens of a chunk
+constexpr int NT = 256;
+constexpr float UNIT_EPS = 1e-6f;
+constexpr int NEVER = 0x7fffffff;
+
+// Token (within the chunk) of row r of token tile i. Tiles 2s and 2s + 1
+// interleave, so that a lane's four rows of each, as results leave the matrix
+// cores, are eight adjacent tokens: the K order of the next product.
+__device__ __forceinline__ int token_of(int i, int r) { return 32 * (i >> 1) + 8 * (r >> 2) + 4 * (i & 1) + (r & 3); }
+
+// ---- Workspace ---------------------------------------------------------------
+// For each chunk number and key head: K and Q, 4 tiles x 4 waves fragments
+// each, K^T, 4 waves x DT x 2. For each chunk number and value head: T, 3
+// parts of the 6 fragments that are not all zero, P, 2 parts of them, then 4
+// x 64 row factors and a header. A fragment is 64 lanes x 16 bytes.
+constexpr int FRAG = 1024;
+
+template <int DT>
+struct Space {
+    static constexpr int Q = 16 * FRAG, KT = 32 * FRAG, KEY = KT + 8 * DT * FRAG;
+    static constexpr int P = 18 * FRAG, UPK = 30 * FRAG, UPQ = UPK + 256, TAIL = UPQ + 256, HEAD = TAIL + 256;
+    static constexpr int VAL = 31 * FRAG;       // HEAD: exp(G_63), first token that is not finite
+};
+
+// Place of fragment (tile i, K step s) among the six of a lower triangle.
+__device__ __forceinline__ int low_frag(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }
+
+struct ChunkArgs {
+    DeltaProblem p;
+    uint8_t *keys, *vals;       // workspace
+    int vec;                    // rows of q and k take 16-byte loads
+    int vec_o;                  // rows of o take 8-byte stores
+    int slices;                 // column slices of a head
+};
+
+__device__ __forceinline__ __bf16 part_of(float &x)
+{
+    const __bf16 h = (__bf16)x;
+    x -= (float)h;
+    return h;
+}
+
+template <int DT>
+__global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
+{
+    using W = Space<DT>;
+    constexpr int D = 64 * DT, PITCH = D + 8, MP = 68;
+    const DeltaProblem &p = a.p;
+    __shared__ __align__(16) uint16_t ks[C * PITCH], qs[C * PITCH];
+    __shared__ __align__(16) float m[C * MP], pm[C * MP], z[4][16 * 17];
+    __shared__ double gs[C];
+    __shared__ float rk[C], rq[C], bs[C];
+    __shared__ int badrow[C];
+
+    const int kh = (int)blockIdx.y;
+    const SeqTile tile = seq_tile(p.seq, C, (int)blockIdx.x);
+    const int64_t t0 = (int64_t)tile.index * C;
+    if (t0 >= tile.len)
+        return;
+    const int rows = (int)(tile.len - t0 < C ? tile.len - t0 : C);
+    const int64_t first = tile.begin + t0;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, r = lane & 15;
+
+    // Rows of K and Q, zeros past the sequence's end and past Dk.
+    if (tid < C)
+        badrow[tid] = 0;
+    for (int i = tid; i < C * MP; i += NT)
+        m[i] = pm[i] = 0.f;
+    __syncthreads();
+    for (int i = tid; i < C * D / 8; i += NT) {
+        const int row = i / (D / 8), c = i % (D / 8) * 8;
+        uint16_t kv[8] __attribute__((aligned(16))) = {}, qv[8] __attribute__((aligned(16))) = {};
+        if (row < rows) {
+            const uint16_t *kp = static_cast<const uint16_t *>(p.k) + (first + row) * p.kst + kh * p.ksh + c;
+            const uint16_t *qp = static_cast<const uint16_t *>(p.q) + (first + row) * p.qst + kh * p.qsh + c;
+            if (a.vec && c + 8 <= p.Dk) {
+                *reinterpret_cast<u32x4 *>(kv) = *reinterpret_cast<const u32x4 *>(kp);
+                *reinterpret_cast<u32x4 *>(qv) = *reinterpret_cast<const u32x4 *>(qp);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < p.Dk) {
+                        kv[e] = kp[e];
+                        qv[e] = qp[e];
+                    }
+            }
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if ((kv[e] & 0x7f80) == 0x7f80) {
+                    kv[e] = 0;
+                    bad = true;
+                }
+            if (bad)
+                badrow[row] = 1;
+        }
+        *reinterpret_cast<u32x4 *>(ks + row * PITCH + c) = *reinterpret_cast<const u32x4 *>(kv);
+        *reinterpret_cast<u32x4 *>(qs + row * PITCH + c) = *reinterpret_cast<const u32x4 *>(qv);
+    }
+    __syncthreads();
+    {   // four threads a row
+        const int row = tid >> 2;
+        float sk = 0.f, sq = 0.f;
+        for (int c = tid & 3; c < D; c += 4) {
+            const float x = bf16_to_f32(ks[row * PITCH + c]), y = bf16_to_f32(qs[row * PITCH + c]);
+            sk = fmaf(x, x, sk);
+            sq = fmaf(y, y, sq);
+        }
+        sk += __shfl_xor(sk, 1);
+        sk += __shfl_xor(sk, 2);
+        sq += __shfl_xor(sq, 1);
+        sq += __shfl_xor(sq, 2);
+        if ((tid & 3) == 0) {
+            rk[row] = p.normalize ? 1.f / sqrtf(sk + UNIT_EPS) : 1.f;
+            rq[row] = (p.normalize ? 1.f / sqrtf(sq + UNIT_EPS) : 1.f) * p.scale;
+        }
+    }
+
+    // K, Q and K^T as fragments.
+    uint8_t *key = a.keys + ((int64_t)blockIdx.x * p.Hk + kh) * W::KEY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {       // wave w writes what wave w of the second kernel reads
+        const int at = token_of(i, r) * PITCH + (DT == 2 ? 32 * w + 8 * g : 16 * w + 4 * g);
+        u32x4 kf = {0, 0, 0, 0}, qf = {0, 0, 0, 0};
+        if constexpr (DT == 2) {
+            kf = *reinterpret_cast<const u32x4 *>(ks + at);
+            qf = *reinterpret_cast<const u32x4 *>(qs + at);
+        } else {
+            const u32x2 k2 = *reinterpret_cast<const u32x2 *>(ks + at), q2 = *reinterpret_cast<const u32x2 *>(qs + at);
+            kf[0] = k2[0], kf[1] = k2[1];
+            qf[0] = q2[0], qf[1] = q2[1];
+        }
+        reinterpret_cast<u32x4 *>(key + (4 * i + w) * FRAG)[lane] = kf;
+        reinterpret_cast<u32x4 *>(key + W::Q + (4 * i + w) * FRAG)[lane] = qf;
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int dk = DT == 2 ? 32 * w + 8 * (r >> 2) + 4 * d + (r & 3) : 16 * w + r;
+            u32x4 f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint16_t *at = ks + (32 * s + 8 * g + 2 * e) * PITCH + dk;
+                f[e] = (uint32_t)at[0] | ((uint32_t)at[PITCH] << 16);
+            }
+            reinterpret_cast<u32x4 *>(key + W::KT + ((w * DT + d) * 2 + s) * FRAG)[lane] = f;
+        }
+
+    // Row tile w of K K^T and Q K^T (rows in token order here).
+    f32x4 kk[4], qk[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        kk[j] = qk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+        const int c = 32 * s + 8 * g;
+        const bf16x8 ka = *reinterpret_cast<const bf16x8 *>(ks + (16 * w + r) * PITCH + c);
+        const bf16x8 qa = *reinterpret_cast<const bf16x8 *>(qs + (16 * w + r) * PITCH + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j <= w) {
+                const bf16x8 kb = *reinterpret_cast<const bf16x8 *>(ks + (16 * j + r) * PITCH + c);
+                kk[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, kb, kk[j], 0, 0, 0);
+                qk[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qa, kb, qk[j], 0, 0, 0);
+            }
+    }
+
+    const int group = p.Hv / p.Hk;
+    for (int h = kh * group; h < (kh + 1) * group; ++h) {
+        // Sums of the gates, in 64 bits; a total gate counts as exp(-10000) = 0.
+        float gate = 0.f, beta = 0.f;
+        if (lane < rows) {
+            gate = p.g[(first + lane) * p.Hv + h];
+            beta = p.beta[(first + lane) * p.Hv + h];
+        }
+        const bool bad = !(gate < INFINITY) || !(fabsf(beta) < INFINITY) || badrow[lane];
+        if (bad) {
+            gate = gate < INFINITY ? gate : 0.f;
+            beta = 0.f;
+        }
+        const uint64_t bads = __ballot(bad);
+        double G = (double)fmaxf(gate, -1e4f);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double o = __shfl_up(G, d);
+            if (lane >= d)
+                G += o;
+        }
+        __syncthreads();
+        if (w == 0) {
+            gs[lane] = G;
+            bs[lane] = beta;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j <= w) {
+                const int col = 16 * j + r;
+                const double gc = gs[col];
+                const float rc = rk[col];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 16 * w + 4 * g + e;
+                    const float d = row >= col ? expf((float)(gs[row] - gc)) * rc : 0.f;
+                    m[row * MP + col] = row > col ? bs[row] * rk[row] * d * kk[j][e] : 0.f;
+                    pm[row * MP + col] = row >= col ? rq[row] * d * qk[j][e] : 0.f;
+                }
+            }
+        __syncthreads();
+        // (1 + A)^-1: the 16x16 blocks on the diagonal by substitution, lane c
+        // a column, then blocks twice as large from
+        //   [[X, 0], [A, Y]]^-1 = [[X^-1, 0], [-Y^-1 A X^-1, Y^-1]].
+        if (lane < 16) {
+            float col[16];
+            float *b = m + 16 * w * MP + 16 * w;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float x = i == lane ? 1.f : 0.f;
+#pragma unroll
+                for (int j = 0; j < i; ++j)
+                    x = fmaf(-b[i * MP + j], col[j], x);
+                col[i] = x;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                b[i * MP + lane] = col[i];
+        }
+        __syncthreads();
+        if (w < 2) {
+            const int i = 2 * w + 1, j = 2 * w;
+            f32x4 t = {0.f, 0.f, 0.f, 0.f}, o = t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                t = __builtin_amdgcn_mfma_f32_16x16x4f32(m[(16 * i + r) * MP + 16 * j + 4 * e + g],
+                                                         m[(16 * j + 4 * e + g) * MP + 16 * j + r], t, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o = __builtin_amdgcn_mfma_f32_16x16x4f32(m[(16 * i + r) * MP + 16 * i + 4 * g + e], t[e], o, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                m[(16 * i + 4 * g + e) * MP + 16 * j + r] = -o[e];
+        }
+        __syncthreads();
+        {
+            const int i = 2 + (w >> 1), j = w & 1;
+            f32x4 t = {0.f, 0.f, 0.f, 0.f}, o = t;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (k >= j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        t = __builtin_amdgcn_mfma_f32_16x16x4f32(m[(16 * i + r) * MP + 16 * k + 4 * e + g],
+                                                                 m[(16 * k + 4 * e + g) * MP + 16 * j + r], t, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                z[w][(4 * g + e) * 17 + r] = t[e];
+            __syncthreads();
+#pragma unroll
+            for (int k = 2; k < 4; ++k)
+                if (k <= i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o = __builtin_amdgcn_mfma_f32_16x16x4f32(m[(16 * i + r) * MP + 16 * k + 4 * e + g],
+                                                                 z[2 * (k - 2) + j][(4 * e + g) * 17 + r], o, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                m[(16 * i + 4 * g + e) * MP + 16 * j + r] = -o[e];
+        }
+        __syncthreads();
+
+        uint8_t *val = a.vals + ((int64_t)blockIdx.x * p.Hv + h) * W::VAL;
+        const int row = token_of(w, r);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (2 * s <= w) {
+                bf16x8 t3[3], p2[2];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int col = 32 * s + 8 * g + e;
+                    float t = m[row * MP + col] * bs[col];
+                    t3[0][e] = part_of(t);
+                    t3[1][e] = part_of(t);
+                    t3[2][e] = part_of(t);
+                    float q = pm[row * MP + col];
+                    p2[0][e] = part_of(q);
+                    p2[1][e] = part_of(q);
+                }
+                const int f = low_frag(w, s);
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    reinterpret_cast<bf16x8 *>(val + (3 * f + i) * FRAG)[lane] = t3[i];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    reinterpret_cast<bf16x8 *>(val + W::P + (2 * f + i) * FRAG)[lane] = p2[i];
+            }
+        if (w == 0) {
+            const float e = expf((float)G);
+            const double last = gs[C - 1];
+            reinterpret_cast<float *>(val + W::UPK)[lane] = e * rk[lane];
+            reinterpret_cast<float *>(val + W::UPQ)[lane] = e * rq[lane];
+            reinterpret_cast<float *>(val + W::TAIL)[lane] = expf((float)(last - G)) * rk[lane];
+            if (lane == 0) {
+                reinterpret_cast<float *>(val + W::HEAD)[0] = expf((float)last);
+                reinterpret_cast<int *>(val + W::HEAD)[1] = bads ? __builtin_ctzll(bads) : NEVER;
+            }
+        }
+    }
+}
+
+// What wave w needs of one chunk, in registers.
+template <int DT, int CB>
+struct Operands {
+    bf16x8 k[4], q[4], kt[DT][2], t[2][3], p[2][2];
+    f32x4 upk, tail;
+    float upq, last;
+    int bad;
+    uint16_t v[CB][4];
+};
+
+template <int DT, int CB>
+__global__ __launch_bounds__(NT) void delta_chunks_kernel(ChunkArgs a)
+{
+    using W = Space<DT>;
+    const DeltaProblem &p = a.p;
+    __shared__ f32x4 xp[4][4][CB][64], op[4][4][CB][64];
+    __shared__ bf16x4 ysh[3][4][CB][64], ush[5][4][CB][64];
+    __shared__ int badcol[CB * 16];
+
+    // Workgroup i runs on XCD i % 8: the slices of one head, consecutive
+    // jobs, meet in one L2.
+    const int job = ((int)blockIdx.x & 7) * ((int)gridDim.x >> 3) + ((int)blockIdx.x >> 3);
+    if (job >= p.seq.num_seqs * p.Hv * a.slices)
+        return;
+    const int slice = job % a.slices, nh = job / a.slices;
+    const int n = nh / p.Hv, h = nh % p.Hv, kh = h / (p.Hv / p.Hk);
+    const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t begin = seq_begin(p.seq, n);
+    const int64_t end = seq_begin(p.seq, n + 1);
+    const int len = end > begin ? (int)(end - begin) : 0;
+    const int chunks = (len + C - 1) / C;
+    const int64_t number = begin / C + n;
+    const int slot = p.state_in || p.state_out ? seq_slot(p.seq, n) : -1;
+    const int64_t sat = ((int64_t)slot * p.Hv + h) * p.Dk * p.Dv;
+    const int col0 = slice * 16 * CB;
+
+    // Wave w's rows of S, as results leave the matrix cores.
+    f32x4 S[DT][CB];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int dk = DT == 2 ? 32 * w + 8 * g + 4 * d + e : 16 * w + 4 * g + e, col = col0 + 16 * cb + r;
+                S[d][cb][e] = p.state_in && slot >= 0 && dk < p.Dk && col < p.Dv
+                                  ? p.state_in[sat + (int64_t)dk * p.Dv + col] : 0.f;
+            }
+    if (threadIdx.x < CB * 16)
+        badcol[threadIdx.x] = NEVER;
+    int badall = NEVER;
+    __syncthreads();
+
+    const int tok4 = 32 * (w >> 1) + 8 * g + 4 * (w & 1);      // first of the lane's four tokens of tile w
+    const int tokr = token_of(w, r);
+    auto load = [&](int c, Operands<DT, CB> &x) __attribute__((always_inline)) {
+        const uint8_t *key = a.keys + ((number + c) * p.Hk + kh) * W::KEY;
+        const uint8_t *val = a.vals + ((number + c) * p.Hv + h) * W::VAL;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x.k[i] = reinterpret_cast<const bf16x8 *>(key + (4 * i + w) * FRAG)[lane];
+            x.q[i] = reinterpret_cast<const bf16x8 *>(key + W::Q + (4 * i + w) * FRAG)[lane];
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (2 * s <= w) {
+                const int f = low_frag(w, s);
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    x.t[s][i] = reinterpret_cast<const bf16x8 *>(val + (3 * f + i) * FRAG)[lane];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    x.p[s][i] = reinterpret_cast<const bf16x8 *>(val + W::P + (2 * f + i) * FRAG)[lane];
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                x.kt[d][s] = reinterpret_cast<const bf16x8 *>(key + W::KT + ((w * DT + d) * 2 + s) * FRAG)[lane];
+        }
+        x.upk = *reinterpret_cast<const f32x4 *>(val + W::UPK + 4 * tok4);
+        x.tail = *reinterpret_cast<const f32x4 *>(val + W::TAIL + 4 * tok4);
+        x.upq = reinterpret_cast<const float *>(val + W::UPQ)[tokr];
+        x.last = reinterpret_cast<const float *>(val + W::HEAD)[0];
+        x.bad = reinterpret_cast<const int *>(val + W::HEAD)[1];
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = c * C + tok4 + e, col = col0 + 16 * cb + r;
+                x.v[cb][e] = t < len && col < p.Dv
+                                 ? static_cast<const uint16_t *>(p.v)[(begin + t) * p.vst + h * p.vsh + col] : (uint16_t)0;
+            }
+    };
+
+    auto step = [&](int c, const Operands<DT, CB> &x) __attribute__((always_inline)) {
+        // K S and S^T Q^T, wave w's rows of S only.
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            bf16x8 sb[3];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float v = DT == 2 || e < 4 ? S[DT == 2 ? e >> 2 : 0][cb][e & 3] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    sb[i][e] = part_of(v);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 2; j >= 0; --j)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.k[i], sb[j], acc, 0, 0, 0);
+                xp[w][i][cb][lane] = acc;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 1; j >= 0; --j)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sb[j], x.q[i], acc, 0, 0, 0);
+                op[w][i][cb][lane] = acc;
+            }
+        }
+        __syncthreads();
+        // Token tile w of Y = V - diag(r exp G) K S, and of O's first term.
+        f32x4 o[CB];
+        if (badall == NEVER && x.bad != NEVER)
+            badall = c * C + x.bad;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            f32x4 s = xp[0][w][cb][lane];
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                s += xp[i][w][cb][lane];
+            bool bad = false;
+            bf16x4 y3[3];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float y = bf16_to_f32(x.v[cb][e]) - x.upk[e] * s[e];
+                if (!(fabsf(y) < INFINITY)) {
+                    bad = true;
+                    y = 0.f;
+                    atomicMin(&badcol[16 * cb + r], c * C + tok4 + e);
+                }
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    y3[i][e] = part_of(y);
+            }
+            (void)bad;
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                ysh[i][w][cb][lane] = y3[i];
+            o[cb] = op[0][w][cb][lane];
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                o[cb] += op[i][w][cb][lane];
+            o[cb] *= x.upq;
+        }
+        __syncthreads();
+        // Token tile w of U = T Y.
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            f32x4 u = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (2 * s <= w) {
+                    bf16x8 y[3];
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        y[i] = __builtin_shufflevector(ysh[i][2 * s][cb][lane], ysh[i][2 * s + 1][cb][lane], 0, 1, 2, 3, 4,
+                                                       5, 6, 7);
+#pragma unroll
+                    for (int k = 2; k >= 0; --k)
+#pragma unroll
+                        for (int i = 0; i <= k; ++i)
+                            u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.t[s][i], y[k - i], u, 0, 0, 0);
+                }
+            bf16x4 u5[5];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float b = u[e] * x.tail[e], d = u[e];
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    u5[i][e] = part_of(b);
+                u5[3][e] = part_of(d);
+                u5[4][e] = part_of(d);
+            }
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                ush[i][w][cb][lane] = u5[i];
+        }
+        __syncthreads();
+        // S' and token tile w of O.
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+            bf16x8 u[5][2];
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    u[i][s] = __builtin_shufflevector(ush[i][2 * s][cb][lane], ush[i][2 * s + 1][cb][lane], 0, 1, 2, 3, 4,
+                                                      5, 6, 7);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                S[d][cb] *= x.last;
+#pragma unroll
+                for (int i = 2; i >= 0; --i)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        S[d][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.kt[d][s], u[i][s], S[d][cb], 0, 0, 0);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (2 * s <= w) {
+                    o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[4][s], x.p[s][0], o[cb], 0, 0, 0);
+                    o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[3][s], x.p[s][1], o[cb], 0, 0, 0);
+                    o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[3][s], x.p[s][0], o[cb], 0, 0, 0);
+                }
+            const int t = c * C + tokr, col = col0 + 16 * cb + 4 * g;
+            if (t < len) {
+                uint16_t ov[4] __attribute__((aligned(8)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool bad = t >= badall || t >= badcol[16 * cb + 4 * g + e];
+                    ov[e] = bad ? (uint16_t)0x7fc0 : __builtin_bit_cast(uint16_t, (__bf16)o[cb][e]);
+                }
+                uint16_t *at = static_cast<uint16_t *>(p.o) + (begin + t) * p.ost + h * p.osh + col;
+                if (a.vec_o && col + 4 <= p.Dv) {
+                    *reinterpret_cast<u32x2 *>(at) = *reinterpret_cast<const u32x2 *>(ov);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < p.Dv)
+                            at[e] = ov[e];
+                }
+            }
+        }
+    };
+
+    if (chunks > 0) {
+        Operands<DT, CB> x0, x1;
+        load(0, x0);
+        for (int c = 0; c < chunks; c += 2) {
+            load(min(c + 1, chunks - 1), x1);
+            step(c, x0);
+            if (c + 1 < chunks) {
+                load(min(c + 2, chunks - 1), x0);
+                step(c + 1, x1);
+            }
+        }
+    }
+    __syncthreads();
+    if (p.state_out && slot >= 0)
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int dk = DT == 2 ? 32 * w + 8 * g + 4 * d + e : 16 * w + 4 * g + e, col = col0 + 16 * cb + r;
+                    const bool bad = badall != NEVER || badcol[16 * cb + r] != NEVER;
+                    if (dk < p.Dk && col < p.Dv)
+                        p.state_out[sat + (int64_t)dk * p.Dv + col] = bad ? NAN : S[d][cb][e];
+                }
+}
+
+template <int DT>
+hipError_t launch(const DeltaProblem &p, hipStream_t s)
+{
+    using W = Space<DT>;
+    ChunkArgs a = {};
+    a.p = p;
+    const int64_t numbers = seq_tiles(p.seq, C);
+    a.keys = static_cast<uint8_t *>(p.workspace);
+    a.vals = a.keys + numbers * p.Hk * W::KEY;
+    a.vec = (((uintptr_t)p.q | (uintptr_t)p.k) % 16 == 0) && ((p.qst | p.qsh | p.kst | p.ksh) % 8 == 0);
+    a.vec_o = ((uintptr_t)p.o % 8 == 0) && ((p.ost | p.osh) % 4 == 0);
+    hipLaunchKernelGGL(delta_prepare_kernel<DT>, dim3((unsigned)numbers, (unsigned)p.Hk), dim3(NT), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    a.slices = (p.Dv + 15) / 16;
+    const int64_t jobs = (int64_t)p.seq.num_seqs * p.Hv * a.slices;
+    hipLaunchKernelGGL((delta_chunks_kernel<DT, 1>), dim3((unsigned)((jobs + 7) / 8 * 8)), dim3(NT), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+bool delta_chunked_supports(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, int Dv, conv_dtype dtype)
+{
+    // Chunk numbers and jobs fit the grids.
+    return dtype == CONV_BF16 && Dk <= 128 && tokens / C + num_seqs <= (1 << 30) &&
+           (int64_t)num_seqs * Hv * ((Dv + 15) / 16) <= (1 << 30);
+}
+
+int64_t delta_chunked_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk)
+{
+    const int64_t numbers = tokens / C + num_seqs;
+    return numbers * (Dk <= 64 ? (int64_t)Hk * Space<1>::KEY + (int64_t)Hv * Space<1>::VAL
+                               : (int64_t)Hk * Space<2>::KEY + (int64_t)Hv * Space<2>::VAL);
+}
+
+hipError_t launch_delta_chunked(const DeltaProblem &p, hipStream_t s)
+{
+    return p.Dk <= 64 ? launch<1>(p, s) : launch<2>(p, s);
+}
+
+}  // namespace convfwd

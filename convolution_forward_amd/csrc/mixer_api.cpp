@@ -127,9 +127,11 @@ conv_status check_delta_sizes(int64_t tokens, int num_seqs, int Hk, int Hv, int 
         return CONV_ERR_DTYPE;
     if (tokens > MAX_ROWS || num_seqs > MAX_ROWS || Dk > 256 || Dv > 65536 || Hv > 65535)
         return CONV_ERR_UNSUPPORTED;
+    const bool can = delta_chunked_supports(tokens, num_seqs, Hk, Hv, Dk, Dv, dtype);
     switch (variant) {
-    case CONV_VARIANT_AUTO:
+    case CONV_VARIANT_AUTO: *tiled = can && tokens > 16 * (int64_t)num_seqs; return CONV_OK;
     case CONV_VARIANT_DIRECT: *tiled = false; return CONV_OK;
+    case CONV_VARIANT_TILED: *tiled = true; return can ? CONV_OK : CONV_ERR_UNSUPPORTED;
     default: return CONV_ERR_UNSUPPORTED;
     }
 }
@@ -263,7 +265,7 @@ int64_t conv_delta_rule_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, 
     bool tiled;
     if (check_delta_sizes(tokens, num_seqs, Hk, Hv, Dk, Dv, dtype, variant, &tiled) != CONV_OK)
         return -1;
-    return 0;
+    return tiled ? delta_chunked_workspace(tokens, num_seqs, Hk, Hv, Dk) : 0;
 }
 
 conv_status conv_delta_rule_fwd(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
@@ -332,7 +334,7 @@ conv_status conv_delta_rule_fwd(const void *q, const int64_t *q_strides, const v
     p.scale = scale;
     p.normalize = normalize;
     p.dtype = dtype;
-    return launched(launch_delta_direct(p, (hipStream_t)stream));
+    return launched(tiled ? launch_delta_chunked(p, (hipStream_t)stream) : launch_delta_direct(p, (hipStream_t)stream));
 }
 
 }  // extern "C"

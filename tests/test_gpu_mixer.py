@@ -269,7 +269,7 @@ def run_delta(q, k, v, g, beta, lens, states, normalize, scale=None, want_state=
     return o
 
 
-VARIANTS = [cf.VARIANT_AUTO, cf.VARIANT_DIRECT]
+VARIANTS = [cf.VARIANT_AUTO, cf.VARIANT_DIRECT]     # AUTO: by chunks wherever that form takes the sizes and pays
 DELTA_LENS = [[1], [2], [63], [64], [65], [0, 1, 130, 0, 64, 3], [1] * 9, [200]]
 
 
@@ -422,6 +422,58 @@ def test_delta_no_tokens():
     o = cf.gated_delta_rule(z(0, 2, 32), z(0, 2, 32), z(0, 2, 16), zf, zf, seq_offsets=ref.seqs([0, 0, 0], DEV),
                             initial_state=st, final_state=fin)
     assert o.shape == (0, 2, 16) and torch.equal(st, fin)
+
+
+@pytest.mark.parametrize("lens", [[1], [3, 0, 1, 2], [17] * 3, [64], [129]], ids=str)
+@pytest.mark.parametrize("Hk,Hv,Dk,Dv", [(1, 1, 8, 16), (1, 2, 64, 64), (2, 4, 128, 128), (1, 3, 100, 34)])
+def test_delta_by_chunks(lens, Hk, Hv, Dk, Dv):
+    """The chunked form forced, single tokens and empty sequences included."""
+    q, k, v, g, beta = delta_inputs(sum(lens), Hk, Hv, Dk, Dv, BF, 350)
+    run_delta(q, k, v, g, beta, lens, rnd((len(lens), Hv, Dk, Dv), 355, std=0.3), True, variant=cf.VARIANT_TILED)
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("which,value", [("k", float("nan")), ("k", float("inf")), ("g", float("nan")),
+                                         ("g", float("inf")), ("beta", float("nan")), ("q", float("nan")),
+                                         ("v", float("-inf")), ("state", float("nan"))])
+def test_delta_not_finite(which, value, variant):
+    """What is not finite reaches its own token and later ones of its head (q: its token only; v and the state: its
+    column), never earlier tokens, other heads or other sequences."""
+    lens, t = [90, 100, 40], 70
+    q, k, v, g, beta = delta_inputs(sum(lens), 2, 2, 64, 32, BF, 360)
+    states = rnd((3, 2, 64, 32), 365, std=0.3)
+    at = 90 + t
+    if which == "state":
+        states[1, 1, 7, 5] = value
+    elif which in "gbeta":
+        (g if which == "g" else beta)[at, 1] = value
+    else:
+        dict(q=q, k=k, v=v)[which][at, 1, 5] = value
+    fin = torch.zeros(3, 2, 64, 32, device=DEV)
+    o = cf.gated_delta_rule(q.to(DEV), k.to(DEV), v.to(DEV), g.to(DEV), beta.to(DEV), normalize=True,
+                            seq_offsets=ref.seqs(lens, DEV), initial_state=states.to(DEV), final_state=fin,
+                            variant=variant).cpu()
+    bad = ~torch.isfinite(o)
+    want = torch.zeros_like(bad)
+    if which == "q":
+        want[at, 1] = True
+    elif which == "state":
+        want[90:190, 1, 5] = True
+    elif which == "v":
+        want[at:190, 1, 5] = True
+    else:
+        want[at:190, 1] = True
+    if value == float("inf") and which == "k":      # normalised: the infinite entry makes the others 0, itself NaN
+        assert bad[want].any() and not bad[~want].any()
+    else:
+        assert torch.equal(bad, want)
+    fin = fin.cpu()
+    assert torch.isfinite(fin[[0, 2]]).all() and torch.isfinite(fin[1, 0]).all()
+    if which == "q":
+        assert torch.isfinite(fin).all()
+    elif which in ("v", "state"):
+        cols = torch.arange(32) != 5
+        assert torch.isfinite(fin[1, 1][:, cols]).all() and not torch.isfinite(fin[1, 1][:, 5]).any()
 
 
 # ---- all of them -----------------------------------------------------------------------------------------------------
