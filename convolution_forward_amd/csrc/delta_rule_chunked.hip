@@ -16,7 +16,7 @@
 // what does not depend on S: T = (1 + A)^-1 diag(beta), P, the row factors,
 // and K, Q and K^T, all in the order in which the second one's matrix
 // instructions take them. The second carries S along each sequence. Columns
-// of S are independent, so a workgroup takes 16 CB of them; its four waves
+// of S are independent, so a workgroup takes 16 CB of them; four of its waves
 // share the rows.
 //
 // Precision: bf16 operands (K, Q) are exact, every other operand of a product
@@ -77,6 +77,10 @@ struct ChunkArgs {
     int vec_o;                  // rows of o take 8-byte stores
     int slices;                 // column slices of a head
 };
+
+// A barrier for LDS traffic only: __syncthreads would also wait for the loads
+// of the next chunk that are in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 __device__ __forceinline__ __bf16 part_of(float &x)
 {
@@ -355,44 +359,143 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
     }
 }
 
-// What wave w needs of one chunk, in registers.
-template <int DT, int CB>
-struct Operands {
-    bf16x8 k[4], q[4], kt[DT][2], t[2][3], p[2][2];
-    f32x4 upk, tail;
-    float upq, last;
-    int bad;
-    uint16_t v[CB][4];
-};
+// x as bf16 parts, the nearest bf16 of what the parts before left.
+template <int N>
+__device__ __forceinline__ void split(const f32x4 &x, bf16x4 (&part)[N])
+{
+    f32x4 left = x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        part[i] = __builtin_convertvector(left, bf16x4);
+        if (i + 1 < N)
+            left -= __builtin_convertvector(part[i], f32x4);
+    }
+}
 
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// Waves 0 to 3 carry S, waves 4 to 7 make the outputs. Three exchanges
+// through LDS a chunk, each ended by a barrier that all eight waves meet:
+//   chain wave w: its rows' shares of K S and (Q S)^T    -> xp, op
+//   chain wave w: token tile w of Y, in three parts      -> ysh
+//   chain wave w: token tile w of U, for S' and for O    -> ush
+// then chain wave w updates its rows of S while output wave w adds up token
+// tile w of O. The time of a chunk is that chain's, not its arithmetic, so
+// every operand is loaded right after its last use, a chunk ahead.
 template <int DT, int CB>
-__global__ __launch_bounds__(NT) void delta_chunks_kernel(ChunkArgs a)
+__global__ __launch_bounds__(512) void delta_chunks_kernel(ChunkArgs a)
 {
     using W = Space<DT>;
     const DeltaProblem &p = a.p;
     __shared__ f32x4 xp[4][4][CB][64], op[4][4][CB][64];
     __shared__ bf16x4 ysh[3][4][CB][64], ush[5][4][CB][64];
-    __shared__ int badcol[CB * 16];
+    __shared__ __align__(16) int badcol[CB * 16];
 
-    // Workgroup i runs on XCD i % 8: the slices of one head, consecutive
-    // jobs, meet in one L2.
-    const int job = ((int)blockIdx.x & 7) * ((int)gridDim.x >> 3) + ((int)blockIdx.x >> 3);
-    if (job >= p.seq.num_seqs * p.Hv * a.slices)
+    // Workgroup i runs on XCD i % 8. The slices of one head go to one XCD,
+    // where they meet in its L2; the heads of a sequence, as long as each
+    // other, go round the XCDs.
+    const int at = (int)blockIdx.x >> 3;
+    const int slice = at % a.slices, nh = at / a.slices * 8 + ((int)blockIdx.x & 7);
+    if (nh >= p.seq.num_seqs * p.Hv)
         return;
-    const int slice = job % a.slices, nh = job / a.slices;
     const int n = nh / p.Hv, h = nh % p.Hv, kh = h / (p.Hv / p.Hk);
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-    const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int w8 = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int w = w8 & 3;
     const int64_t begin = seq_begin(p.seq, n);
     const int64_t end = seq_begin(p.seq, n + 1);
     const int len = end > begin ? (int)(end - begin) : 0;
     const int chunks = (len + C - 1) / C;
     const int64_t number = begin / C + n;
     const int slot = p.state_in || p.state_out ? seq_slot(p.seq, n) : -1;
-    const int64_t sat = ((int64_t)slot * p.Hv + h) * p.Dk * p.Dv;
     const int col0 = slice * 16 * CB;
+    const int tok4 = 32 * (w >> 1) + 8 * g + 4 * (w & 1);      // first of the lane's four tokens of tile w
+    const int tokr = token_of(w, r);
+    const uint8_t *key0 = a.keys + (number * p.Hk + kh) * W::KEY;
+    const uint8_t *val0 = a.vals + (number * p.Hv + h) * W::VAL;
+    const int64_t key_step = (int64_t)p.Hk * W::KEY, val_step = (int64_t)p.Hv * W::VAL;
+    auto frag = [&](const uint8_t *base, int i) __attribute__((always_inline)) {
+        return reinterpret_cast<const bf16x8 *>(base + i * FRAG)[lane];
+    };
 
-    // Wave w's rows of S, as results leave the matrix cores.
+    if (threadIdx.x < CB * 16)
+        badcol[threadIdx.x] = NEVER;
+    __syncthreads();
+
+    if (w8 >= 4) {
+        // ---- Output wave w: token tile w of O, as rows of columns 4g .. 4g + 3, token r.
+        bf16x8 pf[2][2];
+        float upq = 0.f;
+        int bad_here = NEVER, badall = NEVER;
+        auto load = [&](int c) __attribute__((always_inline)) {
+            const uint8_t *val = val0 + c * val_step;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    pf[s][i] = frag(val + W::P, 2 * low_frag(w, 2 * s <= w ? s : 0) + i);
+            upq = reinterpret_cast<const float *>(val + W::UPQ)[tokr];
+            bad_here = reinterpret_cast<const int *>(val + W::HEAD)[1];
+        };
+        if (chunks > 0)
+            load(0);
+        uint16_t *oh = static_cast<uint16_t *>(p.o) + (begin + tokr) * p.ost + h * p.osh + col0 + 4 * g;
+        for (int c = 0; c < chunks; ++c) {
+            f32x4 o[CB];
+            lds_barrier();
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                o[cb] = op[0][w][cb][lane];
+#pragma unroll
+                for (int i = 1; i < 4; ++i)
+                    o[cb] += op[i][w][cb][lane];
+                o[cb] *= upq;
+            }
+            lds_barrier();
+            lds_barrier();
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (2 * s <= w) {
+                        const bf16x8 u0 = join(ush[3][2 * s][cb][lane], ush[3][2 * s + 1][cb][lane]);
+                        const bf16x8 u1 = join(ush[4][2 * s][cb][lane], ush[4][2 * s + 1][cb][lane]);
+                        o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u1, pf[s][0], o[cb], 0, 0, 0);
+                        o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][1], o[cb], 0, 0, 0);
+                        o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][0], o[cb], 0, 0, 0);
+                    }
+            const int t = c * C + tokr;
+            if (badall == NEVER && bad_here != NEVER)
+                badall = c * C + bad_here;
+            load(min(c + 1, chunks - 1));
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                const int *bc = badcol + 16 * cb + 4 * g;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[cb][e] = t >= min(badall, bc[e]) ? NAN : o[cb][e];
+                const bf16x4 ov = __builtin_convertvector(o[cb], bf16x4);
+                const int left = p.Dv - (col0 + 16 * cb + 4 * g);
+                if (t < len) {
+                    if (a.vec_o && left >= 4) {
+                        *reinterpret_cast<bf16x4 *>(oh + 16 * cb) = ov;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (e < left)
+                                oh[16 * cb + e] = f32_to_bf16_rne(o[cb][e]);
+                    }
+                }
+            }
+            oh += C * p.ost;
+        }
+        return;
+    }
+
+    // ---- Chain wave w: its rows of S, as results leave the matrix cores
+    // (row dk_of(d) + e, column r of each 16).
+    const int64_t sat = ((int64_t)slot * p.Hv + h) * p.Dk * p.Dv;
+    auto dk_of = [&](int d) { return DT == 2 ? 32 * w + 8 * g + 4 * d : 16 * w + 4 * g; };
     f32x4 S[DT][CB];
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -400,73 +503,82 @@ __global__ __launch_bounds__(NT) void delta_chunks_kernel(ChunkArgs a)
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int dk = DT == 2 ? 32 * w + 8 * g + 4 * d + e : 16 * w + 4 * g + e, col = col0 + 16 * cb + r;
-                S[d][cb][e] = p.state_in && slot >= 0 && dk < p.Dk && col < p.Dv
-                                  ? p.state_in[sat + (int64_t)dk * p.Dv + col] : 0.f;
+                // All loads at once: what is past the state reads its last row and column.
+                const int dk = dk_of(d) + e, col = col0 + 16 * cb + r;
+                float v = 0.f;
+                if (p.state_in && slot >= 0)
+                    v = p.state_in[sat + (int64_t)min(dk, p.Dk - 1) * p.Dv + min(col, p.Dv - 1)];
+                S[d][cb][e] = dk < p.Dk && col < p.Dv ? v : 0.f;
             }
-    if (threadIdx.x < CB * 16)
-        badcol[threadIdx.x] = NEVER;
-    int badall = NEVER;
-    __syncthreads();
 
-    const int tok4 = 32 * (w >> 1) + 8 * g + 4 * (w & 1);      // first of the lane's four tokens of tile w
-    const int tokr = token_of(w, r);
-    auto load = [&](int c, Operands<DT, CB> &x) __attribute__((always_inline)) {
-        const uint8_t *key = a.keys + ((number + c) * p.Hk + kh) * W::KEY;
-        const uint8_t *val = a.vals + ((number + c) * p.Hv + h) * W::VAL;
+    bf16x8 kf[4], qf[4], ktf[DT][2], tf[2][3];
+    f32x4 upk, tail;
+    float last = 1.f;
+    int bad_any = 0;            // of the chunks whose K^T was loaded: some token is not finite
+    uint16_t v[CB][4];
+    const uint16_t *vh = static_cast<const uint16_t *>(p.v) + begin * p.vst + h * p.vsh;
+    auto load_kq = [&](int c) __attribute__((always_inline)) {
+        const uint8_t *key = key0 + c * key_step;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x.k[i] = reinterpret_cast<const bf16x8 *>(key + (4 * i + w) * FRAG)[lane];
-            x.q[i] = reinterpret_cast<const bf16x8 *>(key + W::Q + (4 * i + w) * FRAG)[lane];
-        }
+        for (int i = 0; i < 4; ++i)
+            kf[i] = frag(key, 4 * i + w);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            if (2 * s <= w) {
-                const int f = low_frag(w, s);
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    x.t[s][i] = reinterpret_cast<const bf16x8 *>(val + (3 * f + i) * FRAG)[lane];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    x.p[s][i] = reinterpret_cast<const bf16x8 *>(val + W::P + (2 * f + i) * FRAG)[lane];
-            }
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-                x.kt[d][s] = reinterpret_cast<const bf16x8 *>(key + W::KT + ((w * DT + d) * 2 + s) * FRAG)[lane];
-        }
-        x.upk = *reinterpret_cast<const f32x4 *>(val + W::UPK + 4 * tok4);
-        x.tail = *reinterpret_cast<const f32x4 *>(val + W::TAIL + 4 * tok4);
-        x.upq = reinterpret_cast<const float *>(val + W::UPQ)[tokr];
-        x.last = reinterpret_cast<const float *>(val + W::HEAD)[0];
-        x.bad = reinterpret_cast<const int *>(val + W::HEAD)[1];
+        for (int i = 0; i < 4; ++i)
+            qf[i] = frag(key + W::Q, 4 * i + w);
+    };
+    auto load_v = [&](int c) __attribute__((always_inline)) {
+        upk = *reinterpret_cast<const f32x4 *>(val0 + c * val_step + W::UPK + 4 * tok4);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int t = c * C + tok4 + e, col = col0 + 16 * cb + r;
-                x.v[cb][e] = t < len && col < p.Dv
-                                 ? static_cast<const uint16_t *>(p.v)[(begin + t) * p.vst + h * p.vsh + col] : (uint16_t)0;
+                // Tokens and columns past the end read the last one's; they are zeroed when used.
+                const int t = min(c * C + tok4 + e, len - 1), col = min(col0 + 16 * cb + r, p.Dv - 1);
+                v[cb][e] = vh[t * p.vst + col];
             }
     };
-
-    auto step = [&](int c, const Operands<DT, CB> &x) __attribute__((always_inline)) {
+    auto load_t = [&](int c) __attribute__((always_inline)) {
+        const uint8_t *val = val0 + c * val_step;
+        // No load is conditional (a branch would make the compiler wait at
+        // its end); waves 0 and 1 do not use what they load for s = 1.
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                tf[s][i] = frag(val, 3 * low_frag(w, 2 * s <= w ? s : 0) + i);
+        tail = *reinterpret_cast<const f32x4 *>(val + W::TAIL + 4 * tok4);
+    };
+    auto load_kt = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                ktf[d][s] = frag(key0 + c * key_step + W::KT, (w * DT + d) * 2 + s);
+        const u32x2 head = *reinterpret_cast<const u32x2 *>(val0 + c * val_step + W::HEAD);
+        last = __uint_as_float(head[0]);
+        bad_any |= (int)head[1] != NEVER;
+    };
+    if (chunks > 0) {
+        load_kq(0);
+        load_v(0);
+        load_t(0);
+        load_kt(0);
+    }
+    for (int c = 0; c < chunks; ++c) {
+        const int next = min(c + 1, chunks - 1);
         // K S and S^T Q^T, wave w's rows of S only.
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-            bf16x8 sb[3];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float v = DT == 2 || e < 4 ? S[DT == 2 ? e >> 2 : 0][cb][e & 3] : 0.f;
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    sb[i][e] = part_of(v);
-            }
+            bf16x4 lo[3], hi[3] = {};
+            split<3>(S[0][cb], lo);
+            if constexpr (DT == 2)
+                split<3>(S[DT - 1][cb], hi);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 2; j >= 0; --j)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.k[i], sb[j], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], join(lo[j], hi[j]), acc, 0, 0, 0);
                 xp[w][i][cb][lane] = acc;
             }
 #pragma unroll
@@ -474,46 +586,40 @@ __global__ __launch_bounds__(NT) void delta_chunks_kernel(ChunkArgs a)
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 1; j >= 0; --j)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(sb[j], x.q[i], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(join(lo[j], hi[j]), qf[i], acc, 0, 0, 0);
                 op[w][i][cb][lane] = acc;
             }
         }
-        __syncthreads();
-        // Token tile w of Y = V - diag(r exp G) K S, and of O's first term.
-        f32x4 o[CB];
-        if (badall == NEVER && x.bad != NEVER)
-            badall = c * C + x.bad;
+        load_kq(next);
+        lds_barrier();
+        // Token tile w of Y = V - diag(r exp G) K S.
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-            f32x4 s = xp[0][w][cb][lane];
+            f32x4 y = xp[0][w][cb][lane];
 #pragma unroll
             for (int i = 1; i < 4; ++i)
-                s += xp[i][w][cb][lane];
+                y += xp[i][w][cb][lane];
             bool bad = false;
-            bf16x4 y3[3];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float y = bf16_to_f32(x.v[cb][e]) - x.upk[e] * s[e];
-                if (!(fabsf(y) < INFINITY)) {
-                    bad = true;
-                    y = 0.f;
-                    atomicMin(&badcol[16 * cb + r], c * C + tok4 + e);
-                }
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    y3[i][e] = part_of(y);
+                y[e] = (c * C + tok4 + e < len ? bf16_to_f32(v[cb][e]) : 0.f) - upk[e] * y[e];
+                bad |= !(fabsf(y[e]) < INFINITY);
             }
-            (void)bad;
+            if (__any(bad))
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!(fabsf(y[e]) < INFINITY)) {
+                        atomicMin(&badcol[16 * cb + r], c * C + tok4 + e);
+                        y[e] = 0.f;
+                    }
+            bf16x4 part[3];
+            split<3>(y, part);
 #pragma unroll
             for (int i = 0; i < 3; ++i)
-                ysh[i][w][cb][lane] = y3[i];
-            o[cb] = op[0][w][cb][lane];
-#pragma unroll
-            for (int i = 1; i < 4; ++i)
-                o[cb] += op[i][w][cb][lane];
-            o[cb] *= x.upq;
+                ysh[i][w][cb][lane] = part[i];
         }
-        __syncthreads();
+        load_v(next);
+        lds_barrier();
         // Token tile w of U = T Y.
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
@@ -524,101 +630,55 @@ __global__ __launch_bounds__(NT) void delta_chunks_kernel(ChunkArgs a)
                     bf16x8 y[3];
 #pragma unroll
                     for (int i = 0; i < 3; ++i)
-                        y[i] = __builtin_shufflevector(ysh[i][2 * s][cb][lane], ysh[i][2 * s + 1][cb][lane], 0, 1, 2, 3, 4,
-                                                       5, 6, 7);
+                        y[i] = join(ysh[i][2 * s][cb][lane], ysh[i][2 * s + 1][cb][lane]);
 #pragma unroll
                     for (int k = 2; k >= 0; --k)
 #pragma unroll
                         for (int i = 0; i <= k; ++i)
-                            u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.t[s][i], y[k - i], u, 0, 0, 0);
+                            u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tf[s][i], y[k - i], u, 0, 0, 0);
                 }
-            bf16x4 u5[5];
+            bf16x4 us[3], uo[2];
+            split<3>(u * tail, us);
+            split<2>(u, uo);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float b = u[e] * x.tail[e], d = u[e];
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    u5[i][e] = part_of(b);
-                u5[3][e] = part_of(d);
-                u5[4][e] = part_of(d);
-            }
-#pragma unroll
-            for (int i = 0; i < 5; ++i)
-                ush[i][w][cb][lane] = u5[i];
+            for (int i = 0; i < 3; ++i)
+                ush[i][w][cb][lane] = us[i];
+            ush[3][w][cb][lane] = uo[0];
+            ush[4][w][cb][lane] = uo[1];
         }
-        __syncthreads();
-        // S' and token tile w of O.
+        load_t(next);
+        lds_barrier();
+        // S'.
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-            bf16x8 u[5][2];
 #pragma unroll
-            for (int i = 0; i < 5; ++i)
+            for (int d = 0; d < DT; ++d)
+                S[d][cb] *= last;
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    u[i][s] = __builtin_shufflevector(ush[i][2 * s][cb][lane], ush[i][2 * s + 1][cb][lane], 0, 1, 2, 3, 4,
-                                                      5, 6, 7);
+            for (int i = 2; i >= 0; --i)
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                S[d][cb] *= x.last;
+                for (int s = 0; s < 2; ++s) {
+                    const bf16x8 u = join(ush[i][2 * s][cb][lane], ush[i][2 * s + 1][cb][lane]);
 #pragma unroll
-                for (int i = 2; i >= 0; --i)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        S[d][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.kt[d][s], u[i][s], S[d][cb], 0, 0, 0);
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (2 * s <= w) {
-                    o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[4][s], x.p[s][0], o[cb], 0, 0, 0);
-                    o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[3][s], x.p[s][1], o[cb], 0, 0, 0);
-                    o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[3][s], x.p[s][0], o[cb], 0, 0, 0);
+                    for (int d = 0; d < DT; ++d)
+                        S[d][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ktf[d][s], u, S[d][cb], 0, 0, 0);
                 }
-            const int t = c * C + tokr, col = col0 + 16 * cb + 4 * g;
-            if (t < len) {
-                uint16_t ov[4] __attribute__((aligned(8)));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool bad = t >= badall || t >= badcol[16 * cb + 4 * g + e];
-                    ov[e] = bad ? (uint16_t)0x7fc0 : __builtin_bit_cast(uint16_t, (__bf16)o[cb][e]);
-                }
-                uint16_t *at = static_cast<uint16_t *>(p.o) + (begin + t) * p.ost + h * p.osh + col;
-                if (a.vec_o && col + 4 <= p.Dv) {
-                    *reinterpret_cast<u32x2 *>(at) = *reinterpret_cast<const u32x2 *>(ov);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (col + e < p.Dv)
-                            at[e] = ov[e];
-                }
-            }
         }
-    };
-
-    if (chunks > 0) {
-        Operands<DT, CB> x0, x1;
-        load(0, x0);
-        for (int c = 0; c < chunks; c += 2) {
-            load(min(c + 1, chunks - 1), x1);
-            step(c, x0);
-            if (c + 1 < chunks) {
-                load(min(c + 2, chunks - 1), x0);
-                step(c + 1, x1);
-            }
-        }
+        load_kt(next);
     }
-    __syncthreads();
-    if (p.state_out && slot >= 0)
+    if (!p.state_out || slot < 0)
+        return;
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
+        for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int dk = DT == 2 ? 32 * w + 8 * g + 4 * d + e : 16 * w + 4 * g + e, col = col0 + 16 * cb + r;
-                    const bool bad = badall != NEVER || badcol[16 * cb + r] != NEVER;
-                    if (dk < p.Dk && col < p.Dv)
-                        p.state_out[sat + (int64_t)dk * p.Dv + col] = bad ? NAN : S[d][cb][e];
-                }
+            for (int e = 0; e < 4; ++e) {
+                const int dk = dk_of(d) + e, col = col0 + 16 * cb + r;
+                const bool bad = bad_any || badcol[16 * cb + r] != NEVER;
+                if (dk < p.Dk && col < p.Dv)
+                    p.state_out[sat + (int64_t)dk * p.Dv + col] = bad ? NAN : S[d][cb][e];
+            }
 }
 
 template <int DT>
@@ -637,8 +697,8 @@ hipError_t launch(const DeltaProblem &p, hipStream_t s)
     if (e != hipSuccess)
         return e;
     a.slices = (p.Dv + 15) / 16;
-    const int64_t jobs = (int64_t)p.seq.num_seqs * p.Hv * a.slices;
-    hipLaunchKernelGGL((delta_chunks_kernel<DT, 1>), dim3((unsigned)((jobs + 7) / 8 * 8)), dim3(NT), 0, s, a);
+    const int64_t heads = ((int64_t)p.seq.num_seqs * p.Hv + 7) / 8 * 8;
+    hipLaunchKernelGGL((delta_chunks_kernel<DT, 1>), dim3((unsigned)(heads * a.slices)), dim3(512), 0, s, a);
     return hipGetLastError();
 }
 
@@ -648,7 +708,7 @@ bool delta_chunked_supports(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk
 {
     // Chunk numbers and jobs fit the grids.
     return dtype == CONV_BF16 && Dk <= 128 && tokens / C + num_seqs <= (1 << 30) &&
-           (int64_t)num_seqs * Hv * ((Dv + 15) / 16) <= (1 << 30);
+           ((int64_t)num_seqs * Hv + 8) * ((Dv + 15) / 16) <= (1 << 30);
 }
 
 int64_t delta_chunked_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk)
