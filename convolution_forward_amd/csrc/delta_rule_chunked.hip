@@ -40,6 +40,7 @@ namespace {
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
@@ -54,8 +55,8 @@ constexpr int NEVER = 0x7fffffff;
 __device__ __forceinline__ int token_of(int i, int r) { return 32 * (i >> 1) + 8 * (r >> 2) + 4 * (i & 1) + (r & 3); }
 
 // ---- Workspace ---------------------------------------------------------------
-// For each chunk number and key head: K and Q, 4 tiles x 4 waves fragments
-// each, K^T, 4 waves x DT x 2. For each chunk number and value head: T, 3
+// For each chunk number and key head: K (wave, tile) and Q (tile, wave), 4 x 4
+// fragments each, K^T, 4 waves x DT x 2. For each chunk number and value head: T, 3
 // parts of the 6 fragments that are not all zero, P, 2 parts of them, then 4
 // x 64 row factors and a header. A fragment is 64 lanes x 16 bytes.
 constexpr int FRAG = 1024;
@@ -95,8 +96,12 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
     using W = Space<DT>;
     constexpr int D = 64 * DT, PITCH = D + 8, MP = 68;
     const DeltaProblem &p = a.p;
-    __shared__ __align__(16) uint16_t ks[C * PITCH], qs[C * PITCH];
-    __shared__ __align__(16) float m[C * MP], pm[C * MP], z[4][16 * 17];
+    // K and Q give their room to A (then T) and P once their products are in registers.
+    constexpr int ROWS = C * PITCH * 2 > C * MP * 4 ? C * PITCH * 2 : C * MP * 4;
+    __shared__ __align__(16) uint8_t room[2 * ROWS];
+    uint16_t *ks = reinterpret_cast<uint16_t *>(room), *qs = reinterpret_cast<uint16_t *>(room + ROWS);
+    float *m = reinterpret_cast<float *>(room), *pm = reinterpret_cast<float *>(room + ROWS);
+    __shared__ float z[4][16 * 17];
     __shared__ double gs[C];
     __shared__ float rk[C], rq[C], bs[C];
     __shared__ int badrow[C];
@@ -115,10 +120,19 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
     // Rows of K and Q, zeros past the sequence's end and past Dk.
     if (tid < C)
         badrow[tid] = 0;
-    for (int i = tid; i < C * MP; i += NT)
-        m[i] = pm[i] = 0.f;
-    __syncthreads();
-    for (int i = tid; i < C * D / 8; i += NT) {
+    const int group = p.Hv / p.Hk;
+    float gate = 0.f, beta = 0.f;       // of the head to come, token `lane`
+    auto load_gate = [&](int h) __attribute__((always_inline)) {
+        if (lane < rows) {
+            gate = p.g[(first + lane) * p.Hv + h];
+            beta = p.beta[(first + lane) * p.Hv + h];
+        }
+    };
+    load_gate(kh * group);
+    lds_barrier();
+#pragma unroll
+    for (int i0 = 0; i0 < C * D / 8; i0 += NT) {
+        const int i = i0 + tid;
         const int row = i / (D / 8), c = i % (D / 8) * 8;
         uint16_t kv[8] __attribute__((aligned(16))) = {}, qv[8] __attribute__((aligned(16))) = {};
         if (row < rows) {
@@ -148,14 +162,21 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
         *reinterpret_cast<u32x4 *>(ks + row * PITCH + c) = *reinterpret_cast<const u32x4 *>(kv);
         *reinterpret_cast<u32x4 *>(qs + row * PITCH + c) = *reinterpret_cast<const u32x4 *>(qv);
     }
-    __syncthreads();
+    lds_barrier();
     {   // four threads a row
         const int row = tid >> 2;
         float sk = 0.f, sq = 0.f;
-        for (int c = tid & 3; c < D; c += 4) {
-            const float x = bf16_to_f32(ks[row * PITCH + c]), y = bf16_to_f32(qs[row * PITCH + c]);
-            sk = fmaf(x, x, sk);
-            sq = fmaf(y, y, sq);
+#pragma unroll
+        for (int c = 8 * (tid & 3); c < D; c += 32) {
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(ks + row * PITCH + c);
+            const u32x4 y = *reinterpret_cast<const u32x4 *>(qs + row * PITCH + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = __uint_as_float(x[e] << 16), x1 = __uint_as_float(x[e] & 0xffff0000u);
+                const float y0 = __uint_as_float(y[e] << 16), y1 = __uint_as_float(y[e] & 0xffff0000u);
+                sk = fmaf(x1, x1, fmaf(x0, x0, sk));
+                sq = fmaf(y1, y1, fmaf(y0, y0, sq));
+            }
         }
         sk += __shfl_xor(sk, 1);
         sk += __shfl_xor(sk, 2);
@@ -181,7 +202,7 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
             kf[0] = k2[0], kf[1] = k2[1];
             qf[0] = q2[0], qf[1] = q2[1];
         }
-        reinterpret_cast<u32x4 *>(key + (4 * i + w) * FRAG)[lane] = kf;
+        reinterpret_cast<u32x4 *>(key + (4 * w + i) * FRAG)[lane] = kf;
         reinterpret_cast<u32x4 *>(key + W::Q + (4 * i + w) * FRAG)[lane] = qf;
     }
 #pragma unroll
@@ -217,14 +238,11 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
             }
     }
 
-    const int group = p.Hv / p.Hk;
+    lds_barrier();
+    for (int i = tid; i < C * MP / 4; i += NT)
+        reinterpret_cast<f32x4 *>(m)[i] = reinterpret_cast<f32x4 *>(pm)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int h = kh * group; h < (kh + 1) * group; ++h) {
         // Sums of the gates, in 64 bits; a total gate counts as exp(-10000) = 0.
-        float gate = 0.f, beta = 0.f;
-        if (lane < rows) {
-            gate = p.g[(first + lane) * p.Hv + h];
-            beta = p.beta[(first + lane) * p.Hv + h];
-        }
         const bool bad = !(gate < INFINITY) || !(fabsf(beta) < INFINITY) || badrow[lane];
         if (bad) {
             gate = gate < INFINITY ? gate : 0.f;
@@ -232,18 +250,21 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
         }
         const uint64_t bads = __ballot(bad);
         double G = (double)fmaxf(gate, -1e4f);
+        const float b = beta;
+        if (h + 1 < (kh + 1) * group)
+            load_gate(h + 1);
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const double o = __shfl_up(G, d);
             if (lane >= d)
                 G += o;
         }
-        __syncthreads();
+        lds_barrier();
         if (w == 0) {
             gs[lane] = G;
-            bs[lane] = beta;
+            bs[lane] = b;
         }
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (j <= w) {
@@ -258,26 +279,26 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
                     pm[row * MP + col] = row >= col ? rq[row] * d * qk[j][e] : 0.f;
                 }
             }
-        __syncthreads();
+        lds_barrier();
         // (1 + A)^-1: the 16x16 blocks on the diagonal by substitution, lane c
         // a column, then blocks twice as large from
         //   [[X, 0], [A, Y]]^-1 = [[X^-1, 0], [-Y^-1 A X^-1, Y^-1]].
         if (lane < 16) {
             float col[16];
-            float *b = m + 16 * w * MP + 16 * w;
+            float *blk = m + 16 * w * MP + 16 * w;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 float x = i == lane ? 1.f : 0.f;
 #pragma unroll
                 for (int j = 0; j < i; ++j)
-                    x = fmaf(-b[i * MP + j], col[j], x);
+                    x = fmaf(-blk[i * MP + j], col[j], x);
                 col[i] = x;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                b[i * MP + lane] = col[i];
+                blk[i * MP + lane] = col[i];
         }
-        __syncthreads();
+        lds_barrier();
         if (w < 2) {
             const int i = 2 * w + 1, j = 2 * w;
             f32x4 t = {0.f, 0.f, 0.f, 0.f}, o = t;
@@ -292,7 +313,7 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
             for (int e = 0; e < 4; ++e)
                 m[(16 * i + 4 * g + e) * MP + 16 * j + r] = -o[e];
         }
-        __syncthreads();
+        lds_barrier();
         {
             const int i = 2 + (w >> 1), j = w & 1;
             f32x4 t = {0.f, 0.f, 0.f, 0.f}, o = t;
@@ -306,7 +327,7 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 z[w][(4 * g + e) * 17 + r] = t[e];
-            __syncthreads();
+            lds_barrier();
 #pragma unroll
             for (int k = 2; k < 4; ++k)
                 if (k <= i)
@@ -318,7 +339,7 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
             for (int e = 0; e < 4; ++e)
                 m[(16 * i + 4 * g + e) * MP + 16 * j + r] = -o[e];
         }
-        __syncthreads();
+        lds_barrier();
 
         uint8_t *val = a.vals + ((int64_t)blockIdx.x * p.Hv + h) * W::VAL;
         const int row = token_of(w, r);
@@ -359,16 +380,25 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
     }
 }
 
-// x as bf16 parts, the nearest bf16 of what the parts before left.
+// x as bf16 parts, the nearest bf16 of what the parts before left. Two values
+// a conversion; a part's value is its bits in the upper half of a float.
 template <int N>
 __device__ __forceinline__ void split(const f32x4 &x, bf16x4 (&part)[N])
 {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
     f32x4 left = x;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        part[i] = __builtin_convertvector(left, bf16x4);
-        if (i + 1 < N)
-            left -= __builtin_convertvector(part[i], f32x4);
+        const uint32_t lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{left[0], left[1]}), bf16x2));
+        const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{left[2], left[3]}), bf16x2));
+        part[i] = __builtin_bit_cast(bf16x4, (u32x2{lo, hi}));
+        if (i + 1 < N) {
+            left[0] -= __uint_as_float(lo << 16);
+            left[1] -= __uint_as_float(lo & 0xffff0000u);
+            left[2] -= __uint_as_float(hi << 16);
+            left[3] -= __uint_as_float(hi & 0xffff0000u);
+        }
     }
 }
 
@@ -376,19 +406,24 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_sh
 
 // Waves 0 to 3 carry S, waves 4 to 7 make the outputs. Three exchanges
 // through LDS a chunk, each ended by a barrier that all eight waves meet:
-//   chain wave w: its rows' shares of K S and (Q S)^T    -> xp, op
-//   chain wave w: token tile w of Y, in three parts      -> ysh
-//   chain wave w: token tile w of U, for S' and for O    -> ush
-// then chain wave w updates its rows of S while output wave w adds up token
-// tile w of O. The time of a chunk is that chain's, not its arithmetic, so
-// every operand is loaded right after its last use, a chunk ahead.
+//   chain wave w: its rows' share of K S; its rows of S in two parts  -> xp; ssh
+//   chain wave w: token tile w of Y in three parts                    -> ysh
+//   chain wave w: token tile w of U, for S' in three parts and for O  -> ush; uo
+// then chain wave w updates its rows of S. Output wave w takes Q S between the
+// first two barriers, adds P U of the chunk before between the second and the
+// third, and stores that and brings V and the row factors after it. The time
+// of a chunk is the chain's latencies, not its arithmetic, so whatever is not
+// the chain is left to the output waves, and every operand is loaded right
+// after its last use, a chunk ahead.
 template <int DT, int CB>
-__global__ __launch_bounds__(512) void delta_chunks_kernel(ChunkArgs a)
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void delta_chunks_kernel(ChunkArgs a)
 {
     using W = Space<DT>;
     const DeltaProblem &p = a.p;
-    __shared__ f32x4 xp[4][4][CB][64], op[4][4][CB][64];
-    __shared__ bf16x4 ysh[3][4][CB][64], ush[5][4][CB][64];
+    __shared__ f32x4 xp[4][4][CB][64], uo[2][4][CB][64];
+    __shared__ bf16x8 ssh[2][4][CB][64];
+    __shared__ bf16x4 ysh[3][4][CB][64], ush[3][4][CB][64];
+    __shared__ f32x4 vsh[4][CB][64], upsh[4][64], tailsh[4][64];
     __shared__ __align__(16) int badcol[CB * 16];
 
     // Workgroup i runs on XCD i % 8. The slices of one head go to one XCD,
@@ -414,8 +449,11 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(ChunkArgs a)
     const uint8_t *key0 = a.keys + (number * p.Hk + kh) * W::KEY;
     const uint8_t *val0 = a.vals + (number * p.Hv + h) * W::VAL;
     const int64_t key_step = (int64_t)p.Hk * W::KEY, val_step = (int64_t)p.Hv * W::VAL;
+    // Fragment i from a base that is the same for all lanes: such a load needs no vector address arithmetic while
+    // i * FRAG fits the instruction's offset (-4096 .. 4095 bytes).
+    const uint32_t lane16 = 16 * lane;
     auto frag = [&](const uint8_t *base, int i) __attribute__((always_inline)) {
-        return reinterpret_cast<const bf16x8 *>(base + i * FRAG)[lane];
+        return *reinterpret_cast<const bf16x8 *>(base + lane16 + i * FRAG);
     };
 
     if (threadIdx.x < CB * 16)
@@ -424,61 +462,99 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(ChunkArgs a)
 
     if (w8 >= 4) {
         // ---- Output wave w: token tile w of O, as rows of columns 4g .. 4g + 3, token r.
-        bf16x8 pf[2][2];
+        bf16x8 qf[4], pf[2][2];
         float upq = 0.f;
         int bad_here = NEVER, badall = NEVER;
-        auto load = [&](int c) __attribute__((always_inline)) {
-            const uint8_t *val = val0 + c * val_step;
+        auto load_q = [&](int c) __attribute__((always_inline)) {
+            const uint8_t *key = key0 + c * key_step + W::Q + 4 * w * FRAG;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                qf[i] = frag(key, i);
+        };
+        auto load_p = [&](int c) __attribute__((always_inline)) {
+            const uint8_t *val = val0 + c * val_step, *pv = val + W::P + 2 * low_frag(w, 0) * FRAG;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
+                if (2 * s <= w)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    pf[s][i] = frag(val + W::P, 2 * low_frag(w, 2 * s <= w ? s : 0) + i);
+                    for (int i = 0; i < 2; ++i)
+                        pf[s][i] = frag(pv, 2 * s + i);
             upq = reinterpret_cast<const float *>(val + W::UPQ)[tokr];
             bad_here = reinterpret_cast<const int *>(val + W::HEAD)[1];
         };
-        if (chunks > 0)
-            load(0);
-        uint16_t *oh = static_cast<uint16_t *>(p.o) + (begin + tokr) * p.ost + h * p.osh + col0 + 4 * g;
-        for (int c = 0; c < chunks; ++c) {
-            f32x4 o[CB];
-            lds_barrier();
+        // V and the row factors of chain wave w's tokens, on to it through LDS.
+        uint16_t v[CB][4];
+        f32x4 upk, tail;
+        const uint16_t *vh = static_cast<const uint16_t *>(p.v) + begin * p.vst + h * p.vsh;
+        const int64_t voff = tok4 * p.vst;      // of the lane's first token within a chunk
+        int vcol[CB];               // columns past the end read the last one's; nothing is stored of them
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb) {
-                o[cb] = op[0][w][cb][lane];
+        for (int cb = 0; cb < CB; ++cb)
+            vcol[cb] = min(col0 + 16 * cb + r, p.Dv - 1);
+        auto load_v = [&](int c) __attribute__((always_inline)) {
+            const uint8_t *val = val0 + c * val_step;
+            upk = *reinterpret_cast<const f32x4 *>(val + W::UPK + 4 * tok4);
+            tail = *reinterpret_cast<const f32x4 *>(val + W::TAIL + 4 * tok4);
+            const uint16_t *vc = vh + (int64_t)c * C * p.vst;
+            // Tokens past the end read the last one's: T's columns are zero for
+            // them. (No branch: the compiler would wait for the loads at its end.)
+            const int last = len - 1 - c * C;
 #pragma unroll
-                for (int i = 1; i < 4; ++i)
-                    o[cb] += op[i][w][cb][lane];
-                o[cb] *= upq;
+            for (int e = 0; e < 4; ++e) {
+                const int64_t off = tok4 + e <= last ? voff : (last - e) * p.vst;
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+                    v[cb][e] = (vc + e * p.vst + off)[vcol[cb]];
             }
-            lds_barrier();
-            lds_barrier();
+        };
+        auto give_v = [&]() __attribute__((always_inline)) {
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb)
+                vsh[w][cb][lane] = f32x4{bf16_to_f32(v[cb][0]), bf16_to_f32(v[cb][1]), bf16_to_f32(v[cb][2]),
+                                         bf16_to_f32(v[cb][3])};
+            upsh[w][lane] = upk;
+            tailsh[w][lane] = tail;
+        };
+        if (chunks > 0) {
+            load_v(0);
+            give_v();
+            load_v(min(1, chunks - 1));
+            load_q(0);
+        }
+        uint16_t *oh = static_cast<uint16_t *>(p.o) + (begin + tokr) * p.ost + h * p.osh + col0 + 4 * g;
+        f32x4 o[CB];
+        // The second term of chunk c's outputs, U in two parts.
+        auto add_pu = [&](int c) __attribute__((always_inline)) {
+            if (badall == NEVER && bad_here != NEVER)
+                badall = c * C + bad_here;
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                o[cb] *= upq;
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (2 * s <= w) {
-                        const bf16x8 u0 = join(ush[3][2 * s][cb][lane], ush[3][2 * s + 1][cb][lane]);
-                        const bf16x8 u1 = join(ush[4][2 * s][cb][lane], ush[4][2 * s + 1][cb][lane]);
+                        bf16x4 lo[2], hi[2];
+                        split<2>(uo[c & 1][2 * s][cb][lane], lo);
+                        split<2>(uo[c & 1][2 * s + 1][cb][lane], hi);
+                        const bf16x8 u0 = join(lo[0], hi[0]), u1 = join(lo[1], hi[1]);
                         o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u1, pf[s][0], o[cb], 0, 0, 0);
                         o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][1], o[cb], 0, 0, 0);
                         o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][0], o[cb], 0, 0, 0);
                     }
+            }
+        };
+        auto store = [&](int c) __attribute__((always_inline)) {
             const int t = c * C + tokr;
-            if (badall == NEVER && bad_here != NEVER)
-                badall = c * C + bad_here;
-            load(min(c + 1, chunks - 1));
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb) {
-                const int *bc = badcol + 16 * cb + 4 * g;
+                const i32x4 bc = *reinterpret_cast<const i32x4 *>(badcol + 16 * cb + 4 * g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     o[cb][e] = t >= min(badall, bc[e]) ? NAN : o[cb][e];
-                const bf16x4 ov = __builtin_convertvector(o[cb], bf16x4);
                 const int left = p.Dv - (col0 + 16 * cb + 4 * g);
                 if (t < len) {
                     if (a.vec_o && left >= 4) {
-                        *reinterpret_cast<bf16x4 *>(oh + 16 * cb) = ov;
+                        *reinterpret_cast<bf16x4 *>(oh + 16 * cb) = __builtin_convertvector(o[cb], bf16x4);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -488,6 +564,40 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(ChunkArgs a)
                 }
             }
             oh += C * p.ost;
+        };
+        for (int c = 0; c < chunks; ++c) {
+            lds_barrier();
+            // S^T Q^T, every wave's rows of S.
+            f32x4 q[CB];
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+                q[cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 1; j >= 0; --j)
+                        q[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ssh[j][i][cb][lane], qf[i], q[cb], 0, 0, 0);
+            }
+            load_q(min(c + 1, chunks - 1));
+            lds_barrier();
+            // While the chain works on U, the chunk before gets its second term.
+            if (c > 0)
+                add_pu(c - 1);
+            load_p(c);
+            lds_barrier();
+            // For the next chunk: the chain reads them between the next two
+            // barriers, and took its last look at this chunk's before the one above.
+            give_v();
+            load_v(min(c + 2, chunks - 1));
+            if (c > 0)
+                store(c - 1);
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb)
+                o[cb] = q[cb];
+        }
+        if (chunks > 0) {
+            add_pu(chunks - 1);
+            store(chunks - 1);
         }
         return;
     }
@@ -511,101 +621,78 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(ChunkArgs a)
                 S[d][cb][e] = dk < p.Dk && col < p.Dv ? v : 0.f;
             }
 
-    bf16x8 kf[4], qf[4], ktf[DT][2], tf[2][3];
-    f32x4 upk, tail;
-    float last = 1.f;
-    int bad_any = 0;            // of the chunks whose K^T was loaded: some token is not finite
-    uint16_t v[CB][4];
-    const uint16_t *vh = static_cast<const uint16_t *>(p.v) + begin * p.vst + h * p.vsh;
-    auto load_kq = [&](int c) __attribute__((always_inline)) {
-        const uint8_t *key = key0 + c * key_step;
+    bf16x8 kf[4], ktf[DT][2], tf[2][3];
+    u32x2 head = {0, 0};
+    bool bad_any = false;       // some token of a chunk so far is not finite
+    auto load_k = [&](int c) __attribute__((always_inline)) {
+        const uint8_t *key = key0 + c * key_step + 4 * w * FRAG;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            kf[i] = frag(key, 4 * i + w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            qf[i] = frag(key + W::Q, 4 * i + w);
-    };
-    auto load_v = [&](int c) __attribute__((always_inline)) {
-        upk = *reinterpret_cast<const f32x4 *>(val0 + c * val_step + W::UPK + 4 * tok4);
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // Tokens and columns past the end read the last one's; they are zeroed when used.
-                const int t = min(c * C + tok4 + e, len - 1), col = min(col0 + 16 * cb + r, p.Dv - 1);
-                v[cb][e] = vh[t * p.vst + col];
-            }
+            kf[i] = frag(key, i);
     };
     auto load_t = [&](int c) __attribute__((always_inline)) {
-        const uint8_t *val = val0 + c * val_step;
-        // No load is conditional (a branch would make the compiler wait at
-        // its end); waves 0 and 1 do not use what they load for s = 1.
+        const uint8_t *val = val0 + c * val_step + (3 * low_frag(w, 0) + 2) * FRAG;
 #pragma unroll
         for (int s = 0; s < 2; ++s)
+            if (2 * s <= w)
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                tf[s][i] = frag(val, 3 * low_frag(w, 2 * s <= w ? s : 0) + i);
-        tail = *reinterpret_cast<const f32x4 *>(val + W::TAIL + 4 * tok4);
+                for (int i = 0; i < 3; ++i)
+                    tf[s][i] = frag(val, 3 * s + i - 2);
     };
     auto load_kt = [&](int c) __attribute__((always_inline)) {
+        const uint8_t *key = key0 + c * key_step + W::KT + 2 * DT * w * FRAG;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                ktf[d][s] = frag(key0 + c * key_step + W::KT, (w * DT + d) * 2 + s);
-        const u32x2 head = *reinterpret_cast<const u32x2 *>(val0 + c * val_step + W::HEAD);
-        last = __uint_as_float(head[0]);
-        bad_any |= (int)head[1] != NEVER;
+                ktf[d][s] = frag(key, 2 * d + s);
+        head = *reinterpret_cast<const u32x2 *>(val0 + c * val_step + W::HEAD);
     };
     if (chunks > 0) {
-        load_kq(0);
-        load_v(0);
+        load_k(0);
         load_t(0);
         load_kt(0);
     }
+    __builtin_amdgcn_s_setprio(3);      // before the output wave of the same SIMD
     for (int c = 0; c < chunks; ++c) {
         const int next = min(c + 1, chunks - 1);
-        // K S and S^T Q^T, wave w's rows of S only.
+        // K S, wave w's rows of S only.
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
             bf16x4 lo[3], hi[3] = {};
             split<3>(S[0][cb], lo);
             if constexpr (DT == 2)
                 split<3>(S[DT - 1][cb], hi);
+            f32x4 acc[4] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (int j = 2; j >= 0; --j)
 #pragma unroll
-                for (int j = 2; j >= 0; --j)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], join(lo[j], hi[j]), acc, 0, 0, 0);
-                xp[w][i][cb][lane] = acc;
-            }
+                for (int i = 0; i < 4; ++i)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], join(lo[j], hi[j]), acc[i], 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; ++i)
+                xp[w][i][cb][lane] = acc[i];
 #pragma unroll
-                for (int j = 1; j >= 0; --j)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(join(lo[j], hi[j]), qf[i], acc, 0, 0, 0);
-                op[w][i][cb][lane] = acc;
-            }
+            for (int j = 0; j < 2; ++j)
+                ssh[j][w][cb][lane] = join(lo[j], hi[j]);
         }
-        load_kq(next);
+        load_k(next);
         lds_barrier();
         // Token tile w of Y = V - diag(r exp G) K S.
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-            f32x4 y = xp[0][w][cb][lane];
+            f32x4 x[4];
 #pragma unroll
-            for (int i = 1; i < 4; ++i)
-                y += xp[i][w][cb][lane];
-            bool bad = false;
+            for (int i = 0; i < 4; ++i)
+                x[i] = xp[i][w][cb][lane];
+            const f32x4 v = vsh[w][cb][lane], up = upsh[w][lane];
+            __builtin_amdgcn_sched_barrier(0);      // all reads before the first sum
+            f32x4 y = v - up * ((x[0] + x[1]) + (x[2] + x[3]));
+            float zero = 0.f;                       // NaN if anything of y is not finite
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[e] = (c * C + tok4 + e < len ? bf16_to_f32(v[cb][e]) : 0.f) - upk[e] * y[e];
-                bad |= !(fabsf(y[e]) < INFINITY);
-            }
-            if (__any(bad))
+            for (int e = 0; e < 4; ++e)
+                zero = fmaf(y[e], 0.f, zero);
+            if (__any(zero != 0.f))
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (!(fabsf(y[e]) < INFINITY)) {
@@ -618,9 +705,9 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(ChunkArgs a)
             for (int i = 0; i < 3; ++i)
                 ysh[i][w][cb][lane] = part[i];
         }
-        load_v(next);
         lds_barrier();
         // Token tile w of U = T Y.
+        const f32x4 tail = tailsh[w][lane];
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
             f32x4 u = {0.f, 0.f, 0.f, 0.f};
@@ -637,23 +724,22 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(ChunkArgs a)
                         for (int i = 0; i <= k; ++i)
                             u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tf[s][i], y[k - i], u, 0, 0, 0);
                 }
-            bf16x4 us[3], uo[2];
+            uo[c & 1][w][cb][lane] = u;
+            bf16x4 us[3];
             split<3>(u * tail, us);
-            split<2>(u, uo);
 #pragma unroll
             for (int i = 0; i < 3; ++i)
                 ush[i][w][cb][lane] = us[i];
-            ush[3][w][cb][lane] = uo[0];
-            ush[4][w][cb][lane] = uo[1];
         }
         load_t(next);
         lds_barrier();
         // S'.
+        bad_any |= (int)head[1] != NEVER;
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
 #pragma unroll
             for (int d = 0; d < DT; ++d)
-                S[d][cb] *= last;
+                S[d][cb] *= __uint_as_float(head[0]);
 #pragma unroll
             for (int i = 2; i >= 0; --i)
 #pragma unroll
