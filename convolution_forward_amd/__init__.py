@@ -191,8 +191,16 @@ def _dtype_code(t) -> int:
     raise ValueError(f"unsupported dtype {t}; use float32 or bfloat16")
 
 
+def _stream_of(gpu: int) -> int:
+    """The current stream of a GPU. torch's raw query gives the handle without
+    building a Stream object (0.1 us against 1.9)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(gpu) if raw is not None else torch.cuda.current_stream(gpu).cuda_stream
+
+
 def _stream_ptr(device) -> int:
-    return _torch().cuda.current_stream(device).cuda_stream
+    return _stream_of(_torch().cuda.current_device() if device.index is None else device.index)
 
 
 def _require_gpu(*tensors):

@@ -18,7 +18,8 @@ namespace convfwd {
 namespace {
 
 constexpr int NT = 256;
-constexpr int TT = 16;
+constexpr int TT = 32;               // tokens of a tile
+constexpr int BATCH = 8;             // rows in flight a thread
 
 template <class T, int V>
 struct Vec {
@@ -26,13 +27,20 @@ struct Vec {
 };
 
 template <class T, int V>
-__device__ __forceinline__ void load_vec(const T *p, float (&f)[V])
+__device__ __forceinline__ Vec<T, V> load_raw(const T *p)
 {
     Vec<T, V> t;
     if constexpr (V > 1)
-        t = *reinterpret_cast<const Vec<T, V> *>(__builtin_assume_aligned(p, V * sizeof(T)));
+        __builtin_memcpy(&t, __builtin_assume_aligned(p, V * sizeof(T)), sizeof(t));
     else
         t.v[0] = *p;
+    return t;
+}
+
+template <class T, int V>
+__device__ __forceinline__ void load_vec(const T *p, float (&f)[V])
+{
+    const Vec<T, V> t = load_raw<T, V>(p);
 #pragma unroll
     for (int i = 0; i < V; ++i)
         f[i] = load_as_f32(&t.v[i]);
@@ -46,7 +54,7 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[V])
     for (int i = 0; i < V; ++i)
         store_from_f32(&t.v[i], f[i]);
     if constexpr (V > 1)
-        *reinterpret_cast<Vec<T, V> *>(__builtin_assume_aligned(p, V * sizeof(T))) = t;
+        __builtin_memcpy(__builtin_assume_aligned(p, V * sizeof(T)), &t, sizeof(t));
     else
         *p = t.v[0];
 }
@@ -90,9 +98,10 @@ __global__ __launch_bounds__(NT) void causal_conv1d_kernel(Causal1dProblem p)
 #pragma unroll
     for (int j = 0; j < K - 1; ++j)
         row(t0 - (K - 1) + j, win[j]);
-    const int64_t end = tile.len - t0 < TT ? tile.len - t0 : TT;
-    for (int t = 0; t < end; ++t) {
-        row(t0 + t, win[K - 1]);
+    const int end = (int)(tile.len - t0 < TT ? tile.len - t0 : TT);
+    const T *xt = x + t0 * p.xs;
+    T *yt = y + t0 * p.ys;
+    auto one = [&](int t) __attribute__((always_inline)) {      // win[K - 1] holds row t
         float f[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -105,7 +114,25 @@ __global__ __launch_bounds__(NT) void causal_conv1d_kernel(Causal1dProblem p)
             for (int j = 0; j < K - 1; ++j)
                 win[j][i] = win[j + 1][i];
         }
-        store_vec<T, V>(y + (t0 + t) * p.ys, f);
+        store_vec<T, V>(yt + t * p.ys, f);
+    };
+    int t = 0;
+    for (; t + BATCH <= end; t += BATCH) {
+        Vec<T, V> rows[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u)
+            rows[u] = load_raw<T, V>(xt + (t + u) * p.xs);
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                win[K - 1][i] = load_as_f32(&rows[u].v[i]);
+            one(t + u);
+        }
+    }
+    for (; t < end; ++t) {
+        load_vec<T, V>(xt + t * p.xs, win[K - 1]);
+        one(t);
     }
     if (first && p.state_out && slot >= 0) {
         // Ascending: row r of the new state is row len + r of (old state, x),

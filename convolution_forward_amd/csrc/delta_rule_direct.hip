@@ -26,12 +26,14 @@ __device__ __forceinline__ float rows_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-template <class T, int R>
+// WIDE: heads, columns and rows allow 16-byte pieces (a host rule): S by four
+// columns, q and k by R rows at once.
+template <class T, int R, bool WIDE>
 __global__ __launch_bounds__(256) void delta_direct_kernel(DeltaProblem p, int slices)
 {
     const int lane = threadIdx.x & 63;
     const int rg = lane >> 3, c = lane & 7;
-    const int64_t job = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
     const int slice = (int)(job % slices);
     const int64_t nh = job / slices;
     const int n = (int)(nh / p.Hv), h = (int)(nh % p.Hv);
@@ -49,18 +51,51 @@ __global__ __launch_bounds__(256) void delta_direct_kernel(DeltaProblem p, int s
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            S[i][j] = p.state_in && slot >= 0 && row + i < p.Dk && col + j < p.Dv
-                          ? p.state_in[sat + (int64_t)(row + i) * p.Dv + col + j]
-                          : 0.f;
+            S[i][j] = 0.f;
+    if (p.state_in && slot >= 0) {
+        const float *si = p.state_in + sat + (int64_t)row * p.Dv + col;
+        if constexpr (WIDE) {
+            if (row < p.Dk && col < p.Dv) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float4 v = *reinterpret_cast<const float4 *>(si + (int64_t)i * p.Dv);
+                    S[i][0] = v.x, S[i][1] = v.y, S[i][2] = v.z, S[i][3] = v.w;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (row + i < p.Dk && col + j < p.Dv)
+                        S[i][j] = si[(int64_t)i * p.Dv + j];
+        }
+    }
     for (int64_t t = begin; t < end; ++t) {
         const T *kp = static_cast<const T *>(p.k) + t * p.kst + kh * p.ksh;
         const T *qp = static_cast<const T *>(p.q) + t * p.qst + kh * p.qsh;
         float k[R], q[R];
         float kk = 0.f, qq = 0.f, kq = 0.f;
+        if constexpr (WIDE) {
+            T kv[R] __attribute__((aligned(16))) = {}, qv[R] __attribute__((aligned(16))) = {};
+            if (row < p.Dk) {
+                __builtin_memcpy(kv, __builtin_assume_aligned(kp + row, 16), sizeof(kv));
+                __builtin_memcpy(qv, __builtin_assume_aligned(qp + row, 16), sizeof(qv));
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                k[i] = load_as_f32(kv + i);
+                q[i] = load_as_f32(qv + i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                k[i] = row + i < p.Dk ? load_as_f32(kp + row + i) : 0.f;
+                q[i] = row + i < p.Dk ? load_as_f32(qp + row + i) : 0.f;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            k[i] = row + i < p.Dk ? load_as_f32(kp + row + i) : 0.f;
-            q[i] = row + i < p.Dk ? load_as_f32(qp + row + i) : 0.f;
             kk = fmaf(k[i], k[i], kk);
             qq = fmaf(q[i], q[i], qq);
             kq = fmaf(k[i], q[i], kq);
@@ -99,27 +134,50 @@ __global__ __launch_bounds__(256) void delta_direct_kernel(DeltaProblem p, int s
                 store_from_f32(static_cast<T *>(p.o) + t * p.ost + h * p.osh + col + j, o[j]);
         }
     }
-    if (p.state_out && slot >= 0)
+    if (p.state_out && slot >= 0) {
+        float *so = p.state_out + sat + (int64_t)row * p.Dv + col;
+        if constexpr (WIDE) {
+            if (row < p.Dk && col < p.Dv) {
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+                for (int i = 0; i < R; ++i)
+                    *reinterpret_cast<float4 *>(so + (int64_t)i * p.Dv) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+            }
+        } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (row + i < p.Dk && col + j < p.Dv)
-                    p.state_out[sat + (int64_t)(row + i) * p.Dv + col + j] = S[i][j];
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (row + i < p.Dk && col + j < p.Dv)
+                        so[(int64_t)i * p.Dv + j] = S[i][j];
+        }
+    }
+}
+
+template <class T, int R>
+void launch_rows(const DeltaProblem &p, hipStream_t s)
+{
+    const int slices = (p.Dv + 31) / 32;
+    const int64_t jobs = (int64_t)p.seq.num_seqs * p.Hv * slices;
+    // Few waves: one a workgroup, so that they spread over the compute units.
+    const int waves = jobs <= 1024 ? 1 : 4;
+    const dim3 grid((unsigned)((jobs + waves - 1) / waves)), block(64 * waves);
+    const uintptr_t bits = (uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.state_in | (uintptr_t)p.state_out |
+                           (uintptr_t)((p.qst | p.qsh | p.kst | p.ksh) * (int64_t)sizeof(T));
+    if (bits % 16 == 0 && p.Dk % R == 0 && p.Dv % 4 == 0)
+        hipLaunchKernelGGL((delta_direct_kernel<T, R, true>), grid, block, 0, s, p, slices);
+    else
+        hipLaunchKernelGGL((delta_direct_kernel<T, R, false>), grid, block, 0, s, p, slices);
 }
 
 template <class T>
 void launch(const DeltaProblem &p, hipStream_t s)
 {
-    const int slices = (p.Dv + 31) / 32;
-    const int64_t jobs = (int64_t)p.seq.num_seqs * p.Hv * slices;
-    const dim3 grid((unsigned)((jobs + 3) / 4));
     if (p.Dk <= 64)
-        hipLaunchKernelGGL((delta_direct_kernel<T, 8>), grid, dim3(256), 0, s, p, slices);
+        launch_rows<T, 8>(p, s);
     else if (p.Dk <= 128)
-        hipLaunchKernelGGL((delta_direct_kernel<T, 16>), grid, dim3(256), 0, s, p, slices);
+        launch_rows<T, 16>(p, s);
     else
-        hipLaunchKernelGGL((delta_direct_kernel<T, 32>), grid, dim3(256), 0, s, p, slices);
+        launch_rows<T, 32>(p, s);
 }
 
 }  // namespace

@@ -3,15 +3,19 @@
 //   h = x + r rounded to the tensors' type;  y_j = h_j * rsqrt(mean(h^2) + eps) * w_j
 //   scale = max|y| / QMAX;  q = y / scale to nearest even
 //
-// One workgroup a row. The mean, the norm and the scale are fp32.
+// One pass over memory: a row's h stays in registers from its load to its
+// quantised store, between the two reductions (sum of squares, largest |y|).
+// The bytes are the time, 16 a load: x and r in, h and q out.
+//
+// The mean, the norm and the scale are fp32. Rows need no alignment: the
+// loads and stores are unaligned ones, and the last piece of a row goes value
+// by value.
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"
 
 namespace convfwd {
 namespace {
-
-constexpr int NT = 256;
 
 __device__ __forceinline__ float wave_sum(float v)
 {
@@ -31,73 +35,240 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
     return v;
 }
 
-template <class T, bool E4M3>
-__global__ __launch_bounds__(NT) void rms_norm_q8_kernel(NormProblem p)
+// Both reductions over the WPR waves of a row.
+template <int WPR>
+struct Reduce {
+    float part[WPR > 1 ? WPR : 1];
+    uint32_t tops[WPR > 1 ? WPR : 1];
+
+    __device__ __forceinline__ float sum(float v, int wave)
+    {
+        v = wave_sum(v);
+        if constexpr (WPR > 1) {
+            if ((threadIdx.x & 63) == 0)
+                part[wave] = v;
+            __syncthreads();
+            v = 0.f;
+#pragma unroll
+            for (int i = 0; i < WPR; ++i)
+                v += part[i];
+        }
+        return v;
+    }
+
+    __device__ __forceinline__ uint32_t top(uint32_t v, int wave)
+    {
+        v = wave_max(v);
+        if constexpr (WPR > 1) {
+            if ((threadIdx.x & 63) == 0)
+                tops[wave] = v;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < WPR; ++i)
+                v = max(v, tops[i]);
+        }
+        return v;
+    }
+};
+
+template <bool E4M3>
+__device__ __forceinline__ float quant_scale(float sum, uint32_t top_bits, float *scale, bool first, bool &fine)
 {
-    __shared__ float part[NT / 64];
-    __shared__ uint32_t tops[NT / 64];
+    constexpr float QMAX = E4M3 ? 448.f : 127.f;
+    const float top = __uint_as_float(top_bits);
+    fine = sum < INFINITY && top < INFINITY;
+    if (first)
+        *scale = fine ? top / QMAX : NAN;
+    return fine && top > 0.f ? QMAX / top : 0.f;
+}
+
+template <class T>
+struct Piece {
+    static constexpr int V = 16 / sizeof(T);
+    T v[V];
+};
+
+template <class T>
+__device__ __forceinline__ Piece<T> load_piece(const T *p, int left)
+{
+    Piece<T> x = {};
+    if (left >= Piece<T>::V) {
+        __builtin_memcpy(&x, p, sizeof(x));
+    } else {
+#pragma unroll
+        for (int i = 0; i < Piece<T>::V; ++i)
+            if (i < left)
+                x.v[i] = p[i];
+    }
+    return x;
+}
+
+template <class E, int V>
+__device__ __forceinline__ void store_piece(E *p, const E (&x)[V], int left)
+{
+    if (left >= V) {
+        __builtin_memcpy(p, x, sizeof(x));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < left)
+                p[i] = x[i];
+    }
+}
+
+// WPR waves a row, NV pieces of 16 bytes a lane; one wave a row takes four
+// rows a workgroup and needs no barrier.
+template <class T, int WPR, int NV, bool RES, bool E4M3>
+__global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rms_norm_q8_kernel(NormProblem p)
+{
+    constexpr int V = Piece<T>::V;
+    __shared__ Reduce<WPR> red;
+    const int wave = threadIdx.x >> 6;
+    const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
+    if (WPR == 1 && row >= p.rows)
+        return;
+    const int at = WPR == 1 ? (threadIdx.x & 63) : threadIdx.x;
+    const T *x = static_cast<const T *>(p.x) + row * p.xs;
+    const T *w = static_cast<const T *>(p.weight);
+    Piece<T> h[NV], r[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        h[i] = load_piece(x + (at + i * 64 * WPR) * V, p.width - (at + i * 64 * WPR) * V);
+    if constexpr (RES) {
+        const T *rp = static_cast<const T *>(p.residual) + row * p.rs;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            r[i] = load_piece(rp + (at + i * 64 * WPR) * V, p.width - (at + i * 64 * WPR) * V);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if constexpr (RES)
+                store_from_f32(&h[i].v[j], load_as_f32(&h[i].v[j]) + load_as_f32(&r[i].v[j]));
+            const float v = load_as_f32(&h[i].v[j]);
+            sum = fmaf(v, v, sum);
+        }
+        if constexpr (RES)
+            store_piece(static_cast<T *>(p.h) + row * p.hs + (at + i * 64 * WPR) * V, h[i].v,
+                        p.width - (at + i * 64 * WPR) * V);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        r[i] = load_piece(w + (at + i * 64 * WPR) * V, p.width - (at + i * 64 * WPR) * V);
+    sum = red.sum(sum, wave);
+    const float rinv = 1.f / sqrtf(sum / (float)p.width + p.eps);
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            top = max(top, __float_as_uint(fabsf(load_as_f32(&h[i].v[j]) * rinv * load_as_f32(&r[i].v[j]))));
+    top = red.top(top, wave);
+    bool fine;
+    const float inv = quant_scale<E4M3>(sum, top, p.scale + row, at == 0, fine);
+    uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.qs;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        uint8_t o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            o[j] = fine ? to_eight<E4M3>(load_as_f32(&h[i].v[j]) * rinv * load_as_f32(&r[i].v[j]) * inv) : 0;
+        store_piece(q + (at + i * 64 * WPR) * V, o, p.width - (at + i * 64 * WPR) * V);
+    }
+}
+
+// Rows past what registers hold: the row is read again for each step.
+constexpr int LONG_WAVES = 16;
+
+template <class T, bool E4M3>
+__global__ __launch_bounds__(64 * LONG_WAVES) void rms_norm_q8_long_kernel(NormProblem p)
+{
+    constexpr int NT = 64 * LONG_WAVES;
+    __shared__ Reduce<LONG_WAVES> red;
+    const int wave = threadIdx.x >> 6;
     const int64_t row = blockIdx.x;
     const T *x = static_cast<const T *>(p.x) + row * p.xs;
     const T *r = p.residual ? static_cast<const T *>(p.residual) + row * p.rs : nullptr;
     const T *w = static_cast<const T *>(p.weight);
     T *h = p.h ? static_cast<T *>(p.h) + row * p.hs : nullptr;
-    uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.qs;
     float sum = 0.f;
     for (int j = threadIdx.x; j < p.width; j += NT) {
-        float v = load_as_f32(x + j);
+        T t = x[j];
         if (r) {
-            T t;
-            store_from_f32(&t, v + load_as_f32(r + j));
+            store_from_f32(&t, load_as_f32(&t) + load_as_f32(r + j));
             h[j] = t;
-            v = load_as_f32(&t);
         }
-        sum += v * v;
+        const float v = load_as_f32(&t);
+        sum = fmaf(v, v, sum);
     }
-    sum = wave_sum(sum);
-    if ((threadIdx.x & 63) == 0)
-        part[threadIdx.x >> 6] = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int i = 0; i < NT / 64; ++i)
-        sum += part[i];
+    sum = red.sum(sum, wave);
     const float rinv = 1.f / sqrtf(sum / (float)p.width + p.eps);
-    const T *src = r ? h : x;
-    uint32_t top_bits = 0;
+    const T *src = r ? h : x;               // each thread reads back what it wrote
+    uint32_t top = 0;
     for (int j = threadIdx.x; j < p.width; j += NT)
-        top_bits = max(top_bits, __float_as_uint(fabsf(load_as_f32(src + j) * rinv * load_as_f32(w + j))));
-    top_bits = wave_max(top_bits);
-    if ((threadIdx.x & 63) == 0)
-        tops[threadIdx.x >> 6] = top_bits;
-    __syncthreads();
-    for (int i = 0; i < NT / 64; ++i)
-        top_bits = max(top_bits, tops[i]);
-    const float top = __uint_as_float(top_bits);
-    constexpr float QMAX = E4M3 ? 448.f : 127.f;
-    const bool fine = sum < INFINITY && top < INFINITY;
-    const float inv = fine && top > 0.f ? QMAX / top : 0.f;
-    if (threadIdx.x == 0)
-        p.scale[row] = fine ? top / QMAX : NAN;
+        top = max(top, __float_as_uint(fabsf(load_as_f32(src + j) * rinv * load_as_f32(w + j))));
+    top = red.top(top, wave);
+    bool fine;
+    const float inv = quant_scale<E4M3>(sum, top, p.scale + row, threadIdx.x == 0, fine);
+    uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.qs;
     for (int j = threadIdx.x; j < p.width; j += NT)
         q[j] = fine ? to_eight<E4M3>(load_as_f32(src + j) * rinv * load_as_f32(w + j) * inv) : 0;
 }
 
-template <class T>
+template <class T, int WPR, int NV, bool E4M3>
+void launch_held(const NormProblem &p, hipStream_t s)
+{
+    const unsigned grid = (unsigned)(WPR == 1 ? (p.rows + 3) / 4 : p.rows);
+    const unsigned block = WPR == 1 ? 256 : 64 * WPR;
+    if (p.residual)
+        hipLaunchKernelGGL((rms_norm_q8_kernel<T, WPR, NV, true, E4M3>), dim3(grid), dim3(block), 0, s, p);
+    else
+        hipLaunchKernelGGL((rms_norm_q8_kernel<T, WPR, NV, false, E4M3>), dim3(grid), dim3(block), 0, s, p);
+}
+
+// The fewest waves a row that hold it in eight pieces a lane, or four waves
+// where rows alone would leave the chip's 1024 wave slots at work half empty
+// (a row's latency then counts more than the barriers).
+template <class T, bool E4M3>
 void launch(const NormProblem &p, hipStream_t s)
 {
-    if (p.qdt == CONV_E4M3)
-        hipLaunchKernelGGL((rms_norm_q8_kernel<T, true>), dim3((unsigned)p.rows), dim3(NT), 0, s, p);
-    else
-        hipLaunchKernelGGL((rms_norm_q8_kernel<T, false>), dim3((unsigned)p.rows), dim3(NT), 0, s, p);
+    constexpr int V = Piece<T>::V;
+    const int pieces = (p.width + 64 * V - 1) / (64 * V);       // of one wave
+    if (pieces <= 8 && (p.rows >= 512 || pieces == 1)) {
+        if (pieces <= 1)
+            launch_held<T, 1, 1, E4M3>(p, s);
+        else if (pieces <= 2)
+            launch_held<T, 1, 2, E4M3>(p, s);
+        else if (pieces <= 4)
+            launch_held<T, 1, 4, E4M3>(p, s);
+        else
+            launch_held<T, 1, 8, E4M3>(p, s);
+    } else if (pieces <= 4) {
+        launch_held<T, 4, 1, E4M3>(p, s);
+    } else if (pieces <= 8) {
+        launch_held<T, 4, 2, E4M3>(p, s);
+    } else if (pieces <= 16) {
+        launch_held<T, 4, 4, E4M3>(p, s);
+    } else if (pieces <= 32) {
+        launch_held<T, 8, 4, E4M3>(p, s);
+    } else if (pieces <= 64) {
+        launch_held<T, 16, 4, E4M3>(p, s);
+    } else {
+        hipLaunchKernelGGL((rms_norm_q8_long_kernel<T, E4M3>), dim3((unsigned)p.rows), dim3(64 * LONG_WAVES), 0, s, p);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_rms_norm_q8(const NormProblem &p, hipStream_t s)
 {
+    const bool e = p.qdt == CONV_E4M3;
     if (p.dtype == CONV_BF16)
-        launch<uint16_t>(p, s);
+        e ? launch<uint16_t, true>(p, s) : launch<uint16_t, false>(p, s);
     else
-        launch<float>(p, s);
+        e ? launch<float, true>(p, s) : launch<float, false>(p, s);
     return hipGetLastError();
 }
 

@@ -13,7 +13,9 @@ import ctypes
 
 import torch
 
-from . import (CONV_BF16, CONV_E4M3, CONV_F32, CONV_I8, VARIANT_AUTO, _check, _stream_ptr, load_library)
+from . import (CONV_BF16, CONV_E4M3, CONV_F32, CONV_I8, VARIANT_AUTO, _check, _stream_of, load_library)
+
+_Strides = ctypes.c_int64 * 2
 
 _FLOAT = {torch.float32: CONV_F32, torch.bfloat16: CONV_BF16}
 _EIGHT = {torch.int8: CONV_I8, torch.float8_e4m3fn: CONV_E4M3}
@@ -27,13 +29,14 @@ def _code(table, t, what):
 
 
 def _same_gpu(first, *others):
-    dev = first.device
-    if dev.type != "cuda":
+    """The GPU's index, the same for every tensor."""
+    gpu = first.get_device()
+    if gpu < 0:
         raise ValueError("tensors must live on the GPU (no CPU path exists)")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: all must be on one GPU")
-    return dev
+        if t is not None and t.get_device() != gpu:
+            raise ValueError(f"tensors on {first.device} and {t.device}: all must be on one GPU")
+    return gpu
 
 
 def _ptr(t):
@@ -47,12 +50,16 @@ def _vector(t, n, dtype, what):
 
 def _rows(t, what, width=None, rows=None, dtype=None):
     """Row stride of a [rows, width] tensor whose channels are adjacent."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (width is not None and t.shape[1] != width) or \
-            (rows is not None and t.shape[0] != rows) or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what} must be [{'rows' if rows is None else rows}, {'width' if width is None else width}]"
-                         f"{'' if dtype is None else f' {dtype}'} with adjacent channels, got {tuple(t.shape)} {t.dtype}"
-                         f" with strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    shape = t.shape
+    if len(shape) == 2 and (width is None or shape[1] == width) and (rows is None or shape[0] == rows) and \
+            (dtype is None or t.dtype == dtype):
+        if t.is_contiguous():
+            return shape[1]
+        if t.stride(1) == 1 or shape[1] == 1:
+            return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+    raise ValueError(f"{what} must be [{'rows' if rows is None else rows}, {'width' if width is None else width}]"
+                     f"{'' if dtype is None else f' {dtype}'} with adjacent channels, got {tuple(shape)} {t.dtype}"
+                     f" with strides {t.stride()}")
 
 
 def _flat(t):
@@ -74,7 +81,7 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, out_dtype=torch.int
     h = x + residual (None without a residual). sum_out may be x or residual.
     """
     lib = load_library()
-    dev = _same_gpu(x, weight, residual, out, scale, sum_out)
+    gpu = _same_gpu(x, weight, residual, out, scale, sum_out)
     dt = _code(_FLOAT, x.dtype, "x")
     width = x.shape[-1]
     x2 = _flat(x)
@@ -87,22 +94,22 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, out_dtype=torch.int
         r2 = _flat(residual)
         rs = _rows(r2, "residual", width, rows, x.dtype)
         if sum_out is None:
-            sum_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         h2 = _flat(sum_out)
         hs = _rows(h2, "sum_out", width, rows, x.dtype)
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
     q2 = _flat(out)
     qs = _rows(q2, "out", width, rows)
     qdt = _code(_EIGHT, out.dtype, "out")
     if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     else:
         _vector(scale, rows, torch.float32, "scale")
     _check(lib.conv_rms_norm_q8_fwd(x2.data_ptr(), xs, _ptr(r2), rs, weight.data_ptr(), _ptr(h2), hs, q2.data_ptr(), qs,
-                                    scale.data_ptr(), rows, width, eps, dt, qdt, _stream_ptr(dev)),
+                                    scale.data_ptr(), rows, width, eps, dt, qdt, _stream_of(gpu)),
            "conv_rms_norm_q8_fwd")
     return out, scale, sum_out
 
@@ -115,7 +122,7 @@ def matmul_q8(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out=N
     torch.bfloat16 or torch.float32.
     """
     lib = load_library()
-    dev = _same_gpu(x, x_scale, w, w_scale, bias, out)
+    gpu = _same_gpu(x, x_scale, w, w_scale, bias, out)
     q = _code(_EIGHT, x.dtype, "x")
     x2 = _flat(x)
     M, K = x2.shape
@@ -126,12 +133,12 @@ def matmul_q8(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out=N
     _vector(w_scale, N, torch.float32, "w_scale")
     _vector(bias, N, torch.float32, "bias")
     if out is None:
-        out = torch.empty(x.shape[:-1] + (N,), dtype=out_dtype, device=dev)
+        out = torch.empty(x.shape[:-1] + (N,), dtype=out_dtype, device=x.device)
     y2 = _flat(out)
     ys = _rows(y2, "out", N, M)
     _check(lib.conv_matmul_q8_fwd(x2.data_ptr(), xs, x_scale.data_ptr(), w.data_ptr(), ws, w_scale.data_ptr(), _ptr(bias),
                                   y2.data_ptr(), ys, M, N, K, q, _code(_FLOAT, out.dtype, "out"), variant,
-                                  _stream_ptr(dev)), "conv_matmul_q8_fwd")
+                                  _stream_of(gpu)), "conv_matmul_q8_fwd")
     return out
 
 
@@ -177,7 +184,7 @@ def causal_conv1d(x, w, bias=None, activation=None, seq_offsets=None, initial_st
     [slots, taps-1, channels] of x's type, possibly the same tensor.
     """
     lib = load_library()
-    dev = _same_gpu(x, w, bias, seq_offsets, initial_state, final_state, slots, out)
+    gpu = _same_gpu(x, w, bias, seq_offsets, initial_state, final_state, slots, out)
     dt = _code(_FLOAT, x.dtype, "x")
     if activation not in (None, "silu"):
         raise ValueError(f"activation {activation!r}: None or 'silu'")
@@ -190,12 +197,12 @@ def causal_conv1d(x, w, bias=None, activation=None, seq_offsets=None, initial_st
     num = _states(initial_state, final_state, (taps - 1, C), x.dtype, slots, seqs)
     x2 = _flat(x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     y2 = _flat(out)
     ys = _rows(y2, "out", C, tokens, x.dtype)
     _check(lib.conv_causal1d_fwd(x2.data_ptr(), _rows(x2, "x"), w.data_ptr(), _ptr(bias), y2.data_ptr(), ys,
                                  _ptr(seq_offsets), _ptr(initial_state), _ptr(final_state), _ptr(slots), num, tokens,
-                                 seqs, C, taps, activation == "silu", dt, _stream_ptr(dev)), "conv_causal1d_fwd")
+                                 seqs, C, taps, activation == "silu", dt, _stream_of(gpu)), "conv_causal1d_fwd")
     return out
 
 
@@ -212,7 +219,7 @@ def _heads(t, tokens, what, heads=None, width=None, dtype=None):
             (t.stride(-1) != 1 and t.shape[-1] > 1) or (dtype is not None and t.dtype != dtype) or \
             t.numel() != tokens * t.shape[-2] * t.shape[-1]:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, strides {t.stride()}, {t.dtype} do not fit the other tensors")
-    return (ctypes.c_int64 * 2)(st, t.stride(-2))
+    return _Strides(st, t.stride(-2))
 
 
 def gated_delta_rule(q, k, v, g, beta, scale=None, normalize: bool = False, seq_offsets=None, initial_state=None,
@@ -228,7 +235,7 @@ def gated_delta_rule(q, k, v, g, beta, scale=None, normalize: bool = False, seq_
     taken from torch's allocator for the call. Returns o like v.
     """
     lib = load_library()
-    dev = _same_gpu(q, k, v, g, beta, seq_offsets, initial_state, final_state, slots, out, workspace)
+    gpu = _same_gpu(q, k, v, g, beta, seq_offsets, initial_state, final_state, slots, out, workspace)
     dt = _code(_FLOAT, q.dtype, "q")
     tokens, seqs = _sequences(q, 2, seq_offsets)
     Hk, Dk = q.shape[-2:]
@@ -240,18 +247,18 @@ def gated_delta_rule(q, k, v, g, beta, scale=None, normalize: bool = False, seq_
     _vector(beta, tokens * Hv, torch.float32, "beta")
     num = _states(initial_state, final_state, (Hv, Dk, Dv), torch.float32, slots, seqs)
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+        out = torch.empty(v.shape, dtype=v.dtype, device=q.device)
     so = _heads(out, tokens, "out", Hv, Dv, q.dtype)
     if workspace is None:
         need = lib.conv_delta_rule_workspace(tokens, seqs, Hk, Hv, Dk, Dv, dt, variant)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _check(lib.conv_delta_rule_fwd(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
                                    _ptr(seq_offsets), _ptr(initial_state), _ptr(final_state), _ptr(slots), num,
                                    out.data_ptr(), so, _ptr(workspace),
                                    0 if workspace is None else workspace.numel() * workspace.element_size(), tokens, seqs,
                                    Hk, Hv, Dk, Dv, Dk ** -0.5 if scale is None else scale, bool(normalize), dt, variant,
-                                   _stream_ptr(dev)), "conv_delta_rule_fwd")
+                                   _stream_of(gpu)), "conv_delta_rule_fwd")
     return out
 
 
