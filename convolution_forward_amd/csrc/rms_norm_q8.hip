@@ -71,15 +71,25 @@ struct Reduce {
     }
 };
 
+// Writes the row's scale; y * lift * inv is what is rounded. lift is 1, or
+// 2^100 where top is so small that QMAX / top would overflow.
+struct Quant {
+    bool fine;
+    float lift, inv;
+};
+
 template <bool E4M3>
-__device__ __forceinline__ float quant_scale(float sum, uint32_t top_bits, float *scale, bool first, bool &fine)
+__device__ __forceinline__ Quant quant_scale(float sum, uint32_t top_bits, float *scale, bool first)
 {
     constexpr float QMAX = E4M3 ? 448.f : 127.f;
     const float top = __uint_as_float(top_bits);
-    fine = sum < INFINITY && top < INFINITY;
+    Quant q;
+    q.fine = sum < INFINITY && top < INFINITY;
+    q.lift = top < 0x1p-100f ? 0x1p100f : 1.f;
+    q.inv = q.fine && top > 0.f ? QMAX / (top * q.lift) : 0.f;
     if (first)
-        *scale = fine ? top / QMAX : NAN;
-    return fine && top > 0.f ? QMAX / top : 0.f;
+        *scale = q.fine ? top / QMAX : NAN;
+    return q;
 }
 
 template <class T>
@@ -140,15 +150,15 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rms_norm_q8_kernel(
         for (int i = 0; i < NV; ++i)
             r[i] = load_piece(rp + (at + i * 64 * WPR) * V, p.width - (at + i * 64 * WPR) * V);
     }
-    float sum = 0.f;
+    float sum = 0.f, y[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if constexpr (RES)
-                store_from_f32(&h[i].v[j], load_as_f32(&h[i].v[j]) + load_as_f32(&r[i].v[j]));
-            const float v = load_as_f32(&h[i].v[j]);
-            sum = fmaf(v, v, sum);
+                store_rne(&h[i].v[j], load_as_f32(&h[i].v[j]) + load_as_f32(&r[i].v[j]));
+            y[i][j] = load_as_f32(&h[i].v[j]);
+            sum = fmaf(y[i][j], y[i][j], sum);
         }
         if constexpr (RES)
             store_piece(static_cast<T *>(p.h) + row * p.hs + (at + i * 64 * WPR) * V, h[i].v,
@@ -163,18 +173,27 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rms_norm_q8_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            top = max(top, __float_as_uint(fabsf(load_as_f32(&h[i].v[j]) * rinv * load_as_f32(&r[i].v[j]))));
+        for (int j = 0; j < V; ++j) {
+            y[i][j] = y[i][j] * rinv * load_as_f32(&r[i].v[j]);
+            top = max(top, __float_as_uint(fabsf(y[i][j])));
+        }
     top = red.top(top, wave);
-    bool fine;
-    const float inv = quant_scale<E4M3>(sum, top, p.scale + row, at == 0, fine);
+    const Quant z = quant_scale<E4M3>(sum, top, p.scale + row, at == 0);
+    const float inv = z.inv;
     uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.qs;
+    if (z.lift != 1.f)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                y[i][j] *= z.lift;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        uint8_t o[V];
+        uint8_t o[V] __attribute__((aligned(8)));
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            o[j] = fine ? to_eight<E4M3>(load_as_f32(&h[i].v[j]) * rinv * load_as_f32(&r[i].v[j]) * inv) : 0;
+        for (int j = 0; j < V; j += 4)
+            reinterpret_cast<uint32_t *>(o)[j / 4] =
+                z.fine ? to_eight4<E4M3>(y[i][j] * inv, y[i][j + 1] * inv, y[i][j + 2] * inv, y[i][j + 3] * inv) : 0u;
         store_piece(q + (at + i * 64 * WPR) * V, o, p.width - (at + i * 64 * WPR) * V);
     }
 }
@@ -197,7 +216,7 @@ __global__ __launch_bounds__(64 * LONG_WAVES) void rms_norm_q8_long_kernel(NormP
     for (int j = threadIdx.x; j < p.width; j += NT) {
         T t = x[j];
         if (r) {
-            store_from_f32(&t, load_as_f32(&t) + load_as_f32(r + j));
+            store_rne(&t, load_as_f32(&t) + load_as_f32(r + j));
             h[j] = t;
         }
         const float v = load_as_f32(&t);
@@ -210,11 +229,10 @@ __global__ __launch_bounds__(64 * LONG_WAVES) void rms_norm_q8_long_kernel(NormP
     for (int j = threadIdx.x; j < p.width; j += NT)
         top = max(top, __float_as_uint(fabsf(load_as_f32(src + j) * rinv * load_as_f32(w + j))));
     top = red.top(top, wave);
-    bool fine;
-    const float inv = quant_scale<E4M3>(sum, top, p.scale + row, threadIdx.x == 0, fine);
+    const Quant z = quant_scale<E4M3>(sum, top, p.scale + row, threadIdx.x == 0);
     uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.qs;
     for (int j = threadIdx.x; j < p.width; j += NT)
-        q[j] = fine ? to_eight<E4M3>(load_as_f32(src + j) * rinv * load_as_f32(w + j) * inv) : 0;
+        q[j] = z.fine ? (uint8_t)to_eight4<E4M3>(load_as_f32(src + j) * rinv * load_as_f32(w + j) * z.lift * z.inv, 0.f, 0.f, 0.f) : 0;
 }
 
 template <class T, int WPR, int NV, bool E4M3>
@@ -236,7 +254,7 @@ void launch(const NormProblem &p, hipStream_t s)
 {
     constexpr int V = Piece<T>::V;
     const int pieces = (p.width + 64 * V - 1) / (64 * V);       // of one wave
-    if (pieces <= 8 && (p.rows >= 512 || pieces == 1)) {
+    if (pieces <= 8 && (p.rows >= 4096 || pieces == 1)) {
         if (pieces <= 1)
             launch_held<T, 1, 1, E4M3>(p, s);
         else if (pieces <= 2)

@@ -39,6 +39,13 @@ def _same_gpu(first, *others):
     return gpu
 
 
+def _empty(like, shape, dtype):
+    """A new contiguous tensor on `like`'s GPU."""
+    if like.is_contiguous():
+        return torch.empty_like(like, dtype=dtype)
+    return like.new_empty(shape, dtype=dtype)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -94,18 +101,18 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, out_dtype=torch.int
         r2 = _flat(residual)
         rs = _rows(r2, "residual", width, rows, x.dtype)
         if sum_out is None:
-            sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            sum_out = _empty(x, x.shape, x.dtype)
         h2 = _flat(sum_out)
         hs = _rows(h2, "sum_out", width, rows, x.dtype)
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+        out = _empty(x, x.shape, out_dtype)
     q2 = _flat(out)
     qs = _rows(q2, "out", width, rows)
     qdt = _code(_EIGHT, out.dtype, "out")
     if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
     else:
         _vector(scale, rows, torch.float32, "scale")
     _check(lib.conv_rms_norm_q8_fwd(x2.data_ptr(), xs, _ptr(r2), rs, weight.data_ptr(), _ptr(h2), hs, q2.data_ptr(), qs,
@@ -133,7 +140,7 @@ def matmul_q8(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out=N
     _vector(w_scale, N, torch.float32, "w_scale")
     _vector(bias, N, torch.float32, "bias")
     if out is None:
-        out = torch.empty(x.shape[:-1] + (N,), dtype=out_dtype, device=x.device)
+        out = x.new_empty(x.shape[:-1] + (N,), dtype=out_dtype)
     y2 = _flat(out)
     ys = _rows(y2, "out", N, M)
     _check(lib.conv_matmul_q8_fwd(x2.data_ptr(), xs, x_scale.data_ptr(), w.data_ptr(), ws, w_scale.data_ptr(), _ptr(bias),
@@ -197,7 +204,7 @@ def causal_conv1d(x, w, bias=None, activation=None, seq_offsets=None, initial_st
     num = _states(initial_state, final_state, (taps - 1, C), x.dtype, slots, seqs)
     x2 = _flat(x)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _empty(x, x.shape, x.dtype)
     y2 = _flat(out)
     ys = _rows(y2, "out", C, tokens, x.dtype)
     _check(lib.conv_causal1d_fwd(x2.data_ptr(), _rows(x2, "x"), w.data_ptr(), _ptr(bias), y2.data_ptr(), ys,
@@ -247,12 +254,12 @@ def gated_delta_rule(q, k, v, g, beta, scale=None, normalize: bool = False, seq_
     _vector(beta, tokens * Hv, torch.float32, "beta")
     num = _states(initial_state, final_state, (Hv, Dk, Dv), torch.float32, slots, seqs)
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=q.device)
+        out = _empty(v, v.shape, v.dtype)
     so = _heads(out, tokens, "out", Hv, Dv, q.dtype)
     if workspace is None:
         need = lib.conv_delta_rule_workspace(tokens, seqs, Hk, Hv, Dk, Dv, dt, variant)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(need, dtype=torch.uint8)
     _check(lib.conv_delta_rule_fwd(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
                                    _ptr(seq_offsets), _ptr(initial_state), _ptr(final_state), _ptr(slots), num,
                                    out.data_ptr(), so, _ptr(workspace),
