@@ -91,7 +91,7 @@ __device__ __forceinline__ __bf16 part_of(float &x)
 }
 
 template <int DT>
-__global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void delta_prepare_kernel(ChunkArgs a)
 {
     using W = Space<DT>;
     constexpr int D = 64 * DT, PITCH = D + 8, MP = 68;
@@ -101,10 +101,11 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
     __shared__ __align__(16) uint8_t room[2 * ROWS];
     uint16_t *ks = reinterpret_cast<uint16_t *>(room), *qs = reinterpret_cast<uint16_t *>(room + ROWS);
     float *m = reinterpret_cast<float *>(room), *pm = reinterpret_cast<float *>(room + ROWS);
-    __shared__ float z[4][16 * 17];
-    __shared__ double gs[C];
-    __shared__ float rk[C], rq[C], bs[C];
-    __shared__ int badrow[C];
+    // Four 16x16 blocks between the two halves of the last inversion step, in a corner of m that nothing else uses.
+    auto z = [&](int i) { return m + 16 * (i >> 1) * MP + 32 + 16 * (i & 1); };
+    __shared__ __align__(16) double gs[4][C];      // of up to four value heads at a time
+    __shared__ __align__(16) float rk[C], rq[C], bs[4][C];
+    __shared__ int badrow[C], badtok[4];
 
     const int kh = (int)blockIdx.y;
     const SeqTile tile = seq_tile(p.seq, C, (int)blockIdx.x);
@@ -117,50 +118,67 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r = lane & 15;
 
-    // Rows of K and Q, zeros past the sequence's end and past Dk.
+    // Rows of K and Q, zeros past the sequence's end and past Dk. All loads
+    // go out before the first is used.
     if (tid < C)
         badrow[tid] = 0;
-    const int group = p.Hv / p.Hk;
-    float gate = 0.f, beta = 0.f;       // of the head to come, token `lane`
-    auto load_gate = [&](int h) __attribute__((always_inline)) {
-        if (lane < rows) {
-            gate = p.g[(first + lane) * p.Hv + h];
-            beta = p.beta[(first + lane) * p.Hv + h];
-        }
-    };
-    load_gate(kh * group);
     lds_barrier();
+    constexpr int PIECES = C * D / 8 / NT;
+    u32x4 kv[PIECES], qv[PIECES];
+    if (a.vec) {
 #pragma unroll
-    for (int i0 = 0; i0 < C * D / 8; i0 += NT) {
-        const int i = i0 + tid;
-        const int row = i / (D / 8), c = i % (D / 8) * 8;
-        uint16_t kv[8] __attribute__((aligned(16))) = {}, qv[8] __attribute__((aligned(16))) = {};
-        if (row < rows) {
-            const uint16_t *kp = static_cast<const uint16_t *>(p.k) + (first + row) * p.kst + kh * p.ksh + c;
-            const uint16_t *qp = static_cast<const uint16_t *>(p.q) + (first + row) * p.qst + kh * p.qsh + c;
-            if (a.vec && c + 8 <= p.Dk) {
-                *reinterpret_cast<u32x4 *>(kv) = *reinterpret_cast<const u32x4 *>(kp);
-                *reinterpret_cast<u32x4 *>(qv) = *reinterpret_cast<const u32x4 *>(qp);
-            } else {
+        for (int i = 0; i < PIECES; ++i) {
+            const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
+            const int64_t at = first + min(row, rows - 1);
+            const int cc = c < p.Dk ? c : 0;
+            kv[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.k) + at * p.kst + kh * p.ksh + cc);
+            qv[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.q) + at * p.qst + kh * p.qsh + cc);
+        }
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
+            if (row >= rows || c >= p.Dk)
+                kv[i] = qv[i] = u32x4{0, 0, 0, 0};
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < PIECES; ++i) {
+            const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
+            uint16_t k8[8] __attribute__((aligned(16))) = {}, q8[8] __attribute__((aligned(16))) = {};
+            if (row < rows) {
+                const uint16_t *kp = static_cast<const uint16_t *>(p.k) + (first + row) * p.kst + kh * p.ksh + c;
+                const uint16_t *qp = static_cast<const uint16_t *>(p.q) + (first + row) * p.qst + kh * p.qsh + c;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (c + e < p.Dk) {
-                        kv[e] = kp[e];
-                        qv[e] = qp[e];
+                        k8[e] = kp[e];
+                        q8[e] = qp[e];
                     }
             }
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if ((kv[e] & 0x7f80) == 0x7f80) {
-                    kv[e] = 0;
-                    bad = true;
-                }
-            if (bad)
-                badrow[row] = 1;
+            *reinterpret_cast<u32x4 *>(ks + row * PITCH + c) = *reinterpret_cast<const u32x4 *>(k8);
+            *reinterpret_cast<u32x4 *>(qs + row * PITCH + c) = *reinterpret_cast<const u32x4 *>(q8);
         }
-        *reinterpret_cast<u32x4 *>(ks + row * PITCH + c) = *reinterpret_cast<const u32x4 *>(kv);
-        *reinterpret_cast<u32x4 *>(qs + row * PITCH + c) = *reinterpret_cast<const u32x4 *>(qv);
+        // Each thread takes its own pieces back.
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
+            kv[i] = *reinterpret_cast<const u32x4 *>(ks + row * PITCH + c);
+            qv[i] = *reinterpret_cast<const u32x4 *>(qs + row * PITCH + c);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            bad |= (kv[i][e] & 0x7f80u) == 0x7f80u || (kv[i][e] & 0x7f800000u) == 0x7f800000u;
+        if (bad) {
+            kv[i] = u32x4{0, 0, 0, 0};
+            badrow[row] = 1;
+        }
+        *reinterpret_cast<u32x4 *>(ks + row * PITCH + c) = kv[i];
+        *reinterpret_cast<u32x4 *>(qs + row * PITCH + c) = qv[i];
     }
     lds_barrier();
     {   // four threads a row
@@ -241,44 +259,63 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
     lds_barrier();
     for (int i = tid; i < C * MP / 4; i += NT)
         reinterpret_cast<f32x4 *>(m)[i] = reinterpret_cast<f32x4 *>(pm)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int h = kh * group; h < (kh + 1) * group; ++h) {
-        // Sums of the gates, in 64 bits; a total gate counts as exp(-10000) = 0.
-        const bool bad = !(gate < INFINITY) || !(fabsf(beta) < INFINITY) || badrow[lane];
-        if (bad) {
-            gate = gate < INFINITY ? gate : 0.f;
-            beta = 0.f;
-        }
-        const uint64_t bads = __ballot(bad);
-        double G = (double)fmaxf(gate, -1e4f);
-        const float b = beta;
-        if (h + 1 < (kh + 1) * group)
-            load_gate(h + 1);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double o = __shfl_up(G, d);
-            if (lane >= d)
-                G += o;
-        }
-        lds_barrier();
-        if (w == 0) {
-            gs[lane] = G;
-            bs[lane] = b;
-        }
-        lds_barrier();
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j <= w) {
-                const int col = 16 * j + r;
-                const double gc = gs[col];
-                const float rc = rk[col];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 16 * w + 4 * g + e;
-                    const float d = row >= col ? expf((float)(gs[row] - gc)) * rc : 0.f;
-                    m[row * MP + col] = row > col ? bs[row] * rk[row] * d * kk[j][e] : 0.f;
-                    pm[row * MP + col] = row >= col ? rq[row] * d * qk[j][e] : 0.f;
+    const int group = p.Hv / p.Hk;
+    for (int hi = 0; hi < group; ++hi) {
+        const int h = kh * group + hi, hs = hi & 3;
+        if (hs == 0) {
+            // Sums of the gates of the next four heads, a wave each, in 64
+            // bits; a total gate counts as exp(-10000) = 0.
+            lds_barrier();
+            if (hi + w < group) {
+                float gate = 0.f, beta = 0.f;
+                if (lane < rows) {
+                    gate = p.g[(first + lane) * p.Hv + h + w];
+                    beta = p.beta[(first + lane) * p.Hv + h + w];
                 }
+                const bool bad = !(gate < INFINITY) || !(fabsf(beta) < INFINITY) || badrow[lane];
+                const uint64_t bads = __ballot(bad);
+                if (bad) {
+                    gate = gate < INFINITY ? gate : 0.f;
+                    beta = 0.f;
+                }
+                double G = (double)fmaxf(gate, -1e4f);
+#pragma unroll
+                for (int d = 1; d < 64; d <<= 1) {
+                    const double o = __shfl_up(G, d);
+                    if (lane >= d)
+                        G += o;
+                }
+                gs[w][lane] = G;
+                bs[w][lane] = beta;
+                if (lane == 0)
+                    badtok[w] = bads ? __builtin_ctzll(bads) : NEVER;
             }
+        }
+        lds_barrier();
+        {
+            const int row0 = 16 * w + 4 * g;
+            double gr[4];
+            float ar[4], pr[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                gr[e] = gs[hs][row0 + e];
+                ar[e] = bs[hs][row0 + e] * rk[row0 + e];
+                pr[e] = rq[row0 + e];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j <= w) {
+                    const int col = 16 * j + r;
+                    const double gc = gs[hs][col];
+                    const float rc = rk[col];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float d = __expf((float)(gr[e] - gc)) * rc;
+                        m[(row0 + e) * MP + col] = row0 + e > col ? ar[e] * d * kk[j][e] : 0.f;
+                        pm[(row0 + e) * MP + col] = row0 + e >= col ? pr[e] * d * qk[j][e] : 0.f;
+                    }
+                }
+        }
         lds_barrier();
         // (1 + A)^-1: the 16x16 blocks on the diagonal by substitution, lane c
         // a column, then blocks twice as large from
@@ -326,7 +363,7 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
                                                                  m[(16 * k + 4 * e + g) * MP + 16 * j + r], t, 0, 0, 0);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                z[w][(4 * g + e) * 17 + r] = t[e];
+                z(w)[(4 * g + e) * MP + r] = t[e];
             lds_barrier();
 #pragma unroll
             for (int k = 2; k < 4; ++k)
@@ -334,7 +371,7 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         o = __builtin_amdgcn_mfma_f32_16x16x4f32(m[(16 * i + r) * MP + 16 * k + 4 * e + g],
-                                                                 z[2 * (k - 2) + j][(4 * e + g) * 17 + r], o, 0, 0, 0);
+                                                                 z(2 * (k - 2) + j)[(4 * e + g) * MP + r], o, 0, 0, 0);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 m[(16 * i + 4 * g + e) * MP + 16 * j + r] = -o[e];
@@ -350,7 +387,7 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int col = 32 * s + 8 * g + e;
-                    float t = m[row * MP + col] * bs[col];
+                    float t = m[row * MP + col] * bs[hs][col];
                     t3[0][e] = part_of(t);
                     t3[1][e] = part_of(t);
                     t3[2][e] = part_of(t);
@@ -367,14 +404,14 @@ __global__ __launch_bounds__(NT) void delta_prepare_kernel(ChunkArgs a)
                     reinterpret_cast<bf16x8 *>(val + W::P + (2 * f + i) * FRAG)[lane] = p2[i];
             }
         if (w == 0) {
-            const float e = expf((float)G);
-            const double last = gs[C - 1];
+            const double G = gs[hs][lane], last = gs[hs][C - 1];
+            const float e = __expf((float)G);
             reinterpret_cast<float *>(val + W::UPK)[lane] = e * rk[lane];
             reinterpret_cast<float *>(val + W::UPQ)[lane] = e * rq[lane];
-            reinterpret_cast<float *>(val + W::TAIL)[lane] = expf((float)(last - G)) * rk[lane];
+            reinterpret_cast<float *>(val + W::TAIL)[lane] = __expf((float)(last - G)) * rk[lane];
             if (lane == 0) {
-                reinterpret_cast<float *>(val + W::HEAD)[0] = expf((float)last);
-                reinterpret_cast<int *>(val + W::HEAD)[1] = bads ? __builtin_ctzll(bads) : NEVER;
+                reinterpret_cast<float *>(val + W::HEAD)[0] = __expf((float)last);
+                reinterpret_cast<int *>(val + W::HEAD)[1] = badtok[hs];
             }
         }
     }

@@ -47,7 +47,7 @@ __device__ __forceinline__ SeqTile seq_tile(const Sequences &s, int tile, int nu
     // for offsets that start at 0, and is where any others end up).
     const int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
     int lo = 0, count = s.num_seqs;
-    while (count > 1) {
+    while (count > 64) {
         const int step = (count + 63) >> 6;
         const int at = lane * step;
         const bool ok = at < count && seq_begin(s, lo + (at < count ? at : 0)) / tile + lo + at <= number;
@@ -56,10 +56,15 @@ __device__ __forceinline__ SeqTile seq_tile(const Sequences &s, int tile, int nu
         lo += k * step;
         count = min(step, count - k * step);
     }
+    // The last 64: each lane looks at one sequence and at its end.
+    const int mine = lo + (lane < count ? lane : 0);
+    const int begin = (int)seq_begin(s, mine), end = (int)seq_begin(s, mine + 1);
+    const uint64_t yes = __ballot(lane < count && begin / tile + mine <= number);
+    const int k = yes ? 63 - __builtin_clzll(yes) : 0;
     SeqTile t;
-    t.n = __builtin_amdgcn_readfirstlane(lo);
-    t.begin = seq_begin(s, t.n);
-    t.len = seq_begin(s, t.n + 1) - t.begin;
+    t.n = __builtin_amdgcn_readfirstlane(lo + k);
+    t.begin = __builtin_amdgcn_readlane(begin, k);
+    t.len = __builtin_amdgcn_readlane(end, k) - (int)t.begin;
     if (t.len < 0)
         t.len = 0;
     const int first = (int)(t.begin / tile) + t.n;
