@@ -194,9 +194,10 @@ def _dtype_code(t) -> int:
 def _stream_of(gpu: int) -> int:
     """The current stream of a GPU. torch's raw query gives the handle without
     building a Stream object (0.1 us against 1.9)."""
-    torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(gpu) if raw is not None else torch.cuda.current_stream(gpu).cuda_stream
+    try:
+        return _torch()._C._cuda_getCurrentRawStream(gpu)
+    except AttributeError:
+        return _torch().cuda.current_stream(gpu).cuda_stream
 
 
 def _stream_ptr(device) -> int:

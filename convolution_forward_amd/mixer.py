@@ -28,6 +28,10 @@ def _code(table, t, what):
     return code
 
 
+# A call's host time counts where the kernel takes a few microseconds (single tokens), so the checks below ask each
+# tensor as little as they can: one shape, one stride tuple, one data pointer.
+
+
 def _same_gpu(first, *others):
     """The GPU's index, the same for every tensor."""
     gpu = first.get_device()
@@ -40,10 +44,10 @@ def _same_gpu(first, *others):
 
 
 def _empty(like, shape, dtype):
-    """A new contiguous tensor on `like`'s GPU."""
-    if like.is_contiguous():
+    """A new contiguous tensor on `like`'s GPU (empty_like is the cheaper call where it gives just that)."""
+    if like.shape == shape and like.is_contiguous():
         return torch.empty_like(like, dtype=dtype)
-    return like.new_empty(shape, dtype=dtype)
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _ptr(t):
@@ -51,32 +55,38 @@ def _ptr(t):
 
 
 def _vector(t, n, dtype, what):
-    if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+    """Data pointer of a contiguous vector of n values, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} values")
+    return t.data_ptr()
 
 
-def _rows(t, what, width=None, rows=None, dtype=None):
-    """Row stride of a [rows, width] tensor whose channels are adjacent."""
+def _rows(t, what, width, rows=None, dtype=None):
+    """(rows, row stride) of a [..., width] tensor whose channels are adjacent and whose rows are evenly spaced."""
     shape = t.shape
-    if len(shape) == 2 and (width is None or shape[1] == width) and (rows is None or shape[0] == rows) and \
-            (dtype is None or t.dtype == dtype):
-        if t.is_contiguous():
-            return shape[1]
-        if t.stride(1) == 1 or shape[1] == 1:
-            return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
-    raise ValueError(f"{what} must be [{'rows' if rows is None else rows}, {'width' if width is None else width}]"
-                     f"{'' if dtype is None else f' {dtype}'} with adjacent channels, got {tuple(shape)} {t.dtype}"
+    if shape[-1] == width and (dtype is None or t.dtype == dtype):
+        n = 1
+        for size in shape[:-1]:
+            n *= size
+        if rows is None or n == rows:
+            if t.is_contiguous():
+                return n, width
+            strides = t.stride()
+            if strides[-1] == 1 or width == 1:
+                step = 0        # from the innermost axis of more than one row outwards, each must continue the last
+                for size, stride in zip(shape[-2::-1], strides[-2::-1]):
+                    if size == 1:
+                        continue
+                    if step and stride != step * count:
+                        break
+                    step, count = (step or stride), (count * size if step else size)
+                else:
+                    return n, max(step, width) if n <= 1 else step
+    raise ValueError(f"{what} must be [{'rows' if rows is None else rows}, {width}]{'' if dtype is None else f' {dtype}'}"
+                     f" with adjacent channels and evenly spaced rows, got {tuple(shape)} {t.dtype}"
                      f" with strides {t.stride()}")
-
-
-def _flat(t):
-    """[..., channels] as [rows, channels] without a copy."""
-    if t.dim() == 2:
-        return t
-    try:
-        return t.view(-1, t.shape[-1])
-    except RuntimeError as e:
-        raise ValueError(f"rows of shape {tuple(t.shape)}, strides {t.stride()} are not evenly spaced") from e
 
 
 def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, out_dtype=torch.int8, out=None, scale=None, sum_out=None):
@@ -87,37 +97,39 @@ def rms_norm_q8(x, weight, residual=None, eps: float = 1e-6, out_dtype=torch.int
     q like x in 8 bits, scale [...] float32 with q * scale the normed values,
     h = x + residual (None without a residual). sum_out may be x or residual.
     """
-    lib = load_library()
     gpu = _same_gpu(x, weight, residual, out, scale, sum_out)
-    dt = _code(_FLOAT, x.dtype, "x")
-    width = x.shape[-1]
-    x2 = _flat(x)
-    rows = x2.shape[0]
-    xs = _rows(x2, "x")
-    _vector(weight, width, x.dtype, "weight")
+    dtype, shape = x.dtype, x.shape
+    dt = _code(_FLOAT, dtype, "x")
+    width = shape[-1]
+    rows, xs = _rows(x, "x", width)
+    wp = _vector(weight, width, dtype, "weight")
+    rp = hp = None
     rs = hs = 0
-    r2 = h2 = None
     if residual is not None:
-        r2 = _flat(residual)
-        rs = _rows(r2, "residual", width, rows, x.dtype)
+        _, rs = _rows(residual, "residual", width, rows, dtype)
+        rp = residual.data_ptr()
         if sum_out is None:
-            sum_out = _empty(x, x.shape, x.dtype)
-        h2 = _flat(sum_out)
-        hs = _rows(h2, "sum_out", width, rows, x.dtype)
+            sum_out, hs = _empty(x, shape, dtype), width
+        else:
+            _, hs = _rows(sum_out, "sum_out", width, rows, dtype)
+        hp = sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
     if out is None:
-        out = _empty(x, x.shape, out_dtype)
-    q2 = _flat(out)
-    qs = _rows(q2, "out", width, rows)
-    qdt = _code(_EIGHT, out.dtype, "out")
-    if scale is None:
-        scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
+        qdt = _code(_EIGHT, out_dtype, "out_dtype")
+        out, qs = _empty(x, shape, out_dtype), width
     else:
-        _vector(scale, rows, torch.float32, "scale")
-    _check(lib.conv_rms_norm_q8_fwd(x2.data_ptr(), xs, _ptr(r2), rs, weight.data_ptr(), _ptr(h2), hs, q2.data_ptr(), qs,
-                                    scale.data_ptr(), rows, width, eps, dt, qdt, _stream_of(gpu)),
-           "conv_rms_norm_q8_fwd")
+        qdt = _code(_EIGHT, out.dtype, "out")
+        _, qs = _rows(out, "out", width, rows)
+    if scale is None:
+        scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+        sp = scale.data_ptr()
+    else:
+        sp = _vector(scale, rows, torch.float32, "scale")
+    st = load_library().conv_rms_norm_q8_fwd(x.data_ptr(), xs, rp, rs, wp, hp, hs, out.data_ptr(), qs, sp, rows, width,
+                                             eps, dt, qdt, _stream_of(gpu))
+    if st:
+        _check(st, "conv_rms_norm_q8_fwd")
     return out, scale, sum_out
 
 
@@ -128,57 +140,58 @@ def matmul_q8(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out=N
     x_scale [...] and w_scale [N] float32, bias [N] float32; out_dtype
     torch.bfloat16 or torch.float32.
     """
-    lib = load_library()
     gpu = _same_gpu(x, x_scale, w, w_scale, bias, out)
-    q = _code(_EIGHT, x.dtype, "x")
-    x2 = _flat(x)
-    M, K = x2.shape
-    xs = _rows(x2, "x")
-    ws = _rows(w, "w", K, None, x.dtype)
-    N = w.shape[0]
-    _vector(x_scale, M, torch.float32, "x_scale")
-    _vector(w_scale, N, torch.float32, "w_scale")
-    _vector(bias, N, torch.float32, "bias")
+    dtype, shape = x.dtype, x.shape
+    q = _code(_EIGHT, dtype, "x")
+    K = shape[-1]
+    M, xs = _rows(x, "x", K)
+    if w.dim() != 2:
+        raise ValueError(f"w must be [channels, {K}], got {tuple(w.shape)}")
+    N, ws = _rows(w, "w", K, None, dtype)
+    sx = _vector(x_scale, M, torch.float32, "x_scale")
+    sw = _vector(w_scale, N, torch.float32, "w_scale")
+    bp = _vector(bias, N, torch.float32, "bias")
     if out is None:
-        out = x.new_empty(x.shape[:-1] + (N,), dtype=out_dtype)
-    y2 = _flat(out)
-    ys = _rows(y2, "out", N, M)
-    _check(lib.conv_matmul_q8_fwd(x2.data_ptr(), xs, x_scale.data_ptr(), w.data_ptr(), ws, w_scale.data_ptr(), _ptr(bias),
-                                  y2.data_ptr(), ys, M, N, K, q, _code(_FLOAT, out.dtype, "out"), variant,
-                                  _stream_of(gpu)), "conv_matmul_q8_fwd")
+        ydt = _code(_FLOAT, out_dtype, "out_dtype")
+        out, ys = torch.empty(shape[:-1] + (N,), dtype=out_dtype, device=x.device), N
+    else:
+        ydt = _code(_FLOAT, out.dtype, "out")
+        _, ys = _rows(out, "out", N, M)
+    st = load_library().conv_matmul_q8_fwd(x.data_ptr(), xs, sx, w.data_ptr(), ws, sw, bp, out.data_ptr(), ys, M, N, K, q,
+                                           ydt, variant, _stream_of(gpu))
+    if st:
+        _check(st, "conv_matmul_q8_fwd")
     return out
 
 
-def _sequences(t, tail, seq_offsets):
+def _sequences(shape, tail, seq_offsets):
     """(tokens, sequences) of a tensor [batch, length, ...] or [tokens, ...]
     whose last `tail` axes are not tokens."""
-    if t.dim() == tail + 2:
+    dim = len(shape) - tail
+    if dim == 2:
         if seq_offsets is not None:
             raise ValueError("seq_offsets go with [tokens, ...] tensors")
-        return t.shape[0] * t.shape[1], t.shape[0]
-    if t.dim() != tail + 1:
-        raise ValueError(f"expected [batch, length, ...] or [tokens, ...], got {tuple(t.shape)}")
+        return shape[0] * shape[1], shape[0]
+    if dim != 1:
+        raise ValueError(f"expected [batch, length, ...] or [tokens, ...], got {tuple(shape)}")
     if seq_offsets is None:
-        return t.shape[0], 1
-    if seq_offsets.dtype != torch.int32 or seq_offsets.dim() != 1 or seq_offsets.numel() < 2 or \
-            not seq_offsets.is_contiguous():
+        return shape[0], 1
+    n = seq_offsets.numel()
+    if seq_offsets.dtype != torch.int32 or n < 2 or seq_offsets.dim() != 1 or not seq_offsets.is_contiguous():
         raise ValueError("seq_offsets must be a contiguous int32 tensor of num_seqs + 1 values")
-    return t.shape[0], seq_offsets.numel() - 1
+    return shape[0], n - 1
 
 
-def _states(initial, final, shape, dtype, slots, num_seqs):
-    """Slots of the state tensors, [num_slots, *shape]."""
-    num = 0
-    for t in (initial, final):
-        if t is None:
-            continue
-        if t.dtype != dtype or tuple(t.shape[1:]) != shape or not t.is_contiguous():
-            raise ValueError(f"states must be contiguous {dtype} tensors [slots, {', '.join(map(str, shape))}]")
-        if num and t.shape[0] != num:
-            raise ValueError("initial_state and final_state must have as many slots")
-        num = t.shape[0]
-    _vector(slots, num_seqs, torch.int32, "slots")
-    return num
+def _state(t, shape, dtype, num):
+    """Slots of a state tensor [slots, *shape]; `num`, if any, is what another has."""
+    if t is None:
+        return num
+    s = t.shape
+    if t.dtype != dtype or s[1:] != shape or not t.is_contiguous():
+        raise ValueError(f"states must be contiguous {dtype} tensors [slots, {', '.join(map(str, shape))}]")
+    if num and s[0] != num:
+        raise ValueError("initial_state and final_state must have as many slots")
+    return s[0]
 
 
 def causal_conv1d(x, w, bias=None, activation=None, seq_offsets=None, initial_state=None, final_state=None, slots=None,
@@ -190,43 +203,48 @@ def causal_conv1d(x, w, bias=None, activation=None, seq_offsets=None, initial_st
     float32; activation None or "silu". initial_state and final_state
     [slots, taps-1, channels] of x's type, possibly the same tensor.
     """
-    lib = load_library()
     gpu = _same_gpu(x, w, bias, seq_offsets, initial_state, final_state, slots, out)
-    dt = _code(_FLOAT, x.dtype, "x")
-    if activation not in (None, "silu"):
+    dtype, shape = x.dtype, x.shape
+    dt = _code(_FLOAT, dtype, "x")
+    if activation is not None and activation != "silu":
         raise ValueError(f"activation {activation!r}: None or 'silu'")
-    tokens, seqs = _sequences(x, 1, seq_offsets)
-    C = x.shape[-1]
-    if w.dim() != 2 or w.shape[0] != C or w.dtype != x.dtype or not w.is_contiguous():
-        raise ValueError(f"w must be a contiguous [{C}, taps] tensor of {x.dtype}")
-    taps = w.shape[1]
-    _vector(bias, C, torch.float32, "bias")
-    num = _states(initial_state, final_state, (taps - 1, C), x.dtype, slots, seqs)
-    x2 = _flat(x)
+    tokens, seqs = _sequences(shape, 1, seq_offsets)
+    C = shape[-1]
+    ws = w.shape
+    if len(ws) != 2 or ws[0] != C or w.dtype != dtype or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous [{C}, taps] tensor of {dtype}")
+    taps = ws[1]
+    bp = _vector(bias, C, torch.float32, "bias")
+    num = _state(initial_state, (taps - 1, C), dtype, 0)
+    num = _state(final_state, (taps - 1, C), dtype, num)
+    lp = _vector(slots, seqs, torch.int32, "slots")
+    _, xs = _rows(x, "x", C)
     if out is None:
-        out = _empty(x, x.shape, x.dtype)
-    y2 = _flat(out)
-    ys = _rows(y2, "out", C, tokens, x.dtype)
-    _check(lib.conv_causal1d_fwd(x2.data_ptr(), _rows(x2, "x"), w.data_ptr(), _ptr(bias), y2.data_ptr(), ys,
-                                 _ptr(seq_offsets), _ptr(initial_state), _ptr(final_state), _ptr(slots), num, tokens,
-                                 seqs, C, taps, activation == "silu", dt, _stream_of(gpu)), "conv_causal1d_fwd")
+        out, ys = _empty(x, shape, dtype), C
+    else:
+        _, ys = _rows(out, "out", C, tokens, dtype)
+    st = load_library().conv_causal1d_fwd(x.data_ptr(), xs, w.data_ptr(), bp, out.data_ptr(), ys, _ptr(seq_offsets),
+                                          _ptr(initial_state), _ptr(final_state), lp, num, tokens, seqs, C, taps,
+                                          activation is not None, dt, _stream_of(gpu))
+    if st:
+        _check(st, "conv_causal1d_fwd")
     return out
 
 
-def _heads(t, tokens, what, heads=None, width=None, dtype=None):
+def _heads(t, tokens, what, heads, width, dtype):
     """(token, head) strides of [tokens, heads, width], tokens possibly over two axes."""
-    if t.dim() == 4:
-        b, n = t.shape[:2]
-        if b > 1 and n > 1 and t.stride(0) != n * t.stride(1):
-            raise ValueError(f"{what}: batch and length of strides {t.stride()} are not one row of tokens")
-        st = t.stride(1) if n > 1 else t.stride(0)
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 4:
+        b, n = shape[:2]
+        if b > 1 and n > 1 and strides[0] != n * strides[1]:
+            raise ValueError(f"{what}: batch and length of strides {strides} are not one row of tokens")
+        rows, st = b * n, strides[1] if n > 1 else strides[0]
     else:
-        st = t.stride(0)
-    if (heads is not None and t.shape[-2] != heads) or (width is not None and t.shape[-1] != width) or \
-            (t.stride(-1) != 1 and t.shape[-1] > 1) or (dtype is not None and t.dtype != dtype) or \
-            t.numel() != tokens * t.shape[-2] * t.shape[-1]:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, strides {t.stride()}, {t.dtype} do not fit the other tensors")
-    return _Strides(st, t.stride(-2))
+        rows, st = shape[0], strides[0]
+    if len(shape) < 3 or rows != tokens or shape[-2] != heads or shape[-1] != width or t.dtype != dtype or \
+            (strides[-1] != 1 and width > 1):
+        raise ValueError(f"{what}: shape {tuple(shape)}, strides {strides}, {t.dtype} do not fit the other tensors")
+    return _Strides(st, strides[-2])
 
 
 def gated_delta_rule(q, k, v, g, beta, scale=None, normalize: bool = False, seq_offsets=None, initial_state=None,
@@ -243,29 +261,37 @@ def gated_delta_rule(q, k, v, g, beta, scale=None, normalize: bool = False, seq_
     """
     lib = load_library()
     gpu = _same_gpu(q, k, v, g, beta, seq_offsets, initial_state, final_state, slots, out, workspace)
-    dt = _code(_FLOAT, q.dtype, "q")
-    tokens, seqs = _sequences(q, 2, seq_offsets)
-    Hk, Dk = q.shape[-2:]
-    Hv, Dv = v.shape[-2:]
-    sq = _heads(q, tokens, "q")
-    sk = _heads(k, tokens, "k", Hk, Dk, q.dtype)
-    sv = _heads(v, tokens, "v", Hv, Dv, q.dtype)
-    _vector(g, tokens * Hv, torch.float32, "g")
-    _vector(beta, tokens * Hv, torch.float32, "beta")
-    num = _states(initial_state, final_state, (Hv, Dk, Dv), torch.float32, slots, seqs)
+    dtype, shape, vshape = q.dtype, q.shape, v.shape
+    dt = _code(_FLOAT, dtype, "q")
+    tokens, seqs = _sequences(shape, 2, seq_offsets)
+    Hk, Dk = shape[-2], shape[-1]
+    Hv, Dv = vshape[-2], vshape[-1]
+    sq = _heads(q, tokens, "q", Hk, Dk, dtype)
+    sk = _heads(k, tokens, "k", Hk, Dk, dtype)
+    sv = _heads(v, tokens, "v", Hv, Dv, dtype)
+    gp = _vector(g, tokens * Hv, torch.float32, "g")
+    bp = _vector(beta, tokens * Hv, torch.float32, "beta")
+    num = _state(initial_state, (Hv, Dk, Dv), torch.float32, 0)
+    num = _state(final_state, (Hv, Dk, Dv), torch.float32, num)
+    lp = _vector(slots, seqs, torch.int32, "slots")
     if out is None:
-        out = _empty(v, v.shape, v.dtype)
-    so = _heads(out, tokens, "out", Hv, Dv, q.dtype)
-    if workspace is None:
-        need = lib.conv_delta_rule_workspace(tokens, seqs, Hk, Hv, Dk, Dv, dt, variant)
-        if need > 0:
-            workspace = q.new_empty(need, dtype=torch.uint8)
-    _check(lib.conv_delta_rule_fwd(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
-                                   _ptr(seq_offsets), _ptr(initial_state), _ptr(final_state), _ptr(slots), num,
-                                   out.data_ptr(), so, _ptr(workspace),
-                                   0 if workspace is None else workspace.numel() * workspace.element_size(), tokens, seqs,
-                                   Hk, Hv, Dk, Dv, Dk ** -0.5 if scale is None else scale, bool(normalize), dt, variant,
-                                   _stream_of(gpu)), "conv_delta_rule_fwd")
+        out, so = torch.empty(vshape, dtype=dtype, device=v.device), None
+    else:
+        so = _heads(out, tokens, "out", Hv, Dv, dtype)
+    wp, wbytes = None, 0
+    if workspace is not None:
+        wp, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        wbytes = lib.conv_delta_rule_workspace(tokens, seqs, Hk, Hv, Dk, Dv, dt, variant)
+        if wbytes > 0:
+            workspace = torch.empty(wbytes, dtype=torch.uint8, device=q.device)
+            wp = workspace.data_ptr()
+    st = lib.conv_delta_rule_fwd(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, gp, bp, _ptr(seq_offsets),
+                                 _ptr(initial_state), _ptr(final_state), lp, num, out.data_ptr(), so, wp, wbytes, tokens,
+                                 seqs, Hk, Hv, Dk, Dv, Dk ** -0.5 if scale is None else scale, normalize, dt, variant,
+                                 _stream_of(gpu))
+    if st:
+        _check(st, "conv_delta_rule_fwd")
     return out
 
 
