@@ -191,17 +191,8 @@ def _dtype_code(t) -> int:
     raise ValueError(f"unsupported dtype {t}; use float32 or bfloat16")
 
 
-def _stream_of(gpu: int) -> int:
-    """The current stream of a GPU. torch's raw query gives the handle without
-    building a Stream object (0.1 us against 1.9)."""
-    try:
-        return _torch()._C._cuda_getCurrentRawStream(gpu)
-    except AttributeError:
-        return _torch().cuda.current_stream(gpu).cuda_stream
-
-
 def _stream_ptr(device) -> int:
-    return _stream_of(_torch().cuda.current_device() if device.index is None else device.index)
+    return _torch().cuda.current_stream(device).cuda_stream
 
 
 def _require_gpu(*tensors):

@@ -1,4 +1,5 @@
-"""Build libconvfwd.so (the HIP kernels and the C ABI) for gfx950, in-tree.
+"""Build libconvfwd.so (the HIP kernels and the C ABI) for gfx950, and the
+binding of the token-mixer calls (_mixer.so, host code only), in-tree.
 
     python -m convolution_forward_amd.build
 
@@ -19,6 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libconvfwd.so")
+BINDING = os.path.join(PKG, "binding", "mixer_binding.cpp")
+BINDING_PATH = os.path.join(LIB_DIR, "_mixer.so")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -72,6 +75,27 @@ def _compile(src: str, incremental: bool = False) -> str:
     return obj
 
 
+def build_binding(incremental: bool = False) -> str:
+    """Compile the torch binding against the installed torch and link it to libconvfwd.so beside it."""
+    import sysconfig
+    from torch.utils import cpp_extension
+    deps = [BINDING, os.path.abspath(__file__)] + [os.path.join(INCLUDE, h) for h in os.listdir(INCLUDE)]
+    if incremental and os.path.exists(BINDING_PATH) and \
+            all(os.path.getmtime(d) < os.path.getmtime(BINDING_PATH) for d in deps):
+        return BINDING_PATH
+    dirs = cpp_extension.include_paths("cuda") + [sysconfig.get_paths()["include"], INCLUDE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1",
+           "-DUSE_ROCM=1"]
+    cmd += [f"-isystem{d}" for d in dirs[:-1]] + ["-I" + INCLUDE, BINDING, "-o", BINDING_PATH + ".tmp", "-L" + LIB_DIR,
+                                                  "-lconvfwd", "-Wl,-rpath,$ORIGIN"]
+    cmd += [f"-L{d}" for d in cpp_extension.library_paths("cuda")] + ["-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING}:\n{res.stdout}\n{res.stderr}")
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(jobs: int | None = None, verbose: bool = False, incremental: bool = False) -> str:
     """Compile every source (only changed ones with incremental=True) and link."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -86,8 +110,9 @@ def build(jobs: int | None = None, verbose: bool = False, incremental: bool = Fa
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    build_binding(incremental)
     if verbose:
-        print(f"built {LIB_PATH} from {len(srcs)} sources")
+        print(f"built {LIB_PATH} from {len(srcs)} sources, and {BINDING_PATH}")
     return LIB_PATH
 
 
