@@ -75,7 +75,6 @@ struct ChunkArgs {
     DeltaProblem p;
     uint8_t *keys, *vals;       // workspace
     int vec;                    // rows of q and k take 16-byte loads
-    int vec_o;                  // rows of o take 8-byte stores
     int slices;                 // column slices of a head
 };
 
@@ -452,7 +451,10 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_sh
 // of a chunk is the chain's latencies, not its arithmetic, so whatever is not
 // the chain is left to the output waves, and every operand is loaded right
 // after its last use, a chunk ahead.
-template <int DT, int CB>
+// VEC: v's rows of 16 columns are two 16-byte pieces and o's take 8-byte
+// stores (a host rule; as a branch inside, it made the compiler wait for
+// every load at its end).
+template <int DT, int CB, bool VEC>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void delta_chunks_kernel(ChunkArgs a)
 {
     using W = Space<DT>;
@@ -460,7 +462,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     __shared__ f32x4 xp[4][4][CB][64], uo[2][4][CB][64];
     __shared__ bf16x8 ssh[2][4][CB][64];
     __shared__ bf16x4 ysh[3][4][CB][64], ush[3][4][CB][64];
-    __shared__ f32x4 vsh[4][CB][64], upsh[4][64], tailsh[4][64];
+    __shared__ f32x4 vsh[4][CB][64], factors[4][2][4];      // factors: r exp G, then r exp(G_63 - G)
+    __shared__ u32x4 vrows[4][CB][32];                      // V as it lies in memory: 16 tokens of 32 bytes
     __shared__ __align__(16) int badcol[CB * 16];
 
     // Workgroup i runs on XCD i % 8. The slices of one head go to one XCD,
@@ -488,6 +491,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     const int64_t key_step = (int64_t)p.Hk * W::KEY, val_step = (int64_t)p.Hv * W::VAL;
     // Fragment i from a base that is the same for all lanes: such a load needs no vector address arithmetic while
     // i * FRAG fits the instruction's offset (-4096 .. 4095 bytes).
+    // A chunk's header. (A scalar load would be waited for at the next
+    // barrier, which waits for LDS traffic on the same counter.)
+    auto header = [&](int c) __attribute__((always_inline)) {
+        return *reinterpret_cast<const u32x2 *>(val0 + c * val_step + W::HEAD);
+    };
     const uint32_t lane16 = 16 * lane;
     auto frag = [&](const uint8_t *base, int i) __attribute__((always_inline)) {
         return *reinterpret_cast<const bf16x8 *>(base + lane16 + i * FRAG);
@@ -517,11 +525,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
                     for (int i = 0; i < 2; ++i)
                         pf[s][i] = frag(pv, 2 * s + i);
             upq = reinterpret_cast<const float *>(val + W::UPQ)[tokr];
-            bad_here = reinterpret_cast<const int *>(val + W::HEAD)[1];
+            bad_here = (int)header(c)[1];
         };
         // V and the row factors of chain wave w's tokens, on to it through LDS.
         uint16_t v[CB][4];
-        f32x4 upk, tail;
+        u32x4 vpiece[CB];
+        f32x4 factor;
         const uint16_t *vh = static_cast<const uint16_t *>(p.v) + begin * p.vst + h * p.vsh;
         const int64_t voff = tok4 * p.vst;      // of the lane's first token within a chunk
         int vcol[CB];               // columns past the end read the last one's; nothing is stored of them
@@ -529,28 +538,42 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
         for (int cb = 0; cb < CB; ++cb)
             vcol[cb] = min(col0 + 16 * cb + r, p.Dv - 1);
         auto load_v = [&](int c) __attribute__((always_inline)) {
-            const uint8_t *val = val0 + c * val_step;
-            upk = *reinterpret_cast<const f32x4 *>(val + W::UPK + 4 * tok4);
-            tail = *reinterpret_cast<const f32x4 *>(val + W::TAIL + 4 * tok4);
+            factor = *reinterpret_cast<const f32x4 *>(val0 + c * val_step + (r < 8 ? W::UPK : W::TAIL) + 4 * tok4);
             const uint16_t *vc = vh + (int64_t)c * C * p.vst;
             // Tokens past the end read the last one's: T's columns are zero for
             // them. (No branch: the compiler would wait for the loads at its end.)
             const int last = len - 1 - c * C;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t off = tok4 + e <= last ? voff : (last - e) * p.vst;
+            if constexpr (VEC) {        // half a token's 32 bytes a lane
+                const uint16_t *row = vc + min(token_of(w, (lane >> 1) & 15), last) * p.vst + col0 + 8 * (lane & 1);
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb)
-                    v[cb][e] = (vc + e * p.vst + off)[vcol[cb]];
+                    vpiece[cb] = *reinterpret_cast<const u32x4 *>(row + 16 * cb);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t off = tok4 + e <= last ? voff : (last - e) * p.vst;
+#pragma unroll
+                    for (int cb = 0; cb < CB; ++cb)
+                        v[cb][e] = (vc + e * p.vst + off)[vcol[cb]];
+                }
             }
         };
         auto give_v = [&]() __attribute__((always_inline)) {
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
+            for (int cb = 0; cb < CB; ++cb) {
+                if constexpr (VEC) {
+                    if (lane < 32)
+                        vrows[w][cb][lane] = vpiece[cb];
+                    const uint16_t *rows = reinterpret_cast<const uint16_t *>(vrows[w][cb]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[cb][e] = rows[16 * (4 * g + e) + r];
+                }
                 vsh[w][cb][lane] = f32x4{bf16_to_f32(v[cb][0]), bf16_to_f32(v[cb][1]), bf16_to_f32(v[cb][2]),
                                          bf16_to_f32(v[cb][3])};
-            upsh[w][lane] = upk;
-            tailsh[w][lane] = tail;
+            }
+            if ((r & 7) == 0)
+                factors[w][r >> 3][g] = factor;
         };
         if (chunks > 0) {
             load_v(0);
@@ -588,11 +611,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     o[cb][e] = t >= min(badall, bc[e]) ? NAN : o[cb][e];
-                const int left = p.Dv - (col0 + 16 * cb + 4 * g);
                 if (t < len) {
-                    if (a.vec_o && left >= 4) {
+                    if constexpr (VEC) {
                         *reinterpret_cast<bf16x4 *>(oh + 16 * cb) = __builtin_convertvector(o[cb], bf16x4);
                     } else {
+                        const int left = p.Dv - (col0 + 16 * cb + 4 * g);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (e < left)
@@ -683,7 +706,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 ktf[d][s] = frag(key, 2 * d + s);
-        head = *reinterpret_cast<const u32x2 *>(val0 + c * val_step + W::HEAD);
+        head = header(c);
     };
     if (chunks > 0) {
         load_k(0);
@@ -722,7 +745,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 x[i] = xp[i][w][cb][lane];
-            const f32x4 v = vsh[w][cb][lane], up = upsh[w][lane];
+            const f32x4 v = vsh[w][cb][lane], up = factors[w][0][g];
             __builtin_amdgcn_sched_barrier(0);      // all reads before the first sum
             f32x4 y = v - up * ((x[0] + x[1]) + (x[2] + x[3]));
             float zero = 0.f;                       // NaN if anything of y is not finite
@@ -744,7 +767,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
         }
         lds_barrier();
         // Token tile w of U = T Y.
-        const f32x4 tail = tailsh[w][lane];
+        const f32x4 tail = factors[w][1][g];
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
             f32x4 u = {0.f, 0.f, 0.f, 0.f};
@@ -814,14 +837,19 @@ hipError_t launch(const DeltaProblem &p, hipStream_t s)
     a.keys = static_cast<uint8_t *>(p.workspace);
     a.vals = a.keys + numbers * p.Hk * W::KEY;
     a.vec = (((uintptr_t)p.q | (uintptr_t)p.k) % 16 == 0) && ((p.qst | p.qsh | p.kst | p.ksh) % 8 == 0);
-    a.vec_o = ((uintptr_t)p.o % 8 == 0) && ((p.ost | p.osh) % 4 == 0);
+    const bool vec = (uintptr_t)p.v % 16 == 0 && (p.vst | p.vsh) % 8 == 0 && p.Dv % 16 == 0 && (uintptr_t)p.o % 8 == 0 &&
+                     (p.ost | p.osh) % 4 == 0;
     hipLaunchKernelGGL(delta_prepare_kernel<DT>, dim3((unsigned)numbers, (unsigned)p.Hk), dim3(NT), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
     a.slices = (p.Dv + 15) / 16;
     const int64_t heads = ((int64_t)p.seq.num_seqs * p.Hv + 7) / 8 * 8;
-    hipLaunchKernelGGL((delta_chunks_kernel<DT, 1>), dim3((unsigned)(heads * a.slices)), dim3(512), 0, s, a);
+    const dim3 grid((unsigned)(heads * a.slices)), block(512);
+    if (vec)
+        hipLaunchKernelGGL((delta_chunks_kernel<DT, 1, true>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((delta_chunks_kernel<DT, 1, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
