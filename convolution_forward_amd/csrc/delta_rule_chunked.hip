@@ -446,11 +446,11 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_sh
 //   chain wave w: token tile w of Y in three parts                    -> ysh
 //   chain wave w: token tile w of U, for S' in three parts and for O  -> ush; uo
 // then chain wave w updates its rows of S. Output wave w takes Q S between the
-// first two barriers, adds P U of the chunk before between the second and the
-// third, and stores that and brings V and the row factors after it. The time
-// of a chunk is the chain's latencies, not its arithmetic, so whatever is not
-// the chain is left to the output waves, and every operand is loaded right
-// after its last use, a chunk ahead.
+// first two barriers, stores the chunk before between the second and the
+// third, and after it brings V and the row factors of the next chunk and adds
+// P U. The time of a chunk is the chain's latencies, not its arithmetic, so
+// whatever is not the chain is left to the output waves, and every operand is
+// loaded right after its last use, a chunk ahead.
 // VEC: v's rows of 16 columns are two 16-byte pieces and o's take 8-byte
 // stores (a host rule; as a branch inside, it made the compiler wait for
 // every load at its end).
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 {
     using W = Space<DT>;
     const DeltaProblem &p = a.p;
-    __shared__ f32x4 xp[4][4][CB][64], uo[2][4][CB][64];
+    __shared__ f32x4 xp[4][4][CB][64], uo[4][CB][64];
     __shared__ bf16x8 ssh[2][4][CB][64];
     __shared__ bf16x4 ysh[3][4][CB][64], ush[3][4][CB][64];
     __shared__ f32x4 vsh[4][CB][64], factors[4][2][4];      // factors: r exp G, then r exp(G_63 - G)
@@ -476,7 +476,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     const int n = nh / p.Hv, h = nh % p.Hv, kh = h / (p.Hv / p.Hk);
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int w8 = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int w = w8 & 3;
+    // Token tiles 2 and 3 have twice the work of 0 and 1, in both roles: the
+    // output wave of a SIMD takes the other half's tile.
+    const int w = w8 < 4 ? w8 : 7 - w8;
     const int64_t begin = seq_begin(p.seq, n);
     const int64_t end = seq_begin(p.seq, n + 1);
     const int len = end > begin ? (int)(end - begin) : 0;
@@ -491,11 +493,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     const int64_t key_step = (int64_t)p.Hk * W::KEY, val_step = (int64_t)p.Hv * W::VAL;
     // Fragment i from a base that is the same for all lanes: such a load needs no vector address arithmetic while
     // i * FRAG fits the instruction's offset (-4096 .. 4095 bytes).
-    // A chunk's header. (A scalar load would be waited for at the next
-    // barrier, which waits for LDS traffic on the same counter.)
-    auto header = [&](int c) __attribute__((always_inline)) {
-        return *reinterpret_cast<const u32x2 *>(val0 + c * val_step + W::HEAD);
-    };
     const uint32_t lane16 = 16 * lane;
     auto frag = [&](const uint8_t *base, int i) __attribute__((always_inline)) {
         return *reinterpret_cast<const bf16x8 *>(base + lane16 + i * FRAG);
@@ -520,12 +517,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
             const uint8_t *val = val0 + c * val_step, *pv = val + W::P + 2 * low_frag(w, 0) * FRAG;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                if (2 * s <= w)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        pf[s][i] = frag(pv, 2 * s + i);
+                for (int i = 0; i < 2; ++i)
+                    pf[s][i] = frag(pv, 2 * s + i);     // s = 1 of waves 0 and 1: the next wave's, not used
             upq = reinterpret_cast<const float *>(val + W::UPQ)[tokr];
-            bad_here = (int)header(c)[1];
+            bad_here = reinterpret_cast<const int *>(val + W::HEAD)[1];
         };
         // V and the row factors of chain wave w's tokens, on to it through LDS.
         uint16_t v[CB][4];
@@ -580,11 +576,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
             give_v();
             load_v(min(1, chunks - 1));
             load_q(0);
+            load_p(0);
         }
         uint16_t *oh = static_cast<uint16_t *>(p.o) + (begin + tokr) * p.ost + h * p.osh + col0 + 4 * g;
         f32x4 o[CB];
         // The second term of chunk c's outputs, U in two parts.
         auto add_pu = [&](int c) __attribute__((always_inline)) {
+            // Nothing that looks at these two may move up to their load, a
+            // phase earlier: it would wait there.
+            asm volatile("" : "+v"(bad_here), "+v"(upq));
             if (badall == NEVER && bad_here != NEVER)
                 badall = c * C + bad_here;
 #pragma unroll
@@ -594,8 +594,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
                 for (int s = 0; s < 2; ++s)
                     if (2 * s <= w) {
                         bf16x4 lo[2], hi[2];
-                        split<2>(uo[c & 1][2 * s][cb][lane], lo);
-                        split<2>(uo[c & 1][2 * s + 1][cb][lane], hi);
+                        split<2>(uo[2 * s][cb][lane], lo);
+                        split<2>(uo[2 * s + 1][cb][lane], hi);
                         const bf16x8 u0 = join(lo[0], hi[0]), u1 = join(lo[1], hi[1]);
                         o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u1, pf[s][0], o[cb], 0, 0, 0);
                         o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][1], o[cb], 0, 0, 0);
@@ -640,25 +640,21 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
             }
             load_q(min(c + 1, chunks - 1));
             lds_barrier();
-            // While the chain works on U, the chunk before gets its second term.
-            if (c > 0)
-                add_pu(c - 1);
-            load_p(c);
-            lds_barrier();
-            // For the next chunk: the chain reads them between the next two
-            // barriers, and took its last look at this chunk's before the one above.
-            give_v();
-            load_v(min(c + 2, chunks - 1));
             if (c > 0)
                 store(c - 1);
 #pragma unroll
             for (int cb = 0; cb < CB; ++cb)
                 o[cb] = q[cb];
+            lds_barrier();
+            // For the next chunk: the chain reads them between the next two
+            // barriers, and took its last look at this chunk's before the one above.
+            give_v();
+            load_v(min(c + 2, chunks - 1));
+            add_pu(c);
+            load_p(min(c + 1, chunks - 1));
         }
-        if (chunks > 0) {
-            add_pu(chunks - 1);
+        if (chunks > 0)
             store(chunks - 1);
-        }
         return;
     }
 
@@ -706,7 +702,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 ktf[d][s] = frag(key, 2 * d + s);
-        head = header(c);
+        // (A scalar load would be waited for at the next barrier, which waits
+        // for LDS traffic on the same counter.)
+        head = *reinterpret_cast<const u32x2 *>(val0 + c * val_step + W::HEAD);
     };
     if (chunks > 0) {
         load_k(0);
@@ -784,7 +782,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
                         for (int i = 0; i <= k; ++i)
                             u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tf[s][i], y[k - i], u, 0, 0, 0);
                 }
-            uo[c & 1][w][cb][lane] = u;
+            uo[w][cb][lane] = u;
             bf16x4 us[3];
             split<3>(u * tail, us);
 #pragma unroll
