@@ -16,7 +16,7 @@
 // what does not depend on S: T = (1 + A)^-1 diag(beta), P, the row factors,
 // and K, Q and K^T, all in the order in which the second one's matrix
 // instructions take them. The second carries S along each sequence. Columns
-// of S are independent, so a workgroup takes 16 CB of them; four of its waves
+// of S are independent, so a workgroup takes 16 of them; four of its waves
 // share the rows.
 //
 // Precision: bf16 operands (K, Q) are exact, every other operand of a product
@@ -454,17 +454,17 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_sh
 // VEC: v's rows of 16 columns are two 16-byte pieces and o's take 8-byte
 // stores (a host rule; as a branch inside, it made the compiler wait for
 // every load at its end).
-template <int DT, int CB, bool VEC>
+template <int DT, bool VEC>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void delta_chunks_kernel(ChunkArgs a)
 {
     using W = Space<DT>;
     const DeltaProblem &p = a.p;
-    __shared__ f32x4 xp[4][4][CB][64], uo[4][CB][64];
-    __shared__ bf16x8 ssh[2][4][CB][64];
-    __shared__ bf16x4 ysh[3][4][CB][64], ush[3][4][CB][64];
-    __shared__ f32x4 vsh[4][CB][64], factors[4][2][4];      // factors: r exp G, then r exp(G_63 - G)
-    __shared__ u32x4 vrows[4][CB][32];                      // V as it lies in memory: 16 tokens of 32 bytes
-    __shared__ __align__(16) int badcol[CB * 16];
+    __shared__ f32x4 xp[4][4][64], uo[4][64];
+    __shared__ bf16x8 ssh[2][4][64];
+    __shared__ bf16x4 ysh[3][4][64], ush[3][4][64];
+    __shared__ f32x4 vsh[4][64], factors[4][2][4];  // factors: r exp G, then r exp(G_63 - G)
+    __shared__ u32x4 vrows[4][32];                  // V as it lies in memory: 16 tokens of 32 bytes
+    __shared__ __align__(16) int badcol[16];
 
     // Workgroup i runs on XCD i % 8. The slices of one head go to one XCD,
     // where they meet in its L2; the heads of a sequence, as long as each
@@ -485,7 +485,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     const int chunks = (len + C - 1) / C;
     const int64_t number = begin / C + n;
     const int slot = p.state_in || p.state_out ? seq_slot(p.seq, n) : -1;
-    const int col0 = slice * 16 * CB;
+    const int col0 = slice * 16;
     const int tok4 = 32 * (w >> 1) + 8 * g + 4 * (w & 1);      // first of the lane's four tokens of tile w
     const int tokr = token_of(w, r);
     const uint8_t *key0 = a.keys + (number * p.Hk + kh) * W::KEY;
@@ -498,7 +498,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
         return *reinterpret_cast<const bf16x8 *>(base + lane16 + i * FRAG);
     };
 
-    if (threadIdx.x < CB * 16)
+    if (threadIdx.x < 16)
         badcol[threadIdx.x] = NEVER;
     __syncthreads();
 
@@ -524,15 +524,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
             bad_here = reinterpret_cast<const int *>(val + W::HEAD)[1];
         };
         // V and the row factors of chain wave w's tokens, on to it through LDS.
-        uint16_t v[CB][4];
-        u32x4 vpiece[CB];
+        uint16_t v[4];
+        u32x4 vpiece;
         f32x4 factor;
         const uint16_t *vh = static_cast<const uint16_t *>(p.v) + begin * p.vst + h * p.vsh;
         const int64_t voff = tok4 * p.vst;      // of the lane's first token within a chunk
-        int vcol[CB];               // columns past the end read the last one's; nothing is stored of them
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-            vcol[cb] = min(col0 + 16 * cb + r, p.Dv - 1);
+        const int vcol = min(col0 + r, p.Dv - 1);   // columns past the end read the last one's; nothing is stored of them
         auto load_v = [&](int c) __attribute__((always_inline)) {
             factor = *reinterpret_cast<const f32x4 *>(val0 + c * val_step + (r < 8 ? W::UPK : W::TAIL) + 4 * tok4);
             const uint16_t *vc = vh + (int64_t)c * C * p.vst;
@@ -541,33 +538,25 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
             const int last = len - 1 - c * C;
             if constexpr (VEC) {        // half a token's 32 bytes a lane
                 const uint16_t *row = vc + min(token_of(w, (lane >> 1) & 15), last) * p.vst + col0 + 8 * (lane & 1);
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb)
-                    vpiece[cb] = *reinterpret_cast<const u32x4 *>(row + 16 * cb);
+                vpiece = *reinterpret_cast<const u32x4 *>(row);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int64_t off = tok4 + e <= last ? voff : (last - e) * p.vst;
-#pragma unroll
-                    for (int cb = 0; cb < CB; ++cb)
-                        v[cb][e] = (vc + e * p.vst + off)[vcol[cb]];
+                    v[e] = (vc + e * p.vst + off)[vcol];
                 }
             }
         };
         auto give_v = [&]() __attribute__((always_inline)) {
+            if constexpr (VEC) {
+                if (lane < 32)
+                    vrows[w][lane] = vpiece;
+                const uint16_t *rows = reinterpret_cast<const uint16_t *>(vrows[w]);
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb) {
-                if constexpr (VEC) {
-                    if (lane < 32)
-                        vrows[w][cb][lane] = vpiece[cb];
-                    const uint16_t *rows = reinterpret_cast<const uint16_t *>(vrows[w][cb]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[cb][e] = rows[16 * (4 * g + e) + r];
-                }
-                vsh[w][cb][lane] = f32x4{bf16_to_f32(v[cb][0]), bf16_to_f32(v[cb][1]), bf16_to_f32(v[cb][2]),
-                                         bf16_to_f32(v[cb][3])};
+                for (int e = 0; e < 4; ++e)
+                    v[e] = rows[16 * (4 * g + e) + r];
             }
+            vsh[w][lane] = f32x4{bf16_to_f32(v[0]), bf16_to_f32(v[1]), bf16_to_f32(v[2]), bf16_to_f32(v[3])};
             if ((r & 7) == 0)
                 factors[w][r >> 3][g] = factor;
         };
@@ -579,7 +568,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
             load_p(0);
         }
         uint16_t *oh = static_cast<uint16_t *>(p.o) + (begin + tokr) * p.ost + h * p.osh + col0 + 4 * g;
-        f32x4 o[CB];
+        f32x4 o;
         // The second term of chunk c's outputs, U in two parts.
         auto add_pu = [&](int c) __attribute__((always_inline)) {
             // Nothing that looks at these two may move up to their load, a
@@ -587,40 +576,34 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
             asm volatile("" : "+v"(bad_here), "+v"(upq));
             if (badall == NEVER && bad_here != NEVER)
                 badall = c * C + bad_here;
+            o *= upq;
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb) {
-                o[cb] *= upq;
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    if (2 * s <= w) {
-                        bf16x4 lo[2], hi[2];
-                        split<2>(uo[2 * s][cb][lane], lo);
-                        split<2>(uo[2 * s + 1][cb][lane], hi);
-                        const bf16x8 u0 = join(lo[0], hi[0]), u1 = join(lo[1], hi[1]);
-                        o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u1, pf[s][0], o[cb], 0, 0, 0);
-                        o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][1], o[cb], 0, 0, 0);
-                        o[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][0], o[cb], 0, 0, 0);
-                    }
-            }
+            for (int s = 0; s < 2; ++s)
+                if (2 * s <= w) {
+                    bf16x4 lo[2], hi[2];
+                    split<2>(uo[2 * s][lane], lo);
+                    split<2>(uo[2 * s + 1][lane], hi);
+                    const bf16x8 u0 = join(lo[0], hi[0]), u1 = join(lo[1], hi[1]);
+                    o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u1, pf[s][0], o, 0, 0, 0);
+                    o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][1], o, 0, 0, 0);
+                    o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][0], o, 0, 0, 0);
+                }
         };
         auto store = [&](int c) __attribute__((always_inline)) {
             const int t = c * C + tokr;
+            const i32x4 bc = *reinterpret_cast<const i32x4 *>(badcol + 4 * g);
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb) {
-                const i32x4 bc = *reinterpret_cast<const i32x4 *>(badcol + 16 * cb + 4 * g);
+            for (int e = 0; e < 4; ++e)
+                o[e] = t >= min(badall, bc[e]) ? NAN : o[e];
+            if (t < len) {
+                if constexpr (VEC) {
+                    *reinterpret_cast<bf16x4 *>(oh) = __builtin_convertvector(o, bf16x4);
+                } else {
+                    const int left = p.Dv - (col0 + 4 * g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[cb][e] = t >= min(badall, bc[e]) ? NAN : o[cb][e];
-                if (t < len) {
-                    if constexpr (VEC) {
-                        *reinterpret_cast<bf16x4 *>(oh + 16 * cb) = __builtin_convertvector(o[cb], bf16x4);
-                    } else {
-                        const int left = p.Dv - (col0 + 16 * cb + 4 * g);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (e < left)
-                                oh[16 * cb + e] = f32_to_bf16_rne(o[cb][e]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left)
+                            oh[e] = f32_to_bf16_rne(o[e]);
                 }
             }
             oh += C * p.ost;
@@ -628,23 +611,17 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
         for (int c = 0; c < chunks; ++c) {
             lds_barrier();
             // S^T Q^T, every wave's rows of S.
-            f32x4 q[CB];
+            f32x4 q = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb) {
-                q[cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 1; j >= 0; --j)
-                        q[cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ssh[j][i][cb][lane], qf[i], q[cb], 0, 0, 0);
-            }
+                for (int j = 1; j >= 0; --j)
+                    q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ssh[j][i][lane], qf[i], q, 0, 0, 0);
             load_q(min(c + 1, chunks - 1));
             lds_barrier();
             if (c > 0)
                 store(c - 1);
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
-                o[cb] = q[cb];
+            o = q;
             lds_barrier();
             // For the next chunk: the chain reads them between the next two
             // barriers, and took its last look at this chunk's before the one above.
@@ -662,20 +639,18 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     // (row dk_of(d) + e, column r of each 16).
     const int64_t sat = ((int64_t)slot * p.Hv + h) * p.Dk * p.Dv;
     auto dk_of = [&](int d) { return DT == 2 ? 32 * w + 8 * g + 4 * d : 16 * w + 4 * g; };
-    f32x4 S[DT][CB];
+    f32x4 S[DT];
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // All loads at once: what is past the state reads its last row and column.
-                const int dk = dk_of(d) + e, col = col0 + 16 * cb + r;
-                float v = 0.f;
-                if (p.state_in && slot >= 0)
-                    v = p.state_in[sat + (int64_t)min(dk, p.Dk - 1) * p.Dv + min(col, p.Dv - 1)];
-                S[d][cb][e] = dk < p.Dk && col < p.Dv ? v : 0.f;
-            }
+        for (int e = 0; e < 4; ++e) {
+            // All loads at once: what is past the state reads its last row and column.
+            const int dk = dk_of(d) + e, col = col0 + r;
+            float v = 0.f;
+            if (p.state_in && slot >= 0)
+                v = p.state_in[sat + (int64_t)min(dk, p.Dk - 1) * p.Dv + min(col, p.Dv - 1)];
+            S[d][e] = dk < p.Dk && col < p.Dv ? v : 0.f;
+        }
 
     bf16x8 kf[4], ktf[DT][2], tf[2][3];
     u32x2 head = {0, 0};
@@ -715,99 +690,87 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     for (int c = 0; c < chunks; ++c) {
         const int next = min(c + 1, chunks - 1);
         // K S, wave w's rows of S only.
+        bf16x4 lo[3], hi[3] = {};
+        split<3>(S[0], lo);
+        if constexpr (DT == 2)
+            split<3>(S[DT - 1], hi);
+        f32x4 acc[4] = {};
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-            bf16x4 lo[3], hi[3] = {};
-            split<3>(S[0][cb], lo);
-            if constexpr (DT == 2)
-                split<3>(S[DT - 1][cb], hi);
-            f32x4 acc[4] = {};
-#pragma unroll
-            for (int j = 2; j >= 0; --j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], join(lo[j], hi[j]), acc[i], 0, 0, 0);
+        for (int j = 2; j >= 0; --j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                xp[w][i][cb][lane] = acc[i];
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], join(lo[j], hi[j]), acc[i], 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                ssh[j][w][cb][lane] = join(lo[j], hi[j]);
-        }
+        for (int i = 0; i < 4; ++i)
+            xp[w][i][lane] = acc[i];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            ssh[j][w][lane] = join(lo[j], hi[j]);
         load_k(next);
         lds_barrier();
         // Token tile w of Y = V - diag(r exp G) K S.
+        f32x4 x[4];
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-            f32x4 x[4];
+        for (int i = 0; i < 4; ++i)
+            x[i] = xp[i][w][lane];
+        const f32x4 v = vsh[w][lane], up = factors[w][0][g];
+        __builtin_amdgcn_sched_barrier(0);      // all reads before the first sum
+        f32x4 y = v - up * ((x[0] + x[1]) + (x[2] + x[3]));
+        float zero = 0.f;                       // NaN if anything of y is not finite
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = xp[i][w][cb][lane];
-            const f32x4 v = vsh[w][cb][lane], up = factors[w][0][g];
-            __builtin_amdgcn_sched_barrier(0);      // all reads before the first sum
-            f32x4 y = v - up * ((x[0] + x[1]) + (x[2] + x[3]));
-            float zero = 0.f;                       // NaN if anything of y is not finite
+        for (int e = 0; e < 4; ++e)
+            zero = fmaf(y[e], 0.f, zero);
+        if (__any(zero != 0.f))
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                zero = fmaf(y[e], 0.f, zero);
-            if (__any(zero != 0.f))
+                if (!(fabsf(y[e]) < INFINITY)) {
+                    atomicMin(&badcol[r], c * C + tok4 + e);
+                    y[e] = 0.f;
+                }
+        bf16x4 part[3];
+        split<3>(y, part);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!(fabsf(y[e]) < INFINITY)) {
-                        atomicMin(&badcol[16 * cb + r], c * C + tok4 + e);
-                        y[e] = 0.f;
-                    }
-            bf16x4 part[3];
-            split<3>(y, part);
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                ysh[i][w][cb][lane] = part[i];
-        }
+        for (int i = 0; i < 3; ++i)
+            ysh[i][w][lane] = part[i];
         lds_barrier();
         // Token tile w of U = T Y.
         const f32x4 tail = factors[w][1][g];
+        f32x4 u = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-            f32x4 u = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < 2; ++s)
+            if (2 * s <= w) {
+                bf16x8 y[3];
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (2 * s <= w) {
-                    bf16x8 y[3];
+                for (int i = 0; i < 3; ++i)
+                    y[i] = join(ysh[i][2 * s][lane], ysh[i][2 * s + 1][lane]);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        y[i] = join(ysh[i][2 * s][cb][lane], ysh[i][2 * s + 1][cb][lane]);
+                for (int k = 2; k >= 0; --k)
 #pragma unroll
-                    for (int k = 2; k >= 0; --k)
+                    for (int i = 0; i <= k; ++i)
+                        u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tf[s][i], y[k - i], u, 0, 0, 0);
+            }
+        uo[w][lane] = u;
+        bf16x4 us[3];
+        split<3>(u * tail, us);
 #pragma unroll
-                        for (int i = 0; i <= k; ++i)
-                            u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tf[s][i], y[k - i], u, 0, 0, 0);
-                }
-            uo[w][cb][lane] = u;
-            bf16x4 us[3];
-            split<3>(u * tail, us);
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                ush[i][w][cb][lane] = us[i];
-        }
+        for (int i = 0; i < 3; ++i)
+            ush[i][w][lane] = us[i];
         load_t(next);
         lds_barrier();
         // S'.
         bad_any |= (int)head[1] != NEVER;
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
+        for (int d = 0; d < DT; ++d)
+            S[d] *= __uint_as_float(head[0]);
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
-                S[d][cb] *= __uint_as_float(head[0]);
+        for (int i = 2; i >= 0; --i)
 #pragma unroll
-            for (int i = 2; i >= 0; --i)
+            for (int s = 0; s < 2; ++s) {
+                const bf16x8 u = join(ush[i][2 * s][lane], ush[i][2 * s + 1][lane]);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const bf16x8 u = join(ush[i][2 * s][cb][lane], ush[i][2 * s + 1][cb][lane]);
-#pragma unroll
-                    for (int d = 0; d < DT; ++d)
-                        S[d][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ktf[d][s], u, S[d][cb], 0, 0, 0);
-                }
-        }
+                for (int d = 0; d < DT; ++d)
+                    S[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ktf[d][s], u, S[d], 0, 0, 0);
+            }
         load_kt(next);
     }
     if (!p.state_out || slot < 0)
@@ -815,14 +778,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int dk = dk_of(d) + e, col = col0 + 16 * cb + r;
-                const bool bad = bad_any || badcol[16 * cb + r] != NEVER;
-                if (dk < p.Dk && col < p.Dv)
-                    p.state_out[sat + (int64_t)dk * p.Dv + col] = bad ? NAN : S[d][cb][e];
-            }
+        for (int e = 0; e < 4; ++e) {
+            const int dk = dk_of(d) + e, col = col0 + r;
+            const bool bad = bad_any || badcol[r] != NEVER;
+            if (dk < p.Dk && col < p.Dv)
+                p.state_out[sat + (int64_t)dk * p.Dv + col] = bad ? NAN : S[d][e];
+        }
 }
 
 template <int DT>
@@ -845,9 +806,9 @@ hipError_t launch(const DeltaProblem &p, hipStream_t s)
     const int64_t heads = ((int64_t)p.seq.num_seqs * p.Hv + 7) / 8 * 8;
     const dim3 grid((unsigned)(heads * a.slices)), block(512);
     if (vec)
-        hipLaunchKernelGGL((delta_chunks_kernel<DT, 1, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((delta_chunks_kernel<DT, true>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((delta_chunks_kernel<DT, 1, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((delta_chunks_kernel<DT, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
