@@ -8,8 +8,12 @@
 // A workgroup takes TT tokens of one sequence (tiles never cross sequences)
 // and 256 channel vectors; a thread slides the taps-1 previous rows of its
 // channels along the tile in registers, so each row is read once plus taps-1
-// rows a tile. The first tile of a sequence also writes the sequence's state,
-// after it has read the old one: the two may be the same memory.
+// rows a tile. The bytes are the time: 8192 tokens of 8192 channels, bf16, 4
+// taps, 59-66 us, 4.1-4.6 TB/s (tiles of 32 tokens read 9 % twice; eight rows
+// in flight a thread; one at a time took 81 us). 64 sequences of one token: 7.2 us, the
+// latency of offsets, slot, state and x one after the other. The first tile of
+// a sequence also writes the sequence's state, after it has read the old one:
+// the two may be the same memory.
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"

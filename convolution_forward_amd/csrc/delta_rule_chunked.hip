@@ -13,11 +13,20 @@
 // in 64 bits, so a strong gate early in a chunk costs the later ones nothing.
 //
 // Two kernels. The first takes every chunk and key head at once and writes
-// what does not depend on S: T = (1 + A)^-1 diag(beta), P, the row factors,
-// and K, Q and K^T, all in the order in which the second one's matrix
-// instructions take them. The second carries S along each sequence. Columns
-// of S are independent, so a workgroup takes 16 of them; four of its waves
-// share the rows.
+// what does not depend on S: T = (1 + A)^-1 diag(beta), P, the row factors, and
+// K and Q, all in the order in which the second one's matrix instructions take
+// them. (K and Q read where they are, 64-byte pieces of 16 rows an instruction,
+// cost the second kernel more than the copy costs the first: six prompts of
+// 4096 tokens, 98 -> 117 us and 36 -> 34.) The second carries S along each
+// sequence. Columns of S are independent, so a workgroup takes 16 of them; four
+// of its waves share the rows. (32 columns halve the loads a column, and the
+// workgroups: no faster, 103 us for the six prompts.)
+//
+// 16384 tokens of one prompt, 16 key and 32 value heads of 128 x 128: the first
+// 124 us, 0.52 GB at 4.2 TB/s; the second 430 us, 256 chunks of 1.7 us each, one
+// workgroup a compute unit. There the chain of exchanges is the time (matrix
+// instructions: a fifth of it). With two workgroups a compute unit a chunk of
+// both takes 2.7 us, the loads' and LDS's paths half busy each.
 //
 // Precision: bf16 operands (K, Q) are exact, every other operand of a product
 // is split into bf16 parts x = hi + mid + lo (each the nearest bf16 of what is
@@ -56,14 +65,14 @@ __device__ __forceinline__ int token_of(int i, int r) { return 32 * (i >> 1) + 8
 
 // ---- Workspace ---------------------------------------------------------------
 // For each chunk number and key head: K (wave, tile) and Q (tile, wave), 4 x 4
-// fragments each, K^T, 4 waves x DT x 2. For each chunk number and value head: T, 3
-// parts of the 6 fragments that are not all zero, P, 2 parts of them, then 4
-// x 64 row factors and a header. A fragment is 64 lanes x 16 bytes.
+// fragments each. For each chunk number and value head: T, 3 parts of the 6
+// fragments that are not all zero, P, 2 parts of them, then 4 x 64 row factors
+// and a header. A fragment is 64 lanes x 16 bytes.
 constexpr int FRAG = 1024;
 
 template <int DT>
 struct Space {
-    static constexpr int Q = 16 * FRAG, KT = 32 * FRAG, KEY = KT + 8 * DT * FRAG;
+    static constexpr int Q = 16 * FRAG, KEY = 32 * FRAG;
     static constexpr int P = 18 * FRAG, UPK = 30 * FRAG, UPQ = UPK + 256, TAIL = UPQ + 256, HEAD = TAIL + 256;
     static constexpr int VAL = 31 * FRAG;       // HEAD: exp(G_63), first token that is not finite
 };
@@ -75,6 +84,7 @@ struct ChunkArgs {
     DeltaProblem p;
     uint8_t *keys, *vals;       // workspace
     int vec;                    // rows of q and k take 16-byte loads
+    int heads;                  // value heads of a key head that a workgroup of the first kernel takes
     int slices;                 // column slices of a head
 };
 
@@ -205,7 +215,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void de
         }
     }
 
-    // K, Q and K^T as fragments.
+    // K and Q as fragments.
     uint8_t *key = a.keys + ((int64_t)blockIdx.x * p.Hk + kh) * W::KEY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {       // wave w writes what wave w of the second kernel reads
@@ -219,22 +229,11 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void de
             kf[0] = k2[0], kf[1] = k2[1];
             qf[0] = q2[0], qf[1] = q2[1];
         }
-        reinterpret_cast<u32x4 *>(key + (4 * w + i) * FRAG)[lane] = kf;
-        reinterpret_cast<u32x4 *>(key + W::Q + (4 * i + w) * FRAG)[lane] = qf;
-    }
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int dk = DT == 2 ? 32 * w + 8 * (r >> 2) + 4 * d + (r & 3) : 16 * w + r;
-            u32x4 f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint16_t *at = ks + (32 * s + 8 * g + 2 * e) * PITCH + dk;
-                f[e] = (uint32_t)at[0] | ((uint32_t)at[PITCH] << 16);
-            }
-            reinterpret_cast<u32x4 *>(key + W::KT + ((w * DT + d) * 2 + s) * FRAG)[lane] = f;
+        if (blockIdx.z == 0) {
+            reinterpret_cast<u32x4 *>(key + (4 * w + i) * FRAG)[lane] = kf;
+            reinterpret_cast<u32x4 *>(key + W::Q + (4 * i + w) * FRAG)[lane] = qf;
         }
+    }
 
     // Row tile w of K K^T and Q K^T (rows in token order here).
     f32x4 kk[4], qk[4];
@@ -258,14 +257,14 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void de
     lds_barrier();
     for (int i = tid; i < C * MP / 4; i += NT)
         reinterpret_cast<f32x4 *>(m)[i] = reinterpret_cast<f32x4 *>(pm)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int group = p.Hv / p.Hk;
-    for (int hi = 0; hi < group; ++hi) {
-        const int h = kh * group + hi, hs = hi & 3;
+    const int group = p.Hv / p.Hk, h0 = (int)blockIdx.z * a.heads, heads = min(a.heads, group - h0);
+    for (int hi = 0; hi < heads; ++hi) {
+        const int h = kh * group + h0 + hi, hs = hi & 3;
         if (hs == 0) {
             // Sums of the gates of the next four heads, a wave each, in 64
             // bits; a total gate counts as exp(-10000) = 0.
             lds_barrier();
-            if (hi + w < group) {
+            if (hi + w < heads) {
                 float gate = 0.f, beta = 0.f;
                 if (lane < rows) {
                     gate = p.g[(first + lane) * p.Hv + h + w];
@@ -440,6 +439,15 @@ __device__ __forceinline__ void split(const f32x4 &x, bf16x4 (&part)[N])
 
 __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
+// Values of four lanes transposed: of each 16 lanes, lane i gets value i % 4 of
+// the places of lanes i / 4, 4 + i / 4, 8 + i / 4 and 12 + i / 4.
+__device__ __forceinline__ bf16x4 transposed(const bf16x4 *place)
+{
+    typedef short i16x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                          (__attribute__((address_space(3))) i16x4 *)(place)));
+}
+
 // Waves 0 to 3 carry S, waves 4 to 7 make the outputs. Three exchanges
 // through LDS a chunk, each ended by a barrier that all eight waves meet:
 //   chain wave w: its rows' share of K S; its rows of S in two parts  -> xp; ssh
@@ -450,7 +458,9 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_sh
 // third, and after it brings V and the row factors of the next chunk and adds
 // P U. The time of a chunk is the chain's latencies, not its arithmetic, so
 // whatever is not the chain is left to the output waves, and every operand is
-// loaded right after its last use, a chunk ahead.
+// loaded right after its last use, a chunk ahead. (16384 tokens: 758 us with
+// four waves that did all, 467 with this split, 430 with K^T transposed out of
+// LDS instead of loaded beside K.)
 // VEC: v's rows of 16 columns are two 16-byte pieces and o's take 8-byte
 // stores (a host rule; as a branch inside, it made the compiler wait for
 // every load at its end).
@@ -462,6 +472,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     __shared__ f32x4 xp[4][4][64], uo[4][64];
     __shared__ bf16x8 ssh[2][4][64];
     __shared__ bf16x4 ysh[3][4][64], ush[3][4][64];
+    __shared__ bf16x4 ksh[4][4][DT][64];            // chain wave w's K, for its transposed reads
     __shared__ f32x4 vsh[4][64], factors[4][2][4];  // factors: r exp G, then r exp(G_63 - G)
     __shared__ u32x4 vrows[4][32];                  // V as it lies in memory: 16 tokens of 32 bytes
     __shared__ __align__(16) int badcol[16];
@@ -652,7 +663,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
             S[d][e] = dk < p.Dk && col < p.Dv ? v : 0.f;
         }
 
-    bf16x8 kf[4], ktf[DT][2], tf[2][3];
+    bf16x8 kf[4], tf[2][3];
     u32x2 head = {0, 0};
     bool bad_any = false;       // some token of a chunk so far is not finite
     auto load_k = [&](int c) __attribute__((always_inline)) {
@@ -670,13 +681,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
                 for (int i = 0; i < 3; ++i)
                     tf[s][i] = frag(val, 3 * s + i - 2);
     };
-    auto load_kt = [&](int c) __attribute__((always_inline)) {
-        const uint8_t *key = key0 + c * key_step + W::KT + 2 * DT * w * FRAG;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                ktf[d][s] = frag(key, 2 * d + s);
+    auto load_head = [&](int c) __attribute__((always_inline)) {
         // (A scalar load would be waited for at the next barrier, which waits
         // for LDS traffic on the same counter.)
         head = *reinterpret_cast<const u32x2 *>(val0 + c * val_step + W::HEAD);
@@ -684,12 +689,18 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     if (chunks > 0) {
         load_k(0);
         load_t(0);
-        load_kt(0);
+        load_head(0);
     }
     __builtin_amdgcn_s_setprio(3);      // before the output wave of the same SIMD
     for (int c = 0; c < chunks; ++c) {
         const int next = min(c + 1, chunks - 1);
         // K S, wave w's rows of S only.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ksh[w][i][0][4 * r + g] = __builtin_shufflevector(kf[i], kf[i], 0, 1, 2, 3);
+            if constexpr (DT == 2)
+                ksh[w][i][DT - 1][4 * r + g] = __builtin_shufflevector(kf[i], kf[i], 4, 5, 6, 7);
+        }
         bf16x4 lo[3], hi[3] = {};
         split<3>(S[0], lo);
         if constexpr (DT == 2)
@@ -736,25 +747,35 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
         // Token tile w of U = T Y.
         const f32x4 tail = factors[w][1][g];
         f32x4 u = {0.f, 0.f, 0.f, 0.f};
+        bf16x8 yf[2][3];
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (2 * s <= w) {
-                bf16x8 y[3];
+            if (2 * s <= w)
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
-                    y[i] = join(ysh[i][2 * s][lane], ysh[i][2 * s + 1][lane]);
+                    yf[s][i] = join(ysh[i][2 * s][lane], ysh[i][2 * s + 1][lane]);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (2 * s <= w)
 #pragma unroll
                 for (int k = 2; k >= 0; --k)
 #pragma unroll
                     for (int i = 0; i <= k; ++i)
-                        u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tf[s][i], y[k - i], u, 0, 0, 0);
-            }
+                        u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(tf[s][i], yf[s][k - i], u, 0, 0, 0);
         uo[w][lane] = u;
         bf16x4 us[3];
         split<3>(u * tail, us);
 #pragma unroll
         for (int i = 0; i < 3; ++i)
             ush[i][w][lane] = us[i];
+        // K^T for the last phase: lane (g, r) gets values r % 4 of lanes
+        // (r / 4, 4g + e), which lie together.
+        bf16x8 ktf[DT][2];
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                ktf[d][s] = join(transposed(ksh[w][2 * s][d] + lane), transposed(ksh[w][2 * s + 1][d] + lane));
         load_t(next);
         lds_barrier();
         // S'.
@@ -771,7 +792,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
                 for (int d = 0; d < DT; ++d)
                     S[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ktf[d][s], u, S[d], 0, 0, 0);
             }
-        load_kt(next);
+        load_head(next);
     }
     if (!p.state_out || slot < 0)
         return;
@@ -798,7 +819,14 @@ hipError_t launch(const DeltaProblem &p, hipStream_t s)
     a.vec = (((uintptr_t)p.q | (uintptr_t)p.k) % 16 == 0) && ((p.qst | p.qsh | p.kst | p.ksh) % 8 == 0);
     const bool vec = (uintptr_t)p.v % 16 == 0 && (p.vst | p.vsh) % 8 == 0 && p.Dv % 16 == 0 && (uintptr_t)p.o % 8 == 0 &&
                      (p.ost | p.osh) % 4 == 0;
-    hipLaunchKernelGGL(delta_prepare_kernel<DT>, dim3((unsigned)numbers, (unsigned)p.Hk), dim3(NT), 0, s, a);
+    // One value head a workgroup while the chip holds them all at once, or
+    // nearly (four a compute unit): 33 chunks of 32 heads, two a key head, took
+    // 78.4 us together and 76.7 apart, 65 chunks 135.7 and 146.2; 9 chunks of 16
+    // heads, four a key head, 37.2 and 27.0.
+    const int group = p.Hv / p.Hk;
+    a.heads = numbers * p.Hv <= 1280 ? 1 : group;
+    hipLaunchKernelGGL(delta_prepare_kernel<DT>,
+                       dim3((unsigned)numbers, (unsigned)p.Hk, (unsigned)((group + a.heads - 1) / a.heads)), dim3(NT), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;

@@ -128,8 +128,14 @@ conv_status check_delta_sizes(int64_t tokens, int num_seqs, int Hk, int Hv, int 
     if (tokens > MAX_ROWS || num_seqs > MAX_ROWS || Dk > 256 || Dv > 65536 || Hv > 65535)
         return CONV_ERR_UNSUPPORTED;
     const bool can = delta_chunked_supports(tokens, num_seqs, Hk, Hv, Dk, Dv, dtype);
+    // Tokens a sequence from which chunks are faster. A lone sequence of 32
+    // heads of 128 x 128 takes 16 us by chunks up to 64 tokens, and token by
+    // token 15.6 for 16 of them, 18.6 for 20; once the chunks' workgroups share
+    // compute units, 8 such sequences take 38 us (token by token 33 for 24
+    // tokens, 42 for 32) and 64 take 200 (192 and 262).
+    const int least = (int64_t)num_seqs * Hv * ((Dv + 15) / 16) <= 256 ? 16 : 26;
     switch (variant) {
-    case CONV_VARIANT_AUTO: *tiled = can && tokens > 16 * (int64_t)num_seqs; return CONV_OK;
+    case CONV_VARIANT_AUTO: *tiled = can && tokens > least * (int64_t)num_seqs; return CONV_OK;
     case CONV_VARIANT_DIRECT: *tiled = false; return CONV_OK;
     case CONV_VARIANT_TILED: *tiled = true; return can ? CONV_OK : CONV_ERR_UNSUPPORTED;
     default: return CONV_ERR_UNSUPPORTED;
