@@ -23,10 +23,10 @@
 // workgroups: no faster, 103 us for the six prompts.)
 //
 // 16384 tokens of one prompt, 16 key and 32 value heads of 128 x 128: the first
-// 124 us, 0.52 GB at 4.2 TB/s; the second 430 us, 256 chunks of 1.7 us each, one
-// workgroup a compute unit. There the chain of exchanges is the time (matrix
-// instructions: a fifth of it). With two workgroups a compute unit a chunk of
-// both takes 2.7 us, the loads' and LDS's paths half busy each.
+// 124 us, 0.52 GB at 4.2 TB/s; the second 412-430 us, 256 chunks of 1.6-1.7 us
+// each, one workgroup a compute unit. There the chain of exchanges is the time
+// (matrix instructions: a fifth of it). With two workgroups a compute unit a
+// chunk of both takes 2.7 us, the loads' and LDS's paths half busy each.
 //
 // Precision: bf16 operands (K, Q) are exact, every other operand of a product
 // is split into bf16 parts x = hi + mid + lo (each the nearest bf16 of what is
@@ -459,7 +459,7 @@ __device__ __forceinline__ bf16x4 transposed(const bf16x4 *place)
 // P U. The time of a chunk is the chain's latencies, not its arithmetic, so
 // whatever is not the chain is left to the output waves, and every operand is
 // loaded right after its last use, a chunk ahead. (16384 tokens: 758 us with
-// four waves that did all, 467 with this split, 430 with K^T transposed out of
+// four waves that did all, 467 with this split, 412-430 with K^T transposed out of
 // LDS instead of loaded beside K.)
 // VEC: v's rows of 16 columns are two 16-byte pieces and o's take 8-byte
 // stores (a host rule; as a branch inside, it made the compiler wait for

@@ -294,6 +294,13 @@ def test_delta_heads(Hk, Hv, Dk, Dv, dtype, variant):
     run_delta(q, k, v, g, beta, lens, rnd((3, Hv, Dk, Dv), 215, std=0.3), False, scale=0.7, variant=variant)
 
 
+def test_delta_many_chunks():
+    """More chunks than the chip holds at once (another split of the preparation), six value heads a key head."""
+    lens = [3] * 130 + [70, 0, 129] + [1] * 90
+    q, k, v, g, beta = delta_inputs(sum(lens), 1, 6, 64, 16, BF, 220)
+    run_delta(q, k, v, g, beta, lens, None, True, variant=cf.VARIANT_TILED)
+
+
 def test_delta_wide_heads():
     """Dk past the chunked form's limit."""
     lens = [20, 3]
