@@ -816,7 +816,7 @@ hipError_t launch(const DeltaProblem &p, hipStream_t s)
     const int64_t numbers = seq_tiles(p.seq, C);
     a.keys = static_cast<uint8_t *>(p.workspace);
     a.vals = a.keys + numbers * p.Hk * W::KEY;
-    a.vec = (((uintptr_t)p.q | (uintptr_t)p.k) % 16 == 0) && ((p.qst | p.qsh | p.kst | p.ksh) % 8 == 0);
+    a.vec = (((uintptr_t)p.q | (uintptr_t)p.k) % 16 == 0) && ((p.qst | p.qsh | p.kst | p.ksh | p.Dk) % 8 == 0);
     const bool vec = (uintptr_t)p.v % 16 == 0 && (p.vst | p.vsh) % 8 == 0 && p.Dv % 16 == 0 && (uintptr_t)p.o % 8 == 0 &&
                      (p.ost | p.osh) % 4 == 0;
     // One value head a workgroup while the chip holds them all at once, or

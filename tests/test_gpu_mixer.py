@@ -294,6 +294,20 @@ def test_delta_heads(Hk, Hv, Dk, Dv, dtype, variant):
     run_delta(q, k, v, g, beta, lens, rnd((3, Hv, Dk, Dv), 215, std=0.3), False, scale=0.7, variant=variant)
 
 
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_delta_padded_rows(dtype, variant):
+    """Heads of 100 and 60 values in aligned rows of 104 and 64, NaN between them."""
+    lens = [70, 2]
+    q, k, v, g, beta = delta_inputs(72, 2, 2, 100, 60, dtype, 225)
+    fin = torch.zeros(2, 2, 100, 60, device=DEV)
+    o = cf.gated_delta_rule(padded(q, 4), padded(k, 4), padded(v, 4), g.to(DEV), beta.to(DEV), normalize=True,
+                            seq_offsets=ref.seqs(lens, DEV), final_state=fin, variant=variant)
+    o0, bo, s0, bs = ref.delta(q, k, v, g, beta, 0.1, True, lens, None)
+    ref.check(o, o0, bo, "o")
+    ref.check(fin, s0, bs, "state")
+
+
 def test_delta_many_chunks():
     """More chunks than the chip holds at once (another split of the preparation), six value heads a key head."""
     lens = [3] * 130 + [70, 0, 129] + [1] * 90
