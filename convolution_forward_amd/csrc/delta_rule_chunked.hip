@@ -1,4 +1,4 @@
-// The gated delta rule by chunks of 64 tokens on the matrix cores, bf16
+// The gated delta rule by chunks of 64 tokens on the matrix cores, bf16 or fp32
 // operands, in fp32 precision.
 //
 // Inside a chunk let G_i be the sum of the gates up to token i, r_i the factor
@@ -28,17 +28,20 @@
 // (matrix instructions: a fifth of it). With two workgroups a compute unit a
 // chunk of both takes 2.7 us, the loads' and LDS's paths half busy each.
 //
-// Precision: bf16 operands (K, Q) are exact, every other operand of a product
+// Precision, bf16: operands (K, Q) are exact, every other operand of a product
 // is split into bf16 parts x = hi + mid + lo (each the nearest bf16 of what is
 // left, 24 bits together), and the products of parts above 2^-24 are added in
 // fp32: three for an exact operand times a split one, six for two split ones.
-// What only o sees (bf16 for these operands) uses two parts, 2^-17.
+// What only o sees (bf16 for these operands) uses two parts, 2^-17. fp32
+// operands go through the fp32 matrix instructions as they are.
 //
 // Values that are not finite: a zero of T or P times a NaN would carry it to
 // earlier tokens. So rows of K that hold one are read as zeros, and values of
 // V - .. that are not finite as zeros, and the token is noted; from it on the
 // outputs and the final state are set to NaN, for all columns (K, g, beta) or
 // for its own (V, S).
+#include <type_traits>
+
 #include "common.h"
 #include "internal.h"
 #include "sequences.h"
@@ -70,11 +73,14 @@ __device__ __forceinline__ int token_of(int i, int r) { return 32 * (i >> 1) + 8
 // and a header. A fragment is 64 lanes x 16 bytes.
 constexpr int FRAG = 1024;
 
-template <int DT>
+// In fp32: K (wave, tile, d), Q (tile, wave, d) and K^T (wave, d, tile), 16 DT
+// fragments each; T and P, 10 fragments each.
+template <int DT, bool F32>
 struct Space {
-    static constexpr int Q = 16 * FRAG, KEY = 32 * FRAG;
-    static constexpr int P = 18 * FRAG, UPK = 30 * FRAG, UPQ = UPK + 256, TAIL = UPQ + 256, HEAD = TAIL + 256;
-    static constexpr int VAL = 31 * FRAG;       // HEAD: exp(G_63), first token that is not finite
+    static constexpr int Q = (F32 ? 16 * DT : 16) * FRAG, KT = 2 * Q, KEY = F32 ? 3 * Q : 2 * Q;
+    static constexpr int P = (F32 ? 10 : 18) * FRAG, UPK = (F32 ? 20 : 30) * FRAG, UPQ = UPK + 256, TAIL = UPQ + 256,
+                         HEAD = TAIL + 256;     // exp(G_63), first token that is not finite
+    static constexpr int VAL = UPK + FRAG;
 };
 
 // Place of fragment (tile i, K step s) among the six of a lower triangle.
@@ -99,16 +105,17 @@ __device__ __forceinline__ __bf16 part_of(float &x)
     return h;
 }
 
-template <int DT>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void delta_prepare_kernel(ChunkArgs a)
+template <int DT, bool F32>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(F32 ? 2 : 4))) void delta_prepare_kernel(ChunkArgs a)
 {
-    using W = Space<DT>;
-    constexpr int D = 64 * DT, PITCH = D + 8, MP = 68;
+    using W = Space<DT, F32>;
+    using T = typename std::conditional<F32, float, uint16_t>::type;
+    constexpr int D = 64 * DT, E = 16 / sizeof(T), PITCH = D + E, MP = 68;
     const DeltaProblem &p = a.p;
     // K and Q give their room to A (then T) and P once their products are in registers.
-    constexpr int ROWS = C * PITCH * 2 > C * MP * 4 ? C * PITCH * 2 : C * MP * 4;
+    constexpr int KROWS = C * PITCH * (int)sizeof(T), ROWS = KROWS > C * MP * 4 ? KROWS : C * MP * 4;
     __shared__ __align__(16) uint8_t room[2 * ROWS];
-    uint16_t *ks = reinterpret_cast<uint16_t *>(room), *qs = reinterpret_cast<uint16_t *>(room + ROWS);
+    T *ks = reinterpret_cast<T *>(room), *qs = reinterpret_cast<T *>(room + ROWS);
     float *m = reinterpret_cast<float *>(room), *pm = reinterpret_cast<float *>(room + ROWS);
     // Four 16x16 blocks between the two halves of the last inversion step, in a corner of m that nothing else uses.
     auto z = [&](int i) { return m + 16 * (i >> 1) * MP + 32 + 16 * (i & 1); };
@@ -132,33 +139,33 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void de
     if (tid < C)
         badrow[tid] = 0;
     lds_barrier();
-    constexpr int PIECES = C * D / 8 / NT;
+    constexpr int PIECES = C * D / E / NT;
     u32x4 kv[PIECES], qv[PIECES];
     if (a.vec) {
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
+            const int row = (i * NT + tid) / (D / E), c = (i * NT + tid) % (D / E) * E;
             const int64_t at = first + min(row, rows - 1);
             const int cc = c < p.Dk ? c : 0;
-            kv[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.k) + at * p.kst + kh * p.ksh + cc);
-            qv[i] = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p.q) + at * p.qst + kh * p.qsh + cc);
+            kv[i] = *reinterpret_cast<const u32x4 *>(static_cast<const T *>(p.k) + at * p.kst + kh * p.ksh + cc);
+            qv[i] = *reinterpret_cast<const u32x4 *>(static_cast<const T *>(p.q) + at * p.qst + kh * p.qsh + cc);
         }
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
+            const int row = (i * NT + tid) / (D / E), c = (i * NT + tid) % (D / E) * E;
             if (row >= rows || c >= p.Dk)
                 kv[i] = qv[i] = u32x4{0, 0, 0, 0};
         }
     } else {
 #pragma unroll 1
         for (int i = 0; i < PIECES; ++i) {
-            const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
-            uint16_t k8[8] __attribute__((aligned(16))) = {}, q8[8] __attribute__((aligned(16))) = {};
+            const int row = (i * NT + tid) / (D / E), c = (i * NT + tid) % (D / E) * E;
+            T k8[E] __attribute__((aligned(16))) = {}, q8[E] __attribute__((aligned(16))) = {};
             if (row < rows) {
-                const uint16_t *kp = static_cast<const uint16_t *>(p.k) + (first + row) * p.kst + kh * p.ksh + c;
-                const uint16_t *qp = static_cast<const uint16_t *>(p.q) + (first + row) * p.qst + kh * p.qsh + c;
+                const T *kp = static_cast<const T *>(p.k) + (first + row) * p.kst + kh * p.ksh + c;
+                const T *qp = static_cast<const T *>(p.q) + (first + row) * p.qst + kh * p.qsh + c;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < E; ++e)
                     if (c + e < p.Dk) {
                         k8[e] = kp[e];
                         q8[e] = qp[e];
@@ -170,18 +177,18 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void de
         // Each thread takes its own pieces back.
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {
-            const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
+            const int row = (i * NT + tid) / (D / E), c = (i * NT + tid) % (D / E) * E;
             kv[i] = *reinterpret_cast<const u32x4 *>(ks + row * PITCH + c);
             qv[i] = *reinterpret_cast<const u32x4 *>(qs + row * PITCH + c);
         }
     }
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-        const int row = (i * NT + tid) / (D / 8), c = (i * NT + tid) % (D / 8) * 8;
+        const int row = (i * NT + tid) / (D / E), c = (i * NT + tid) % (D / E) * E;
         bool bad = false;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            bad |= (kv[i][e] & 0x7f80u) == 0x7f80u || (kv[i][e] & 0x7f800000u) == 0x7f800000u;
+            bad |= (!F32 && (kv[i][e] & 0x7f80u) == 0x7f80u) || (kv[i][e] & 0x7f800000u) == 0x7f800000u;
         if (bad) {
             kv[i] = u32x4{0, 0, 0, 0};
             badrow[row] = 1;
@@ -194,15 +201,20 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void de
         const int row = tid >> 2;
         float sk = 0.f, sq = 0.f;
 #pragma unroll
-        for (int c = 8 * (tid & 3); c < D; c += 32) {
+        for (int c = E * (tid & 3); c < D; c += 4 * E) {
             const u32x4 x = *reinterpret_cast<const u32x4 *>(ks + row * PITCH + c);
             const u32x4 y = *reinterpret_cast<const u32x4 *>(qs + row * PITCH + c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x0 = __uint_as_float(x[e] << 16), x1 = __uint_as_float(x[e] & 0xffff0000u);
-                const float y0 = __uint_as_float(y[e] << 16), y1 = __uint_as_float(y[e] & 0xffff0000u);
-                sk = fmaf(x1, x1, fmaf(x0, x0, sk));
-                sq = fmaf(y1, y1, fmaf(y0, y0, sq));
+                if constexpr (F32) {
+                    sk = fmaf(__uint_as_float(x[e]), __uint_as_float(x[e]), sk);
+                    sq = fmaf(__uint_as_float(y[e]), __uint_as_float(y[e]), sq);
+                } else {
+                    const float x0 = __uint_as_float(x[e] << 16), x1 = __uint_as_float(x[e] & 0xffff0000u);
+                    const float y0 = __uint_as_float(y[e] << 16), y1 = __uint_as_float(y[e] & 0xffff0000u);
+                    sk = fmaf(x1, x1, fmaf(x0, x0, sk));
+                    sq = fmaf(y1, y1, fmaf(y0, y0, sq));
+                }
             }
         }
         sk += __shfl_xor(sk, 1);
@@ -217,21 +229,40 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void de
 
     // K and Q as fragments.
     uint8_t *key = a.keys + ((int64_t)blockIdx.x * p.Hk + kh) * W::KEY;
+    if constexpr (F32) {
+        if (blockIdx.z == 0)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {       // wave w writes what wave w of the second kernel reads
-        const int at = token_of(i, r) * PITCH + (DT == 2 ? 32 * w + 8 * g : 16 * w + 4 * g);
-        u32x4 kf = {0, 0, 0, 0}, qf = {0, 0, 0, 0};
-        if constexpr (DT == 2) {
-            kf = *reinterpret_cast<const u32x4 *>(ks + at);
-            qf = *reinterpret_cast<const u32x4 *>(qs + at);
-        } else {
-            const u32x2 k2 = *reinterpret_cast<const u32x2 *>(ks + at), q2 = *reinterpret_cast<const u32x2 *>(qs + at);
-            kf[0] = k2[0], kf[1] = k2[1];
-            qf[0] = q2[0], qf[1] = q2[1];
-        }
-        if (blockIdx.z == 0) {
-            reinterpret_cast<u32x4 *>(key + (4 * w + i) * FRAG)[lane] = kf;
-            reinterpret_cast<u32x4 *>(key + W::Q + (4 * i + w) * FRAG)[lane] = qf;
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const int at = (16 * i + r) * PITCH + 16 * (DT * w + d) + 4 * g;
+                    f32x4 f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f[e] = ks[(16 * i + 4 * g + e) * PITCH + 16 * (DT * w + d) + r];
+                    reinterpret_cast<f32x4 *>(key + ((4 * w + i) * DT + d) * FRAG)[lane] =
+                        *reinterpret_cast<const f32x4 *>(ks + at);
+                    reinterpret_cast<f32x4 *>(key + W::Q + ((4 * i + w) * DT + d) * FRAG)[lane] =
+                        *reinterpret_cast<const f32x4 *>(qs + at);
+                    reinterpret_cast<f32x4 *>(key + W::KT + ((DT * w + d) * 4 + i) * FRAG)[lane] = f;
+                }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {       // wave w writes what wave w of the second kernel reads
+            const int at = token_of(i, r) * PITCH + (DT == 2 ? 32 * w + 8 * g : 16 * w + 4 * g);
+            u32x4 kf = {0, 0, 0, 0}, qf = {0, 0, 0, 0};
+            if constexpr (DT == 2) {
+                kf = *reinterpret_cast<const u32x4 *>(ks + at);
+                qf = *reinterpret_cast<const u32x4 *>(qs + at);
+            } else {
+                const u32x2 k2 = *reinterpret_cast<const u32x2 *>(ks + at), q2 = *reinterpret_cast<const u32x2 *>(qs + at);
+                kf[0] = k2[0], kf[1] = k2[1];
+                qf[0] = q2[0], qf[1] = q2[1];
+            }
+            if (blockIdx.z == 0) {
+                reinterpret_cast<u32x4 *>(key + (4 * w + i) * FRAG)[lane] = kf;
+                reinterpret_cast<u32x4 *>(key + W::Q + (4 * i + w) * FRAG)[lane] = qf;
+            }
         }
     }
 
@@ -240,18 +271,37 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void de
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         kk[j] = qk[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (F32) {
+#pragma unroll 2
+        for (int s = 0; s < D / 16; ++s) {
+            const int c = 16 * s + 4 * g;
+            const f32x4 ka = *reinterpret_cast<const f32x4 *>(ks + (16 * w + r) * PITCH + c);
+            const f32x4 qa = *reinterpret_cast<const f32x4 *>(qs + (16 * w + r) * PITCH + c);
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-        const int c = 32 * s + 8 * g;
-        const bf16x8 ka = *reinterpret_cast<const bf16x8 *>(ks + (16 * w + r) * PITCH + c);
-        const bf16x8 qa = *reinterpret_cast<const bf16x8 *>(qs + (16 * w + r) * PITCH + c);
+            for (int j = 0; j < 4; ++j)
+                if (j <= w) {
+                    const f32x4 kb = *reinterpret_cast<const f32x4 *>(ks + (16 * j + r) * PITCH + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j <= w) {
-                const bf16x8 kb = *reinterpret_cast<const bf16x8 *>(ks + (16 * j + r) * PITCH + c);
-                kk[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, kb, kk[j], 0, 0, 0);
-                qk[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qa, kb, qk[j], 0, 0, 0);
-            }
+                    for (int e = 0; e < 4; ++e) {
+                        kk[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(ka[e], kb[e], kk[j], 0, 0, 0);
+                        qk[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(qa[e], kb[e], qk[j], 0, 0, 0);
+                    }
+                }
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s) {
+            const int c = 32 * s + 8 * g;
+            const bf16x8 ka = *reinterpret_cast<const bf16x8 *>(ks + (16 * w + r) * PITCH + c);
+            const bf16x8 qa = *reinterpret_cast<const bf16x8 *>(qs + (16 * w + r) * PITCH + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j <= w) {
+                    const bf16x8 kb = *reinterpret_cast<const bf16x8 *>(ks + (16 * j + r) * PITCH + c);
+                    kk[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ka, kb, kk[j], 0, 0, 0);
+                    qk[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qa, kb, qk[j], 0, 0, 0);
+                }
+        }
     }
 
     lds_barrier();
@@ -377,30 +427,43 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void de
         lds_barrier();
 
         uint8_t *val = a.vals + ((int64_t)blockIdx.x * p.Hv + h) * W::VAL;
-        const int row = token_of(w, r);
+        if constexpr (F32) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-            if (2 * s <= w) {
-                bf16x8 t3[3], p2[2];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int col = 32 * s + 8 * g + e;
-                    float t = m[row * MP + col] * bs[hs][col];
-                    t3[0][e] = part_of(t);
-                    t3[1][e] = part_of(t);
-                    t3[2][e] = part_of(t);
-                    float q = pm[row * MP + col];
-                    p2[0][e] = part_of(q);
-                    p2[1][e] = part_of(q);
+            for (int j = 0; j < 4; ++j)
+                if (j <= w) {
+                    const int col = 16 * j + 4 * g, f = w * (w + 1) / 2 + j;
+                    reinterpret_cast<f32x4 *>(val + f * FRAG)[lane] =
+                        *reinterpret_cast<const f32x4 *>(m + (16 * w + r) * MP + col) *
+                        *reinterpret_cast<const f32x4 *>(bs[hs] + col);
+                    reinterpret_cast<f32x4 *>(val + W::P + f * FRAG)[lane] =
+                        *reinterpret_cast<const f32x4 *>(pm + (16 * w + r) * MP + col);
                 }
-                const int f = low_frag(w, s);
+        } else {
+            const int row = token_of(w, r);
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    reinterpret_cast<bf16x8 *>(val + (3 * f + i) * FRAG)[lane] = t3[i];
+            for (int s = 0; s < 2; ++s)
+                if (2 * s <= w) {
+                    bf16x8 t3[3], p2[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    reinterpret_cast<bf16x8 *>(val + W::P + (2 * f + i) * FRAG)[lane] = p2[i];
-            }
+                    for (int e = 0; e < 8; ++e) {
+                        const int col = 32 * s + 8 * g + e;
+                        float t = m[row * MP + col] * bs[hs][col];
+                        t3[0][e] = part_of(t);
+                        t3[1][e] = part_of(t);
+                        t3[2][e] = part_of(t);
+                        float q = pm[row * MP + col];
+                        p2[0][e] = part_of(q);
+                        p2[1][e] = part_of(q);
+                    }
+                    const int f = low_frag(w, s);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        reinterpret_cast<bf16x8 *>(val + (3 * f + i) * FRAG)[lane] = t3[i];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        reinterpret_cast<bf16x8 *>(val + W::P + (2 * f + i) * FRAG)[lane] = p2[i];
+                }
+        }
         if (w == 0) {
             const double G = gs[hs][lane], last = gs[hs][C - 1];
             const float e = __expf((float)G);
@@ -467,7 +530,7 @@ __device__ __forceinline__ bf16x4 transposed(const bf16x4 *place)
 template <int DT, bool VEC>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void delta_chunks_kernel(ChunkArgs a)
 {
-    using W = Space<DT>;
+    using W = Space<DT, false>;
     const DeltaProblem &p = a.p;
     __shared__ f32x4 xp[4][4][64], uo[4][64];
     __shared__ bf16x8 ssh[2][4][64];
@@ -807,25 +870,269 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
         }
 }
 
+// The same in fp32 with fp32 matrix instructions (16x16x4). A result's four
+// rows a lane are the next product's operand as they lie, value e for step e,
+// so nothing is split and tokens keep their order; the waves, barriers and the
+// order of loads are those of the kernel above. 2047 tokens, 16 heads of 128 x
+// 128: 120 us with the preparation, token by token 1330. The instructions are
+// half of a chunk's 2.8 us. 128 registers (two spilled) for two workgroups a
+// compute unit: 8 sequences of 256 tokens, 32 heads, 167 -> 150 us.
 template <int DT>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void delta_chunks_f32_kernel(ChunkArgs a)
+{
+    using W = Space<DT, true>;
+    const DeltaProblem &p = a.p;
+    __shared__ f32x4 xp[4][4][64], ssh[4][DT][64], ysh[4][64], ush[4][64], uo[4][64], vsh[4][64];
+    __shared__ f32x4 factors[4][2][4];
+    __shared__ int badcol[16];
+
+    const int at = (int)blockIdx.x >> 3;
+    const int slice = at % a.slices, nh = at / a.slices * 8 + ((int)blockIdx.x & 7);
+    if (nh >= p.seq.num_seqs * p.Hv)
+        return;
+    const int n = nh / p.Hv, h = nh % p.Hv, kh = h / (p.Hv / p.Hk);
+    const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    const int w8 = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int w = w8 < 4 ? w8 : 7 - w8;
+    const int64_t begin = seq_begin(p.seq, n);
+    const int64_t end = seq_begin(p.seq, n + 1);
+    const int len = end > begin ? (int)(end - begin) : 0;
+    const int chunks = (len + C - 1) / C;
+    const int64_t number = begin / C + n;
+    const int slot = p.state_in || p.state_out ? seq_slot(p.seq, n) : -1;
+    const int col = slice * 16 + r;
+    const int tok4 = 16 * w + 4 * g;
+    const uint8_t *key0 = a.keys + (number * p.Hk + kh) * W::KEY;
+    const uint8_t *val0 = a.vals + (number * p.Hv + h) * W::VAL;
+    const int64_t key_step = (int64_t)p.Hk * W::KEY, val_step = (int64_t)p.Hv * W::VAL;
+    const uint32_t lane16 = 16 * lane;
+    auto frag = [&](const uint8_t *base, int i) __attribute__((always_inline)) {
+        return *reinterpret_cast<const f32x4 *>(base + lane16 + i * FRAG);
+    };
+    auto mac = [](const f32x4 &x, const f32x4 &y, f32x4 sum) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            sum = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], sum, 0, 0, 0);
+        return sum;
+    };
+    const int low = w * (w + 1) / 2;        // first fragment of row tile w of T and P
+
+    if (threadIdx.x < 16)
+        badcol[threadIdx.x] = NEVER;
+    __syncthreads();
+
+    if (w8 >= 4) {
+        f32x4 qf[4 * DT], pf[4], upq = {}, o;
+        int bad_here = NEVER, badall = NEVER;
+        auto load_q = [&](int c) __attribute__((always_inline)) {
+            const uint8_t *key = key0 + c * key_step + W::Q + 4 * DT * w * FRAG;
+#pragma unroll
+            for (int i = 0; i < 4 * DT; ++i)
+                qf[i] = frag(key, i);
+        };
+        auto load_p = [&](int c) __attribute__((always_inline)) {
+            const uint8_t *val = val0 + c * val_step, *pv = val + W::P + low * FRAG;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                pf[j] = frag(pv, min(j, w));
+            upq = *reinterpret_cast<const f32x4 *>(val + W::UPQ + 4 * tok4);
+            bad_here = reinterpret_cast<const int *>(val + W::HEAD)[1];
+        };
+        float v[4];
+        f32x4 factor;
+        const float *vh = static_cast<const float *>(p.v) + begin * p.vst + h * p.vsh + min(col, p.Dv - 1);
+        auto load_v = [&](int c) __attribute__((always_inline)) {
+            factor = *reinterpret_cast<const f32x4 *>(val0 + c * val_step + (r < 8 ? W::UPK : W::TAIL) + 4 * tok4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = vh[min(c * C + tok4 + e, len - 1) * p.vst];
+        };
+        auto give_v = [&]() __attribute__((always_inline)) {
+            vsh[w][lane] = f32x4{v[0], v[1], v[2], v[3]};
+            if ((r & 7) == 0)
+                factors[w][r >> 3][g] = factor;
+        };
+        if (chunks > 0) {
+            load_v(0);
+            give_v();
+            load_v(min(1, chunks - 1));
+            load_q(0);
+            load_p(0);
+        }
+        float *oh = static_cast<float *>(p.o) + (begin + tok4) * p.ost + h * p.osh + col;
+        auto add_pu = [&](int c) __attribute__((always_inline)) {
+            asm volatile("" : "+v"(bad_here));      // (not looked at before this phase, see above)
+            if (badall == NEVER && bad_here != NEVER)
+                badall = c * C + bad_here;
+            o *= upq;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j <= w)
+                    o = mac(pf[j], uo[j][lane], o);
+        };
+        auto store = [&](int c) __attribute__((always_inline)) {
+            const int bad = min(badall, badcol[r]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = c * C + tok4 + e;
+                if (t < len && col < p.Dv)
+                    oh[e * p.ost] = t >= bad ? NAN : o[e];
+            }
+            oh += C * p.ost;
+        };
+        for (int c = 0; c < chunks; ++c) {
+            lds_barrier();
+            f32x4 q = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    q = mac(qf[DT * i + d], ssh[i][d][lane], q);
+            load_q(min(c + 1, chunks - 1));
+            lds_barrier();
+            if (c > 0)
+                store(c - 1);
+            o = q;
+            lds_barrier();
+            give_v();
+            load_v(min(c + 2, chunks - 1));
+            add_pu(c);
+            load_p(min(c + 1, chunks - 1));
+        }
+        if (chunks > 0)
+            store(chunks - 1);
+        return;
+    }
+
+    const int64_t sat = ((int64_t)slot * p.Hv + h) * p.Dk * p.Dv;
+    auto dk_of = [&](int d) { return 16 * (DT * w + d) + 4 * g; };
+    f32x4 S[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int dk = dk_of(d) + e;
+            float v = 0.f;
+            if (p.state_in && slot >= 0)
+                v = p.state_in[sat + (int64_t)min(dk, p.Dk - 1) * p.Dv + min(col, p.Dv - 1)];
+            S[d][e] = dk < p.Dk && col < p.Dv ? v : 0.f;
+        }
+
+    f32x4 kf[4][DT], ktf[DT][4], tf[4];
+    u32x2 head = {0, 0};
+    bool bad_any = false;
+    auto load_k = [&](int c) __attribute__((always_inline)) {
+        const uint8_t *key = key0 + c * key_step + 4 * DT * w * FRAG;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                kf[i][d] = frag(key, i * DT + d);
+    };
+    auto load_t = [&](int c) __attribute__((always_inline)) {
+        const uint8_t *val = val0 + c * val_step + low * FRAG;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            tf[j] = frag(val, min(j, w));
+    };
+    auto load_kt = [&](int c) __attribute__((always_inline)) {
+        const uint8_t *key = key0 + c * key_step + W::KT + 4 * DT * w * FRAG;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                ktf[d][j] = frag(key, 4 * d + j);
+        head = *reinterpret_cast<const u32x2 *>(val0 + c * val_step + W::HEAD);
+    };
+    if (chunks > 0) {
+        load_k(0);
+        load_t(0);
+        load_kt(0);
+    }
+    __builtin_amdgcn_s_setprio(3);
+    for (int c = 0; c < chunks; ++c) {
+        const int next = min(c + 1, chunks - 1);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+            ssh[w][d][lane] = S[d];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                acc = mac(kf[i][d], S[d], acc);
+            xp[w][i][lane] = acc;
+        }
+        load_k(next);
+        lds_barrier();
+        f32x4 y = vsh[w][lane] -
+                  factors[w][0][g] * ((xp[0][w][lane] + xp[1][w][lane]) + (xp[2][w][lane] + xp[3][w][lane]));
+        float zero = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            zero = fmaf(y[e], 0.f, zero);
+        if (__any(zero != 0.f))
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (!(fabsf(y[e]) < INFINITY)) {
+                    atomicMin(&badcol[r], c * C + tok4 + e);
+                    y[e] = 0.f;
+                }
+        ysh[w][lane] = y;
+        lds_barrier();
+        const f32x4 tail = factors[w][1][g];
+        f32x4 u = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j <= w)
+                u = mac(tf[j], ysh[j][lane], u);
+        uo[w][lane] = u;
+        ush[w][lane] = u * tail;
+        load_t(next);
+        lds_barrier();
+        bad_any |= (int)head[1] != NEVER;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            S[d] *= __uint_as_float(head[0]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                S[d] = mac(ktf[d][j], ush[j][lane], S[d]);
+        }
+        load_kt(next);
+    }
+    if (!p.state_out || slot < 0)
+        return;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int dk = dk_of(d) + e;
+            if (dk < p.Dk && col < p.Dv)
+                p.state_out[sat + (int64_t)dk * p.Dv + col] = bad_any || badcol[r] != NEVER ? NAN : S[d][e];
+        }
+}
+
+template <int DT, bool F32>
 hipError_t launch(const DeltaProblem &p, hipStream_t s)
 {
-    using W = Space<DT>;
+    using W = Space<DT, F32>;
     ChunkArgs a = {};
     a.p = p;
     const int64_t numbers = seq_tiles(p.seq, C);
     a.keys = static_cast<uint8_t *>(p.workspace);
     a.vals = a.keys + numbers * p.Hk * W::KEY;
-    a.vec = (((uintptr_t)p.q | (uintptr_t)p.k) % 16 == 0) && ((p.qst | p.qsh | p.kst | p.ksh | p.Dk) % 8 == 0);
+    a.vec = ((uintptr_t)p.q | (uintptr_t)p.k) % 16 == 0 && (p.qst | p.qsh | p.kst | p.ksh | p.Dk) % (F32 ? 4 : 8) == 0;
     const bool vec = (uintptr_t)p.v % 16 == 0 && (p.vst | p.vsh) % 8 == 0 && p.Dv % 16 == 0 && (uintptr_t)p.o % 8 == 0 &&
                      (p.ost | p.osh) % 4 == 0;
     // One value head a workgroup while the chip holds them all at once, or
     // nearly (four a compute unit): 33 chunks of 32 heads, two a key head, took
     // 78.4 us together and 76.7 apart, 65 chunks 135.7 and 146.2; 9 chunks of 16
-    // heads, four a key head, 37.2 and 27.0.
+    // heads, four a key head, 37.2 and 27.0. In fp32 (two a compute unit, and
+    // more work that they would share): 17 chunks of 32 heads, two a key head,
+    // 81 together and 86 apart; of 16, four a key head, 78 and 72.
     const int group = p.Hv / p.Hk;
-    a.heads = numbers * p.Hv <= 1280 ? 1 : group;
-    hipLaunchKernelGGL(delta_prepare_kernel<DT>,
+    a.heads = numbers * p.Hv <= (F32 ? 512 : 1280) ? 1 : group;
+    hipLaunchKernelGGL((delta_prepare_kernel<DT, F32>),
                        dim3((unsigned)numbers, (unsigned)p.Hk, (unsigned)((group + a.heads - 1) / a.heads)), dim3(NT), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
@@ -833,7 +1140,9 @@ hipError_t launch(const DeltaProblem &p, hipStream_t s)
     a.slices = (p.Dv + 15) / 16;
     const int64_t heads = ((int64_t)p.seq.num_seqs * p.Hv + 7) / 8 * 8;
     const dim3 grid((unsigned)(heads * a.slices)), block(512);
-    if (vec)
+    if constexpr (F32)
+        hipLaunchKernelGGL(delta_chunks_f32_kernel<DT>, grid, block, 0, s, a);
+    else if (vec)
         hipLaunchKernelGGL((delta_chunks_kernel<DT, true>), grid, block, 0, s, a);
     else
         hipLaunchKernelGGL((delta_chunks_kernel<DT, false>), grid, block, 0, s, a);
@@ -842,23 +1151,32 @@ hipError_t launch(const DeltaProblem &p, hipStream_t s)
 
 }  // namespace
 
-bool delta_chunked_supports(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, int Dv, conv_dtype dtype)
+bool delta_chunked_supports(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, int Dv)
 {
     // Chunk numbers and jobs fit the grids.
-    return dtype == CONV_BF16 && Dk <= 128 && tokens / C + num_seqs <= (1 << 30) &&
+    return Dk <= 128 && tokens / C + num_seqs <= (1 << 30) &&
            ((int64_t)num_seqs * Hv + 8) * ((Dv + 15) / 16) <= (1 << 30);
 }
 
-int64_t delta_chunked_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk)
+template <int DT, bool F32>
+static int64_t chunk_bytes(int Hk, int Hv)
+{
+    return (int64_t)Hk * Space<DT, F32>::KEY + (int64_t)Hv * Space<DT, F32>::VAL;
+}
+
+int64_t delta_chunked_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, conv_dtype dtype)
 {
     const int64_t numbers = tokens / C + num_seqs;
-    return numbers * (Dk <= 64 ? (int64_t)Hk * Space<1>::KEY + (int64_t)Hv * Space<1>::VAL
-                               : (int64_t)Hk * Space<2>::KEY + (int64_t)Hv * Space<2>::VAL);
+    if (dtype == CONV_F32)
+        return numbers * (Dk <= 64 ? chunk_bytes<1, true>(Hk, Hv) : chunk_bytes<2, true>(Hk, Hv));
+    return numbers * (Dk <= 64 ? chunk_bytes<1, false>(Hk, Hv) : chunk_bytes<2, false>(Hk, Hv));
 }
 
 hipError_t launch_delta_chunked(const DeltaProblem &p, hipStream_t s)
 {
-    return p.Dk <= 64 ? launch<1>(p, s) : launch<2>(p, s);
+    if (p.dtype == CONV_F32)
+        return p.Dk <= 64 ? launch<1, true>(p, s) : launch<2, true>(p, s);
+    return p.Dk <= 64 ? launch<1, false>(p, s) : launch<2, false>(p, s);
 }
 
 }  // namespace convfwd

@@ -16,8 +16,8 @@
 // loaded a token ahead and a wave takes 16 columns, half the work a step.
 //
 // 128 sequences of one token, 32 heads of 128 x 128: 99 us, 0.54 GB at 5.4
-// TB/s; one sequence, 4.3 us. Long ones are their chain, 0.7 us a token (2048
-// fp32 tokens: 1.5 ms).
+// TB/s; one sequence, 4.3 us. Long ones are their chain, 0.7 us a token
+// (by chunks less from some 16 to 60 tokens on).
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"

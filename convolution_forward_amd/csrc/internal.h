@@ -161,8 +161,8 @@ struct DeltaProblem {
 };
 
 hipError_t launch_delta_direct(const DeltaProblem &p, hipStream_t s);
-bool delta_chunked_supports(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, int Dv, conv_dtype dtype);
-int64_t delta_chunked_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk);
+bool delta_chunked_supports(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, int Dv);
+int64_t delta_chunked_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, conv_dtype dtype);
 hipError_t launch_delta_chunked(const DeltaProblem &p, hipStream_t s);
 
 // Streaming copies used for bandwidth / counter calibration.

@@ -127,13 +127,16 @@ conv_status check_delta_sizes(int64_t tokens, int num_seqs, int Hk, int Hv, int 
         return CONV_ERR_DTYPE;
     if (tokens > MAX_ROWS || num_seqs > MAX_ROWS || Dk > 256 || Dv > 65536 || Hv > 65535)
         return CONV_ERR_UNSUPPORTED;
-    const bool can = delta_chunked_supports(tokens, num_seqs, Hk, Hv, Dk, Dv, dtype);
+    const bool can = delta_chunked_supports(tokens, num_seqs, Hk, Hv, Dk, Dv);
     // Tokens a sequence from which chunks are faster. A lone sequence of 32
     // heads of 128 x 128 takes 16 us by chunks up to 64 tokens, and token by
     // token 15.6 for 16 of them, 18.6 for 20; once the chunks' workgroups share
     // compute units, 8 such sequences take 38 us (token by token 33 for 24
     // tokens, 42 for 32) and 64 take 200 (192 and 262).
-    const int least = (int64_t)num_seqs * Hv * ((Dv + 15) / 16) <= 256 ? 16 : 26;
+    // In fp32, where a chunk costs more: 22.6 us alone (28 tokens one by one
+    // 22.7), 59 for 8 sequences (48 tokens 56, 64 71), 360 to 400 for 64 (344, 454).
+    const bool alone = (int64_t)num_seqs * Hv * ((Dv + 15) / 16) <= 256;
+    const int least = dtype == CONV_F32 ? (alone ? 28 : 50) : alone ? 16 : 26;
     switch (variant) {
     case CONV_VARIANT_AUTO: *tiled = can && tokens > least * (int64_t)num_seqs; return CONV_OK;
     case CONV_VARIANT_DIRECT: *tiled = false; return CONV_OK;
@@ -271,7 +274,7 @@ int64_t conv_delta_rule_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, 
     bool tiled;
     if (check_delta_sizes(tokens, num_seqs, Hk, Hv, Dk, Dv, dtype, variant, &tiled) != CONV_OK)
         return -1;
-    return tiled ? delta_chunked_workspace(tokens, num_seqs, Hk, Hv, Dk) : 0;
+    return tiled ? delta_chunked_workspace(tokens, num_seqs, Hk, Hv, Dk, dtype) : 0;
 }
 
 conv_status conv_delta_rule_fwd(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,

@@ -425,8 +425,8 @@ CONVFWD_API conv_status conv_causal1d_fwd(const void *x, int64_t x_stride, const
  *              256-byte aligned, used during the call only (NULL when that is 0).
  *   variant    CONV_VARIANT_DIRECT: token by token, any sizes with Dk <= 256.
  *              CONV_VARIANT_TILED: by chunks of 64 tokens on the matrix
- *              cores, bf16 with Dk <= 128. CONV_VARIANT_AUTO picks by the sizes.
- *              Both compute in fp32 precision.
+ *              cores, Dk <= 128. CONV_VARIANT_AUTO picks by the sizes. Both
+ *              compute in fp32 precision.
  */
 CONVFWD_API conv_status conv_delta_rule_fwd(const void *q, const int64_t *q_strides, const void *k,
                                             const int64_t *k_strides, const void *v, const int64_t *v_strides,

@@ -308,10 +308,11 @@ def test_delta_padded_rows(dtype, variant):
     ref.check(fin, s0, bs, "state")
 
 
-def test_delta_many_chunks():
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_delta_many_chunks(dtype):
     """More chunks than the chip holds at once (another split of the preparation), six value heads a key head."""
     lens = [3] * 130 + [70, 0, 129] + [1] * 90
-    q, k, v, g, beta = delta_inputs(sum(lens), 1, 6, 64, 16, BF, 220)
+    q, k, v, g, beta = delta_inputs(sum(lens), 1, 6, 64, 16, dtype, 220)
     run_delta(q, k, v, g, beta, lens, None, True, variant=cf.VARIANT_TILED)
 
 
