@@ -323,21 +323,23 @@ def test_delta_wide_heads():
     run_delta(q, k, v, g, beta, lens, None, True)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("variant", VARIANTS)
-def test_delta_correlated_keys(variant):
+def test_delta_correlated_keys(variant, dtype):
     """Nearly equal keys and beta 1: the triangular system at its worst."""
     lens = [150]
-    q, k, v, g, beta = delta_inputs(150, 1, 2, 64, 32, BF, 240)
-    k = (k[:1] + 0.05 * rnd(k.shape, 241)).to(BF)
+    q, k, v, g, beta = delta_inputs(150, 1, 2, 64, 32, dtype, 240)
+    k = (k[:1] + 0.05 * rnd(k.shape, 241)).to(dtype)
     run_delta(q, k, v, torch.zeros_like(g), torch.ones_like(beta), lens, None, True, variant=variant)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("variant", VARIANTS)
-def test_delta_gates(variant):
+def test_delta_gates(variant, dtype):
     """Gates of every strength: none, total (-inf, which forgets all before it, even what is not finite in no place),
     and long runs of strong ones whose sum passes what an fp32 difference resolves."""
     T = 200
-    q, k, v, g, beta = delta_inputs(T, 1, 3, 64, 32, BF, 250)
+    q, k, v, g, beta = delta_inputs(T, 1, 3, 64, 32, dtype, 250)
     g[:, 0] = 0.0
     g[::7, 1] = float("-inf")
     g[100, 1] = -3e38
@@ -347,10 +349,11 @@ def test_delta_gates(variant):
     run_delta(q, k, v, g, beta, [T], rnd((1, 3, 64, 32), 255), True, variant=variant)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("variant", VARIANTS)
-def test_delta_zero_rows(variant):
+def test_delta_zero_rows(variant, dtype):
     """Keys and queries of zeros (normalised: still zeros)."""
-    q, k, v, g, beta = delta_inputs(100, 1, 1, 32, 32, BF, 260)
+    q, k, v, g, beta = delta_inputs(100, 1, 1, 32, 32, dtype, 260)
     k[10:80], q[70:] = 0, 0
     run_delta(q, k, v, g, beta, [100], None, True, variant=variant)
 
@@ -372,11 +375,12 @@ def test_delta_nan_stays_in_its_sequence_and_head(variant, T):
     assert not bad[:, 1, cols].any() and not torch.isnan(fin[1, 1][:, cols]).any()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("variant", VARIANTS)
 @pytest.mark.parametrize("lens", [[1, 1, 1, 1, 1], [70, 0, 1, 128, 9]], ids=str)
-def test_delta_slots_in_place(lens, variant):
+def test_delta_slots_in_place(lens, variant, dtype):
     slots = [6, 0, -1, 3, 9]
-    q, k, v, g, beta = delta_inputs(sum(lens), 2, 2, 64, 64, BF, 280)
+    q, k, v, g, beta = delta_inputs(sum(lens), 2, 2, 64, 64, dtype, 280)
     pool = rnd((7, 2, 64, 64), 285, std=0.3)
     start = torch.stack([pool[s] if 0 <= s < 7 else torch.zeros_like(pool[0]) for s in slots])
     dev = pool.to(DEV)
@@ -454,15 +458,16 @@ def test_delta_by_chunks(lens, Hk, Hv, Dk, Dv):
     run_delta(q, k, v, g, beta, lens, rnd((len(lens), Hv, Dk, Dv), 355, std=0.3), True, variant=cf.VARIANT_TILED)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("variant", VARIANTS)
 @pytest.mark.parametrize("which,value", [("k", float("nan")), ("k", float("inf")), ("g", float("nan")),
                                          ("g", float("inf")), ("beta", float("nan")), ("q", float("nan")),
                                          ("v", float("-inf")), ("state", float("nan"))])
-def test_delta_not_finite(which, value, variant):
+def test_delta_not_finite(which, value, variant, dtype):
     """What is not finite reaches its own token and later ones of its head (q: its token only; v and the state: its
     column), never earlier tokens, other heads or other sequences."""
     lens, t = [90, 100, 40], 70
-    q, k, v, g, beta = delta_inputs(sum(lens), 2, 2, 64, 32, BF, 360)
+    q, k, v, g, beta = delta_inputs(sum(lens), 2, 2, 64, 32, dtype, 360)
     states = rnd((3, 2, 64, 32), 365, std=0.3)
     at = 90 + t
     if which == "state":
