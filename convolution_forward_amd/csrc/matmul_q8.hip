@@ -489,19 +489,20 @@ hipError_t launch(Q8Args &a, hipStream_t s)
     if (a.M <= 32)
         return launch_few<2, E4M3, OB, ALIGNED>(a, s);
     // The tile whose rounds over the 256 compute units cost least. A round's
-    // cost is its time at K = 4096 over the 64x64 tile's (int8: 8.9, 12.5,
-    // 17.3, 27, 43 us; e4m3 15.8, 20, 32, 49, 81): the larger a tile, the fewer
+    // cost is its time at K = 4096 over the 64x64 tile's (int8, from 32x64 up:
+    // 8.5, 8.9, 12.5, 17.3, 27, 43 us; e4m3 13.3, 15.8, 20, 32, 49, 81): the larger a tile, the fewer
     // bytes it loads for each product, and the longer it holds its unit. (1024
     // x 8192 x 4096: 128x256 36 us, 128x128 45, 256x256 52; 512 x 4096 x
-    // 4096: 64x128 14.7, 64x64 17.7, 128x128 19.)
+    // 4096: 64x128 14.7, 64x64 17.7, 128x128 19; 64 x 8192 x 4096: 32x64 11.0,
+    // 64x64 12.5, in e4m3 13.9 and 16.1; 256 x 4096 x 4096: 64x64 9.2, 32x64 11.4.)
     auto cost = [&](int tm, int tn, int each) {
         const int64_t tiles = (int64_t)((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn);
         return (tiles + 255) / 256 * each;
     };
-    const int64_t costs[5] = {cost(256, 256, 48), cost(128, 256, 31), cost(128, 128, 20), cost(64, 128, 14),
-                              cost(64, 64, 10)};
+    const int64_t costs[6] = {cost(256, 256, 48), cost(128, 256, 31), cost(128, 128, 20), cost(64, 128, 14),
+                              cost(64, 64, 10), cost(32, 64, 9)};
     int best = 0;
-    for (int i = 1; i < 5; ++i)
+    for (int i = 1; i < 6; ++i)
         if (costs[i] < costs[best])
             best = i;
     switch (best) {
@@ -509,7 +510,8 @@ hipError_t launch(Q8Args &a, hipStream_t s)
     case 1: return launch_tiles<4, 4, 2, 4, 1, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
     case 2: return launch_tiles<4, 2, 2, 4, 1, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
     case 3: return launch_tiles<2, 2, 2, 4, 1, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
-    default: return launch_tiles<1, 2, 4, 2, 2, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
+    case 4: return launch_tiles<1, 2, 4, 2, 2, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
+    default: return launch_tiles<1, 2, 2, 2, 2, ALIGNED ? 3 : 2, E4M3, OB, ALIGNED>(a, s);
     }
 }
 

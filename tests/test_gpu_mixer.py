@@ -123,6 +123,19 @@ def test_product(m, n, k, qdt, variant):
 
 
 @pytest.mark.parametrize("qdt", [I8, E4])
+@pytest.mark.parametrize("k", [288, 413])
+@pytest.mark.parametrize("m,n", [(40, 100), (60, 8402), (130, 8300), (250, 12901), (500, 16000), (1000, 16008)])
+def test_product_tiles(m, n, k, qdt):
+    """A size for each tile, the largest one's last, with rows, channels and K that it does not divide."""
+    x, w = eight((m, k), 51, qdt), eight((n, k), 52, qdt)
+    xs, ws, bias = rnd(m, 53).abs() * 0.05, rnd(n, 54).abs() * 0.01, rnd(n, 55)
+    for dt in (F32, BF):
+        y = cf.matmul_q8(x.to(DEV), xs.to(DEV), w.to(DEV), ws.to(DEV), bias=bias.to(DEV), out_dtype=dt)
+        want, bound = ref.product(x, xs, w, ws, bias)
+        ref.check(y, want, bound, f"product {m}x{n}x{k} {qdt} {dt}")
+
+
+@pytest.mark.parametrize("qdt", [I8, E4])
 @pytest.mark.parametrize("m", [5, 70, 300])
 def test_product_strided(qdt, m):
     """Operand rows with a pitch of every alignment, K inside a 16-byte piece, what lies between rows never used."""
