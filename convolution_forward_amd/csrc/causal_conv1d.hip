@@ -198,7 +198,7 @@ void launch(const Causal1dProblem &p, hipStream_t s)
 
 hipError_t launch_causal1d(const Causal1dProblem &p, hipStream_t s)
 {
-    if (seq_tiles(p.seq, TT) > (int64_t(1) << 30) || p.channels > (1 << 23))
+    if (seq_tiles(p.seq, TT) >= (int64_t(1) << 24) || p.channels > (1 << 23))
         return hipErrorInvalidValue;
     if (p.dtype == CONV_BF16)
         launch<uint16_t>(p, s);

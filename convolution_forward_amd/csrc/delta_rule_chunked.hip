@@ -1153,9 +1153,8 @@ hipError_t launch(const DeltaProblem &p, hipStream_t s)
 
 bool delta_chunked_supports(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, int Dv)
 {
-    // Chunk numbers and jobs fit the grids.
-    return Dk <= 128 && tokens / C + num_seqs <= (1 << 30) &&
-           ((int64_t)num_seqs * Hv + 8) * ((Dv + 15) / 16) <= (1 << 30);
+    // The threads of both grids stay below 2^32.
+    return Dk <= 128 && tokens / C + num_seqs < (1 << 24) && ((int64_t)num_seqs * Hv + 8) * ((Dv + 15) / 16) < (1 << 23);
 }
 
 template <int DT, bool F32>

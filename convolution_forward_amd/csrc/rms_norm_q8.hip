@@ -290,14 +290,29 @@ void launch(const NormProblem &p, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_rms_norm_q8(const NormProblem &p, hipStream_t s)
+hipError_t launch_rms_norm_q8(const NormProblem &all, hipStream_t s)
 {
-    const bool e = p.qdt == CONV_E4M3;
-    if (p.dtype == CONV_BF16)
-        e ? launch<uint16_t, true>(p, s) : launch<uint16_t, false>(p, s);
-    else
-        e ? launch<float, true>(p, s) : launch<float, false>(p, s);
-    return hipGetLastError();
+    // By 2^21 rows, so that a grid's threads stay below 2^32.
+    const int64_t most = 1 << 21, e = all.dtype == CONV_BF16 ? 2 : 4;
+    auto at = [](auto *t, int64_t bytes) { return t ? (decltype(t))((uintptr_t)t + bytes) : nullptr; };
+    for (int64_t first = 0; first < all.rows; first += most) {
+        NormProblem p = all;
+        p.rows = all.rows - first < most ? all.rows - first : most;
+        p.x = at(all.x, first * all.xs * e);
+        p.residual = at(all.residual, first * all.rs * e);
+        p.h = at(all.h, first * all.hs * e);
+        p.q = at(all.q, first * all.qs);
+        p.scale = all.scale + first;
+        const bool e4m3 = p.qdt == CONV_E4M3;
+        if (p.dtype == CONV_BF16)
+            e4m3 ? launch<uint16_t, true>(p, s) : launch<uint16_t, false>(p, s);
+        else
+            e4m3 ? launch<float, true>(p, s) : launch<float, false>(p, s);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess)
+            return err;
+    }
+    return hipSuccess;
 }
 
 }  // namespace convfwd

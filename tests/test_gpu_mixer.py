@@ -48,6 +48,17 @@ def check_norm(q, s, h, x, w, r, eps, qdt):
     ref.check(q, want, want.abs() * (2 * rel + 4 * ref.U), "q", qdt)
 
 
+def test_norm_many_rows():
+    """More rows than one launch takes: the same as a call on the rows round its end."""
+    rows = 2 ** 21 + 3
+    x = torch.arange(rows * 8, device=DEV).remainder(8191).sub(4000).to(BF).reshape(rows, 8)
+    w = rnd(8, 14, BF).to(DEV)
+    q, s, h = cf.rms_norm_q8(x, w, residual=x.flip(0))
+    some = slice(2 ** 21 - 4, None)
+    for a, b in zip((q, s, h), cf.rms_norm_q8(x[some], w, residual=x.flip(0)[some])):
+        assert torch.equal(a[some], b)
+
+
 def test_norm_strided_and_in_place():
     """Rows with a pitch (NaN between them), 2-byte alignment only, and the sum written over the residual."""
     for width, extra in ((256, 8), (256, 1), (1030, 3)):

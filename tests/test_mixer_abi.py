@@ -115,6 +115,9 @@ def test_delta_workspace_query(lib):
     assert cf.delta_rule_workspace(0, 1, 1, 1, 64, 64) >= 0
     assert cf.delta_rule_workspace(1, 1, 2, 3, 64, 64) == -1
     assert cf.delta_rule_workspace(1, 1, 1, 1, 300, 64) == -1
+    # More heads and sequences than a grid of chunks holds: token by token, without a workspace.
+    assert cf.delta_rule_workspace(40000 * 64, 40000, 16, 32, 128, 128) == 0
+    assert cf.delta_rule_workspace(40000 * 64, 40000, 16, 32, 128, 128, variant=cf.VARIANT_TILED) == -1
 
 
 def test_binding_rejects_cpu_tensors(lib):
