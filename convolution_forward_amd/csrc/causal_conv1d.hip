@@ -6,14 +6,14 @@
 //   y[t,c] = act(bias[c] + sum_j w[c,j] * xx[t - taps + 1 + j, c])
 //
 // A workgroup takes TT tokens of one sequence (tiles never cross sequences)
-// and 256 channel vectors; a thread slides the taps-1 previous rows of its
+// and 512 channels; a thread slides the taps-1 previous rows of its
 // channels along the tile in registers, so each row is read once plus taps-1
 // rows a tile. The bytes are the time: 8192 tokens of 8192 channels, bf16, 4
-// taps, 59-66 us, 4.1-4.6 TB/s (tiles of 32 tokens read 9 % twice; eight rows
-// in flight a thread; one at a time took 81 us). 64 sequences of one token: 7.2 us, the
-// latency of offsets, slot, state and x one after the other. The first tile of
-// a sequence also writes the sequence's state, after it has read the old one:
-// the two may be the same memory.
+// taps, 56 us, 4.8 TB/s (tiles of 32 tokens read 9 % twice; eight rows in
+// flight a thread; one at a time took 81 us). 64 sequences of one token: 5.1
+// us, the latency of offsets, slot, state and x one after the other. The first
+// tile of a sequence also writes the sequence's state, after it has read the
+// old one: the two may be the same memory.
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"
@@ -22,7 +22,7 @@
 namespace convfwd {
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 128;
 constexpr int TT = 32;               // tokens of a tile
 constexpr int BATCH = 8;             // rows in flight a thread
 
@@ -58,10 +58,14 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[V])
 #pragma unroll
     for (int i = 0; i < V; ++i)
         store_rne(&t.v[i], f[i]);
-    if constexpr (V > 1)
-        __builtin_memcpy(__builtin_assume_aligned(p, V * sizeof(T)), &t, sizeof(t));
-    else
+    if constexpr (V > 1) {
+        // Streaming stores: 8192 x 8192 bf16 65.2 -> 60.9 us. (Loads keep the
+        // caches, where the rows before a tile are found again.)
+        typedef uint32_t Piece __attribute__((ext_vector_type(V * sizeof(T) / 4)));
+        __builtin_nontemporal_store(__builtin_bit_cast(Piece, t), reinterpret_cast<Piece *>(p));
+    } else {
         *p = t.v[0];
+    }
 }
 
 template <class T, int V, int K>
@@ -184,11 +188,14 @@ void launch_taps(const Causal1dProblem &p, hipStream_t s)
 template <class T>
 void launch(const Causal1dProblem &p, hipStream_t s)
 {
-    constexpr int V = 16 / sizeof(T);
+    // Four channels a thread: with eight bf16 ones the window and the taps took
+    // the registers of half the waves (8192 x 8192: 56.9 us against 60.9, 64
+    // single tokens 5.1 against 6.3).
+    constexpr int V = 4;
     const uintptr_t bits = (uintptr_t)p.x | (uintptr_t)p.y | (uintptr_t)p.w | (uintptr_t)p.state_in | (uintptr_t)p.state_out |
                            (uintptr_t)(p.xs * sizeof(T)) | (uintptr_t)(p.ys * sizeof(T)) |
                            (uintptr_t)(p.channels * sizeof(T));
-    if (bits % 16 == 0)
+    if (bits % (V * sizeof(T)) == 0)
         launch_taps<T, V>(p, s);
     else
         launch_taps<T, 1>(p, s);
