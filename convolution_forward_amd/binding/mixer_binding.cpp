@@ -378,7 +378,8 @@ PyObject *gated_delta_rule(PyObject *const *a)
     Tensor space;
     int64_t bytes = 0;
     if (work) {
-        bytes = work->numel() * work->element_size();
+        bytes = work->numel();
+        vector(work, bytes, at::kByte, "workspace");
     } else {
         bytes = conv_delta_rule_workspace(seq.tokens, seq.count, hk, hv, dk, dv, dt, variant);
         if (bytes > 0)
