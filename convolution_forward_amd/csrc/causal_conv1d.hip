@@ -74,11 +74,11 @@ __global__ __launch_bounds__(NT) void causal_conv1d_kernel(Causal1dProblem p)
     const int c = ((int)blockIdx.y * NT + (int)threadIdx.x) * V;
     // The weights' loads go out before the search for the sequence.
     const bool live = c < p.channels;
-    T wv[V * K] __attribute__((aligned(16)));
+    T wv[V * K] __attribute__((aligned(V * sizeof(T))));
     float b[V];
     const T *wp = static_cast<const T *>(p.w) + (int64_t)(live ? c : 0) * K;
     if constexpr (V > 1) {
-        __builtin_memcpy(wv, __builtin_assume_aligned(wp, 16), sizeof(wv));
+        __builtin_memcpy(wv, __builtin_assume_aligned(wp, V * sizeof(T)), sizeof(wv));     // what the host's rule checks
     } else {
 #pragma unroll
         for (int i = 0; i < K; ++i)

@@ -3,7 +3,8 @@ import pytest
 import torch
 
 import convolution_forward_amd as cf
-from test_gpu_mixer import BF, DEV, delta_inputs
+import mixer_ref as ref
+from test_gpu_mixer import BF, DEV, F32, delta_inputs, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +22,20 @@ def test_workspace_is_contiguous_bytes(make):
     o = cf.gated_delta_rule(q, k, v, g, beta, workspace=torch.empty(n, dtype=torch.uint8, device=DEV),
                             variant=cf.VARIANT_TILED)
     assert torch.equal(o, cf.gated_delta_rule(q, k, v, g, beta, variant=cf.VARIANT_TILED))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("taps", range(2, 9))
+@pytest.mark.parametrize("channels,shift", [(64, 0), (68, 0), (64, 4), (68, 4), (66, 2)])
+def test_conv_taps(taps, channels, shift, dtype):
+    """Every number of taps, four channels a thread and one, the weights `shift` values past an aligned address."""
+    lens = [40, 1, 0, 70]
+    x, w = rnd((sum(lens), channels), 65, dtype), rnd((channels, taps), 66, dtype, 0.5)
+    b, st = rnd(channels, 67), rnd((4, taps - 1, channels), 68, dtype)
+    wd = torch.cat([torch.zeros(shift, dtype=dtype), w.flatten()]).to(DEV)[shift:].view(channels, taps)
+    fin = torch.zeros_like(st, device=DEV)
+    y = cf.causal_conv1d(x.to(DEV), wd, bias=b.to(DEV), activation="silu", seq_offsets=ref.seqs(lens, DEV),
+                         initial_state=st.to(DEV), final_state=fin)
+    y0, bound, new = ref.conv(x, w, b, True, lens, st)
+    ref.check(y, y0, bound, "y")
+    assert torch.equal(fin.cpu().double(), new), "state"
