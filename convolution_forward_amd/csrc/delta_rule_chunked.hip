@@ -36,10 +36,11 @@
 // operands go through the fp32 matrix instructions as they are.
 //
 // Values that are not finite: a zero of T or P times a NaN would carry it to
-// earlier tokens. So rows of K that hold one are read as zeros, and values of
-// V - .. that are not finite as zeros, and the token is noted; from it on the
-// outputs and the final state are set to NaN, for all columns (K, g, beta) or
-// for its own (V, S).
+// earlier tokens. So rows of K that hold one are read as zeros, and so are
+// values of V - .., of U and of a product on the way to T that are not finite
+// or have overflowed, and the token is noted; from it on the outputs and the
+// final state are set to NaN, for all columns (K, g, beta, T) or for its own
+// (V, S, U).
 #include <type_traits>
 
 #include "common.h"
@@ -384,6 +385,18 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(F32 ? 2 : 4)
                 blk[i * MP + lane] = col[i];
         }
         lds_barrier();
+        // A X^-1's rows that overflowed would meet the zeros of Y^-1 in earlier tokens' rows. (Elsewhere rows of A and T
+        // that are not finite stay in theirs, and U shows them.)
+        auto finite = [&](f32x4 &t, int token) __attribute__((always_inline)) {
+            const float zero = fmaf(t[0], 0.f, fmaf(t[1], 0.f, fmaf(t[2], 0.f, t[3] * 0.f)));
+            if (__any(zero != 0.f))
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!(fabsf(t[e]) < INFINITY)) {
+                        atomicMin(&badtok[hs], token + e);
+                        t[e] = 0.f;
+                    }
+        };
         if (w < 2) {
             const int i = 2 * w + 1, j = 2 * w;
             f32x4 t = {0.f, 0.f, 0.f, 0.f}, o = t;
@@ -391,6 +404,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(F32 ? 2 : 4)
             for (int e = 0; e < 4; ++e)
                 t = __builtin_amdgcn_mfma_f32_16x16x4f32(m[(16 * i + r) * MP + 16 * j + 4 * e + g],
                                                          m[(16 * j + 4 * e + g) * MP + 16 * j + r], t, 0, 0, 0);
+            finite(t, 16 * i + 4 * g);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 o = __builtin_amdgcn_mfma_f32_16x16x4f32(m[(16 * i + r) * MP + 16 * i + 4 * g + e], t[e], o, 0, 0, 0);
@@ -409,6 +423,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(F32 ? 2 : 4)
                     for (int e = 0; e < 4; ++e)
                         t = __builtin_amdgcn_mfma_f32_16x16x4f32(m[(16 * i + r) * MP + 16 * k + 4 * e + g],
                                                                  m[(16 * k + 4 * e + g) * MP + 16 * j + r], t, 0, 0, 0);
+            finite(t, 16 * i + 4 * g);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 z(w)[(4 * g + e) * MP + r] = t[e];
@@ -496,6 +511,30 @@ __device__ __forceinline__ void split(const f32x4 &x, bf16x4 (&part)[N])
             left[1] -= __uint_as_float(lo & 0xffff0000u);
             left[2] -= __uint_as_float(hi << 16);
             left[3] -= __uint_as_float(hi & 0xffff0000u);
+        }
+    }
+}
+
+// Two tiles of U, four tokens of a column each from `token` and token + apart
+// on. One that is not finite (it has overflowed) is noted in *bad and set to
+// zero, since P's zeros would carry it to earlier tokens.
+__device__ __forceinline__ void finite_u(f32x4 &a, f32x4 &b, int *bad, int token, int apart)
+{
+    float zero = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        zero = fmaf(a[e], 0.f, fmaf(b[e], 0.f, zero));
+    if (!__any(zero != 0.f))
+        return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (!(fabsf(a[e]) < INFINITY)) {
+            atomicMin(bad, token + e);
+            a[e] = 0.f;
+        }
+        if (!(fabsf(b[e]) < INFINITY)) {
+            atomicMin(bad, token + apart + e);
+            b[e] = 0.f;
         }
     }
 }
@@ -654,9 +693,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 if (2 * s <= w) {
+                    f32x4 ua = uo[2 * s][lane], ub = uo[2 * s + 1][lane];
+                    finite_u(ua, ub, &badcol[r], c * C + 32 * s + 8 * g, 4);
                     bf16x4 lo[2], hi[2];
-                    split<2>(uo[2 * s][lane], lo);
-                    split<2>(uo[2 * s + 1][lane], hi);
+                    split<2>(ua, lo);
+                    split<2>(ub, hi);
                     const bf16x8 u0 = join(lo[0], hi[0]), u1 = join(lo[1], hi[1]);
                     o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u1, pf[s][0], o, 0, 0, 0);
                     o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][1], o, 0, 0, 0);
@@ -864,7 +905,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int dk = dk_of(d) + e, col = col0 + r;
-            const bool bad = bad_any || badcol[r] != NEVER;
+            const bool bad = bad_any || badcol[r] != NEVER || (chunks > 0 && !(fabsf(S[d][e]) < INFINITY));
             if (dk < p.Dk && col < p.Dv)
                 p.state_out[sat + (int64_t)dk * p.Dv + col] = bad ? NAN : S[d][e];
         }
@@ -966,9 +1007,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
                 badall = c * C + bad_here;
             o *= upq;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j <= w)
-                    o = mac(pf[j], uo[j][lane], o);
+            for (int s = 0; s < 2; ++s)
+                if (2 * s <= w) {
+                    f32x4 ua = uo[2 * s][lane], ub = uo[2 * s + 1][lane];
+                    finite_u(ua, ub, &badcol[r], c * C + 32 * s + 4 * g, 16);
+                    o = mac(pf[2 * s], ua, o);
+                    if (2 * s < w)
+                        o = mac(pf[2 * s + 1], ub, o);
+                }
         };
         auto store = [&](int c) __attribute__((always_inline)) {
             const int bad = min(badall, badcol[r]);
@@ -1107,8 +1153,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int dk = dk_of(d) + e;
+            const bool bad = bad_any || badcol[r] != NEVER || (chunks > 0 && !(fabsf(S[d][e]) < INFINITY));
             if (dk < p.Dk && col < p.Dv)
-                p.state_out[sat + (int64_t)dk * p.Dv + col] = bad_any || badcol[r] != NEVER ? NAN : S[d][e];
+                p.state_out[sat + (int64_t)dk * p.Dv + col] = bad ? NAN : S[d][e];
         }
 }
 

@@ -39,3 +39,42 @@ def test_conv_taps(taps, channels, shift, dtype):
     y0, bound, new = ref.conv(x, w, b, True, lens, st)
     ref.check(y, y0, bound, "y")
     assert torch.equal(fin.cpu().double(), new), "state"
+
+
+def overflow_inputs(which, dtype):
+    """Finite inputs, keys not normalised, that pass 32 bits at some token: (q, k, v, g, beta, tokens up to which the
+    rule is a contraction, tokens up to which a 64-bit evaluation stays inside 32 bits, tokens from which it does not)."""
+    q, k, v, g, beta = delta_inputs(100, 1, 2, 64, 32, dtype, 380, unit=True)
+    g, k = torch.zeros_like(g), k.float()
+    if which == "products":             # of the keys of tokens 20 and 40
+        k[20], k[40] = 2e19, 2e19
+        beta[20], beta[40] = 1e-30, 1
+        tame, fine, over = 20, 40, 41
+    elif which == "growth":             # of the state, by 5e4 a token
+        k[20:] *= 240
+        beta[20:] = 1
+        tame, fine, over = 20, 28, 32
+    else:                               # of the triangle's inverse: 1e22 by token 16, then keys of 1e20
+        k[4:16] *= 25
+        k[16:24] *= 1e-3
+        k[24:] *= 1e20
+        beta[4:] = 1
+        tame, fine, over = 4, 24, 26
+    return q, k.to(dtype), v, g, beta, tame, fine, over
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("variant", [cf.VARIANT_DIRECT, cf.VARIANT_TILED])
+@pytest.mark.parametrize("which", ["products", "growth", "inverse"])
+def test_delta_overflow_reaches_no_earlier_token(which, variant, dtype):
+    q, k, v, g, beta, tame, fine, over = overflow_inputs(which, dtype)
+    T = q.shape[0]
+    other = delta_inputs(T, 1, 2, 64, 32, dtype, 390, unit=True)
+    three = [torch.cat([b, a, b]).to(DEV) for a, b in zip((q, k, v, g, beta), other)]
+    fin = torch.zeros(3, 2, 64, 32, device=DEV)
+    o = cf.gated_delta_rule(*three, scale=0.125, seq_offsets=ref.seqs([T] * 3, DEV), final_state=fin, variant=variant).cpu()
+    good = torch.isfinite(o)
+    assert good[:T + fine].all() and good[2 * T:].all() and torch.isfinite(fin[[0, 2]]).all()
+    assert not good[T + over:2 * T].any() and not torch.isfinite(fin[1]).any()
+    o0, bo, _, _ = ref.delta(q[:tame], k[:tame], v[:tame], g[:tame], beta[:tame], 0.125, False, [tame], None)
+    ref.check(o[T:T + tame], o0, bo, "o before")
