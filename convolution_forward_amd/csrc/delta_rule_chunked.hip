@@ -32,8 +32,7 @@
 // is split into bf16 parts x = hi + mid + lo (each the nearest bf16 of what is
 // left, 24 bits together), and the products of parts above 2^-24 are added in
 // fp32: three for an exact operand times a split one, six for two split ones.
-// What only o sees (bf16 for these operands) uses two parts, 2^-17. fp32
-// operands go through the fp32 matrix instructions as they are.
+// fp32 operands go through the fp32 matrix instructions as they are.
 //
 // Values that are not finite: a zero of T or P times a NaN would carry it to
 // earlier tokens. So rows of K that hold one are read as zeros, and so are
@@ -70,8 +69,8 @@ __device__ __forceinline__ int token_of(int i, int r) { return 32 * (i >> 1) + 8
 // ---- Workspace ---------------------------------------------------------------
 // For each chunk number and key head: K (wave, tile) and Q (tile, wave), 4 x 4
 // fragments each. For each chunk number and value head: T, 3 parts of the 6
-// fragments that are not all zero, P, 2 parts of them, then 4 x 64 row factors
-// and a header. A fragment is 64 lanes x 16 bytes.
+// fragments that are not all zero, P, the same 6 in fp32, two each, then 4 x 64
+// row factors and a header. A fragment is 64 lanes x 16 bytes.
 constexpr int FRAG = 1024;
 
 // In fp32: K (wave, tile, d), Q (tile, wave, d) and K^T (wave, d, tile), 16 DT
@@ -458,7 +457,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(F32 ? 2 : 4)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 if (2 * s <= w) {
-                    bf16x8 t3[3], p2[2];
+                    bf16x8 t3[3];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int col = 32 * s + 8 * g + e;
@@ -466,9 +465,6 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(F32 ? 2 : 4)
                         t3[0][e] = part_of(t);
                         t3[1][e] = part_of(t);
                         t3[2][e] = part_of(t);
-                        float q = pm[row * MP + col];
-                        p2[0][e] = part_of(q);
-                        p2[1][e] = part_of(q);
                     }
                     const int f = low_frag(w, s);
 #pragma unroll
@@ -476,7 +472,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(F32 ? 2 : 4)
                         reinterpret_cast<bf16x8 *>(val + (3 * f + i) * FRAG)[lane] = t3[i];
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        reinterpret_cast<bf16x8 *>(val + W::P + (2 * f + i) * FRAG)[lane] = p2[i];
+                        reinterpret_cast<f32x4 *>(val + W::P + (2 * f + i) * FRAG)[lane] =
+                            *reinterpret_cast<const f32x4 *>(pm + row * MP + 32 * s + 8 * g + 4 * i);
                 }
         }
         if (w == 0) {
@@ -552,17 +549,19 @@ __device__ __forceinline__ bf16x4 transposed(const bf16x4 *place)
 
 // Waves 0 to 3 carry S, waves 4 to 7 make the outputs. Three exchanges
 // through LDS a chunk, each ended by a barrier that all eight waves meet:
-//   chain wave w: its rows' share of K S; its rows of S in two parts  -> xp; ssh
+//   chain wave w: its rows' share of K S; its rows of S in three parts -> xp; ssh
 //   chain wave w: token tile w of Y in three parts                    -> ysh
 //   chain wave w: token tile w of U, for S' in three parts and for O  -> ush; uo
 // then chain wave w updates its rows of S. Output wave w takes Q S between the
-// first two barriers, stores the chunk before between the second and the
-// third, and after it brings V and the row factors of the next chunk and adds
-// P U. The time of a chunk is the chain's latencies, not its arithmetic, so
-// whatever is not the chain is left to the output waves, and every operand is
-// loaded right after its last use, a chunk ahead. (16384 tokens: 758 us with
-// four waves that did all, 467 with this split, 412-430 with K^T transposed out of
-// LDS instead of loaded beside K.)
+// first two barriers, stores the chunk before and splits its rows of P between
+// the second and the third, and after it brings V and the row factors of the
+// next chunk and adds P U. The time of a chunk is the chain's latencies, not
+// its arithmetic, so whatever is not the chain is left to the output waves, and
+// every operand is loaded right after its last use, a chunk ahead. (16384
+// tokens, this kernel: 758 us with four waves that did all, 467 with the split,
+// 430 with K^T transposed out of LDS instead of loaded beside K; that with two
+// parts of S, U and P for the outputs, 2^-17, and 465 with all three. P split
+// only where it is used, 16384 tokens are no slower, and 16 heads of 64 x 64 4 %.)
 // VEC: v's rows of 16 columns are two 16-byte pieces and o's take 8-byte
 // stores (a host rule; as a branch inside, it made the compiler wait for
 // every load at its end).
@@ -572,7 +571,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
     using W = Space<DT, false>;
     const DeltaProblem &p = a.p;
     __shared__ f32x4 xp[4][4][64], uo[4][64];
-    __shared__ bf16x8 ssh[2][4][64];
+    __shared__ bf16x8 ssh[3][4][64];
     __shared__ bf16x4 ysh[3][4][64], ush[3][4][64];
     __shared__ bf16x4 ksh[4][4][DT][64];            // chain wave w's K, for its transposed reads
     __shared__ f32x4 vsh[4][64], factors[4][2][4];  // factors: r exp G, then r exp(G_63 - G)
@@ -617,7 +616,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 
     if (w8 >= 4) {
         // ---- Output wave w: token tile w of O, as rows of columns 4g .. 4g + 3, token r.
-        bf16x8 qf[4], pf[2][2];
+        bf16x8 qf[4];
+        f32x4 pf[2][2];
         float upq = 0.f;
         int bad_here = NEVER, badall = NEVER;
         auto load_q = [&](int c) __attribute__((always_inline)) {
@@ -627,12 +627,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
                 qf[i] = frag(key, i);
         };
         auto load_p = [&](int c) __attribute__((always_inline)) {
-            const uint8_t *val = val0 + c * val_step, *pv = val + W::P + 2 * low_frag(w, 0) * FRAG;
+            const uint8_t *pv = val0 + c * val_step + W::P + 2 * low_frag(w, 0) * FRAG;
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    pf[s][i] = frag(pv, 2 * s + i);     // s = 1 of waves 0 and 1: the next wave's, not used
+                    pf[s][i] = __builtin_bit_cast(f32x4, frag(pv, 2 * s + i));  // s = 1 of waves 0 and 1: the next wave's, not used
+        };
+        auto load_rows = [&](int c) __attribute__((always_inline)) {
+            const uint8_t *val = val0 + c * val_step;
             upq = reinterpret_cast<const float *>(val + W::UPQ)[tokr];
             bad_here = reinterpret_cast<const int *>(val + W::HEAD)[1];
         };
@@ -679,10 +682,25 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
             load_v(min(1, chunks - 1));
             load_q(0);
             load_p(0);
+            load_rows(0);
         }
         uint16_t *oh = static_cast<uint16_t *>(p.o) + (begin + tokr) * p.ost + h * p.osh + col0 + 4 * g;
         f32x4 o;
-        // The second term of chunk c's outputs, U in two parts.
+        // P in parts, before the phase that needs them.
+        bf16x8 pp[2][3];
+        auto split_p = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (2 * s <= w) {
+                    bf16x4 lo[3], hi[3];
+                    split<3>(pf[s][0], lo);
+                    split<3>(pf[s][1], hi);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        pp[s][i] = join(lo[i], hi[i]);
+                }
+        };
+        // The second term of chunk c's outputs.
         auto add_pu = [&](int c) __attribute__((always_inline)) {
             // Nothing that looks at these two may move up to their load, a
             // phase earlier: it would wait there.
@@ -695,13 +713,18 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
                 if (2 * s <= w) {
                     f32x4 ua = uo[2 * s][lane], ub = uo[2 * s + 1][lane];
                     finite_u(ua, ub, &badcol[r], c * C + 32 * s + 8 * g, 4);
-                    bf16x4 lo[2], hi[2];
-                    split<2>(ua, lo);
-                    split<2>(ub, hi);
-                    const bf16x8 u0 = join(lo[0], hi[0]), u1 = join(lo[1], hi[1]);
-                    o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u1, pf[s][0], o, 0, 0, 0);
-                    o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][1], o, 0, 0, 0);
-                    o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u0, pf[s][0], o, 0, 0, 0);
+                    bf16x4 lo[3], hi[3];
+                    bf16x8 u[3];
+                    split<3>(ua, lo);
+                    split<3>(ub, hi);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        u[i] = join(lo[i], hi[i]);
+#pragma unroll
+                    for (int k = 2; k >= 0; --k)
+#pragma unroll
+                        for (int i = 0; i <= k; ++i)
+                            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u[k - i], pp[s][i], o, 0, 0, 0);
                 }
         };
         auto store = [&](int c) __attribute__((always_inline)) {
@@ -730,20 +753,22 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 1; j >= 0; --j)
+                for (int j = 2; j >= 0; --j)
                     q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ssh[j][i][lane], qf[i], q, 0, 0, 0);
             load_q(min(c + 1, chunks - 1));
             lds_barrier();
             if (c > 0)
                 store(c - 1);
             o = q;
+            split_p();
+            load_p(min(c + 1, chunks - 1));
             lds_barrier();
             // For the next chunk: the chain reads them between the next two
             // barriers, and took its last look at this chunk's before the one above.
             give_v();
             load_v(min(c + 2, chunks - 1));
             add_pu(c);
-            load_p(min(c + 1, chunks - 1));
+            load_rows(min(c + 1, chunks - 1));
         }
         if (chunks > 0)
             store(chunks - 1);
@@ -819,7 +844,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
         for (int i = 0; i < 4; ++i)
             xp[w][i][lane] = acc[i];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 3; ++j)
             ssh[j][w][lane] = join(lo[j], hi[j]);
         load_k(next);
         lds_barrier();

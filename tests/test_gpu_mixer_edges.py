@@ -78,3 +78,23 @@ def test_delta_overflow_reaches_no_earlier_token(which, variant, dtype):
     assert not good[T + over:2 * T].any() and not torch.isfinite(fin[1]).any()
     o0, bo, _, _ = ref.delta(q[:tame], k[:tame], v[:tame], g[:tame], beta[:tame], 0.125, False, [tame], None)
     ref.check(o[T:T + tame], o0, bo, "o before")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("variant", [cf.VARIANT_DIRECT, cf.VARIANT_TILED])
+def test_delta_outputs_hold_32_bits(variant, dtype):
+    """One key direction and beta 1: each token's value replaces the row it is written to, so o = scale v, as the sum of
+    the old row (some 1000) and its negative. 33 roundings on the way, of terms no larger than those two: the rows and U
+    in three parts, P likewise (4), the products of the parts (3, 3, 6, 12), Y, its factor and U in three parts."""
+    T, D, Dv = 70, 64, 48
+    q = torch.zeros(T, 1, D)
+    q[..., 0] = 1
+    v = rnd((T, 1, Dv), 371, std=0.05).to(dtype)
+    g, beta = torch.zeros(T, 1), torch.ones(T, 1)
+    state = torch.zeros(1, 1, D, Dv)
+    state[0, 0, 0] = 600 + 400 * torch.rand(Dv, generator=torch.Generator().manual_seed(372))
+    scale = torch.tensor(0.7).item()        # 24 significant bits
+    o = cf.gated_delta_rule(q.to(dtype).to(DEV), q.to(dtype).to(DEV), v.to(DEV), g.to(DEV), beta.to(DEV), scale=scale,
+                            initial_state=state.to(DEV), variant=variant)
+    bound = 33 * ref.U * scale * (state[0, 0, 0].double() + 2 * v.double().abs())
+    ref.check(o, scale * v.double(), bound, "o")
