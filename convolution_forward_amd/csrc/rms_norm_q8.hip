@@ -40,20 +40,21 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 // Both reductions over the WPR waves of a row.
 template <int WPR>
 struct Reduce {
-    float part[WPR > 1 ? WPR : 1];
+    float part[2][WPR > 1 ? WPR : 1];
     uint32_t tops[WPR > 1 ? WPR : 1];
 
-    __device__ __forceinline__ float sum(float v, int wave)
+    // `again`: the row's second sum.
+    __device__ __forceinline__ float sum(float v, int wave, int again = 0)
     {
         v = wave_sum(v);
         if constexpr (WPR > 1) {
             if ((threadIdx.x & 63) == 0)
-                part[wave] = v;
+                part[again][wave] = v;
             __syncthreads();
             v = 0.f;
 #pragma unroll
             for (int i = 0; i < WPR; ++i)
-                v += part[i];
+                v += part[again][i];
         }
         return v;
     }
@@ -72,6 +73,19 @@ struct Reduce {
         return v;
     }
 };
+
+// A mean square this small (only an eps as small allows it) has lost bits
+// below fp32's range: such rows are squared again, times 2^100.
+constexpr float TINY = 0x1p-96f, LIFT = 0x1p100f;
+
+__device__ __forceinline__ float mean_square(float sum, const NormProblem &p) { return sum / (float)p.width + p.eps; }
+__device__ __forceinline__ float lifted_mean_square(float sum, const NormProblem &p)
+{
+    return sum / (float)p.width + p.eps * LIFT * LIFT;
+}
+
+// (A row of zeros without an eps stays zeros.)
+__device__ __forceinline__ float root_inverse(float ms) { return ms == 0.f ? 0.f : 1.f / sqrtf(ms); }
 
 // Writes the row's scale; y * lift * inv is what is rounded. lift is 1, or
 // 2^100 where top is so small that QMAX / top would overflow.
@@ -183,7 +197,20 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rms_norm_q8_kernel(
     for (int i = 0; i < NV; ++i)
         r[i] = load_piece<false>(w + (at + i * 64 * WPR) * V, p.width - (at + i * 64 * WPR) * V);
     sum = red.sum(sum, wave);
-    const float rinv = 1.f / sqrtf(sum / (float)p.width + p.eps);
+    float ms = mean_square(sum, p);
+    if (__builtin_expect(ms < TINY, 0)) {       // the same for all of the row's waves
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                y[i][j] *= LIFT;
+                sum = fmaf(y[i][j], y[i][j], sum);
+            }
+        sum = red.sum(sum, wave, 1);
+        ms = lifted_mean_square(sum, p);
+    }
+    const float rinv = root_inverse(ms);
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -238,16 +265,27 @@ __global__ __launch_bounds__(64 * LONG_WAVES) void rms_norm_q8_long_kernel(NormP
         sum = fmaf(v, v, sum);
     }
     sum = red.sum(sum, wave);
-    const float rinv = 1.f / sqrtf(sum / (float)p.width + p.eps);
     const T *src = r ? h : x;               // each thread reads back what it wrote
+    float ms = mean_square(sum, p), up = 1.f;
+    if (ms < TINY) {
+        up = LIFT;
+        sum = 0.f;
+        for (int j = threadIdx.x; j < p.width; j += NT) {
+            const float v = load_as_f32(src + j) * up;
+            sum = fmaf(v, v, sum);
+        }
+        sum = red.sum(sum, wave, 1);
+        ms = lifted_mean_square(sum, p);
+    }
+    const float rinv = root_inverse(ms);
     uint32_t top = 0;
     for (int j = threadIdx.x; j < p.width; j += NT)
-        top = max(top, __float_as_uint(fabsf(load_as_f32(src + j) * rinv * load_as_f32(w + j))));
+        top = max(top, __float_as_uint(fabsf(load_as_f32(src + j) * up * rinv * load_as_f32(w + j))));
     top = red.top(top, wave);
     const Quant z = quant_scale<E4M3>(sum, top, p.scale + row, threadIdx.x == 0);
     uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.qs;
     for (int j = threadIdx.x; j < p.width; j += NT)
-        q[j] = z.fine ? (uint8_t)to_eight4<E4M3>(load_as_f32(src + j) * rinv * load_as_f32(w + j) * z.lift * z.inv, 0.f, 0.f, 0.f) : 0;
+        q[j] = z.fine ? (uint8_t)to_eight4<E4M3>(load_as_f32(src + j) * up * rinv * load_as_f32(w + j) * z.lift * z.inv, 0.f, 0.f, 0.f) : 0;
 }
 
 template <class T, int WPR, int NV, bool E4M3>

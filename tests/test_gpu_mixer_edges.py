@@ -4,7 +4,7 @@ import torch
 
 import convolution_forward_amd as cf
 import mixer_ref as ref
-from test_gpu_mixer import BF, DEV, F32, delta_inputs, rnd
+from test_gpu_mixer import BF, DEV, E4, F32, I8, check_norm, delta_inputs, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -22,6 +22,24 @@ def test_workspace_is_contiguous_bytes(make):
     o = cf.gated_delta_rule(q, k, v, g, beta, workspace=torch.empty(n, dtype=torch.uint8, device=DEV),
                             variant=cf.VARIANT_TILED)
     assert torch.equal(o, cf.gated_delta_rule(q, k, v, g, beta, variant=cf.VARIANT_TILED))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("qdt", [I8, E4])
+@pytest.mark.parametrize("width", [300, 3000, 40000])
+def test_norm_without_eps(width, qdt, dtype):
+    """Rows of zeros have scale 0 and q 0; rows whose squares leave fp32's range are normed like others."""
+    x = rnd((6, width), 22, dtype)
+    x[0] = 0
+    x[1] = -0.0
+    x[2] *= 1e-22
+    x[3] *= 1e-36
+    x[4] = 0
+    x[4, width - 1] = -1e-38
+    w = rnd(width, 23, dtype)
+    q, s, _ = cf.rms_norm_q8(x.to(DEV), w.to(DEV), eps=0.0, out_dtype=qdt)
+    assert (s[:2] == 0).all() and (q[:2].to(F32) == 0).all()
+    check_norm(q[2:], s[2:], None, x[2:], w, None, 0.0, qdt)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
