@@ -241,13 +241,15 @@ void launch_rows(const DeltaProblem &p, hipStream_t s)
         hipLaunchKernelGGL((delta_direct_kernel<T, R, CL, false>), grid, block, 0, s, p, slices);
 }
 
+bool single_tokens(int64_t tokens, int num_seqs) { return tokens <= 4 * (int64_t)num_seqs; }
+
 template <class T>
 void launch(const DeltaProblem &p, hipStream_t s)
 {
     // 32 columns a wave against 16, 32 heads: one token 4.3 us against 5.2, of
     // 128 sequences 101 against 107; four tokens 7.3 either way; eight 11.1
     // against 9.9. (Past 128 rows the registers hold 16 columns a wave only.)
-    const bool single = p.seq.tokens <= 4 * (int64_t)p.seq.num_seqs;
+    const bool single = single_tokens(p.seq.tokens, p.seq.num_seqs);
     if (p.Dk <= 64)
         single ? launch_rows<T, 8, 8>(p, s) : launch_rows<T, 4, 4>(p, s);
     else if (p.Dk <= 128)
@@ -258,10 +260,15 @@ void launch(const DeltaProblem &p, hipStream_t s)
 
 }  // namespace
 
+// The grid's threads stay below 2^32 (64 a wave, up to three waves idle).
+bool delta_direct_supports(int64_t tokens, int num_seqs, int Hv, int Dk, int Dv)
+{
+    const int columns = single_tokens(tokens, num_seqs) && Dk <= 128 ? 32 : 16;
+    return (int64_t)num_seqs * Hv * ((Dv + columns - 1) / columns) <= (int64_t(1) << 26) - 4;
+}
+
 hipError_t launch_delta_direct(const DeltaProblem &p, hipStream_t s)
 {
-    if ((int64_t)p.seq.num_seqs * p.Hv * ((p.Dv + 15) / 16) > (int64_t(1) << 32))
-        return hipErrorInvalidValue;
     if (p.dtype == CONV_BF16)
         launch<uint16_t>(p, s);
     else

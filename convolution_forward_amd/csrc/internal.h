@@ -160,6 +160,7 @@ struct DeltaProblem {
     conv_dtype dtype;
 };
 
+bool delta_direct_supports(int64_t tokens, int num_seqs, int Hv, int Dk, int Dv);
 hipError_t launch_delta_direct(const DeltaProblem &p, hipStream_t s);
 bool delta_chunked_supports(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, int Dv);
 int64_t delta_chunked_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, conv_dtype dtype);

@@ -137,12 +137,10 @@ conv_status check_delta_sizes(int64_t tokens, int num_seqs, int Hk, int Hv, int 
     // 22.7), 59 for 8 sequences (48 tokens 56, 64 71), 360 to 400 for 64 (344, 454).
     const bool alone = (int64_t)num_seqs * Hv * ((Dv + 15) / 16) <= 256;
     const int least = dtype == CONV_F32 ? (alone ? 28 : 50) : alone ? 16 : 26;
-    switch (variant) {
-    case CONV_VARIANT_AUTO: *tiled = can && tokens > least * (int64_t)num_seqs; return CONV_OK;
-    case CONV_VARIANT_DIRECT: *tiled = false; return CONV_OK;
-    case CONV_VARIANT_TILED: *tiled = true; return can ? CONV_OK : CONV_ERR_UNSUPPORTED;
-    default: return CONV_ERR_UNSUPPORTED;
-    }
+    if (variant != CONV_VARIANT_AUTO && variant != CONV_VARIANT_DIRECT && variant != CONV_VARIANT_TILED)
+        return CONV_ERR_UNSUPPORTED;
+    *tiled = variant == CONV_VARIANT_TILED || (variant == CONV_VARIANT_AUTO && can && tokens > least * (int64_t)num_seqs);
+    return (*tiled ? can : delta_direct_supports(tokens, num_seqs, Hv, Dk, Dv)) ? CONV_OK : CONV_ERR_UNSUPPORTED;
 }
 
 }  // namespace

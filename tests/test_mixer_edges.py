@@ -2,7 +2,11 @@
 import re
 import subprocess
 
+import pytest
+
+import convolution_forward_amd as cf
 from convolution_forward_amd import build
+from test_mixer_abi import DELTA, lib  # noqa: F401  (fake addresses: nothing may be launched)
 
 
 def test_conv_promises_no_more_alignment_than_is_checked(tmp_path):
@@ -20,3 +24,16 @@ def test_conv_promises_no_more_alignment_than_is_checked(tmp_path):
         assert aligned and max(aligned) <= max(most, 4), form[0]    # (biases and offsets are 4-byte values)
         seen += 1
     assert seen == 28       # two types, two widths, 2 to 8 taps
+
+
+@pytest.mark.parametrize("variant", [cf.VARIANT_AUTO, cf.VARIANT_DIRECT])
+def test_delta_past_a_grid_is_unsupported(lib, variant):  # noqa: F811
+    """Token by token a wave takes 32 columns of single tokens and 16 of others: 2^26 waves are 2^32 threads."""
+    n = 1 << 20
+    sizes = dict(T=n, n=n, Hk=2, Hv=4, Dk=64, Dv=512)
+    call = {**DELTA, **sizes, "off": None, "slots": None, "si": None, "so": None, "variant": variant}
+    assert lib.conv_delta_rule_fwd(*call.values()) == cf.CONV_ERR_UNSUPPORTED
+    assert cf.delta_rule_workspace(*sizes.values(), variant=variant) == -1
+    assert cf.delta_rule_workspace(n, n, 2, 4, 64, 480, variant=variant) == 0
+    assert cf.delta_rule_workspace(8 * n, n, 2, 4, 64, 256, variant=variant) == -1
+    assert cf.delta_rule_workspace(8 * n, n, 2, 4, 64, 240, variant=variant) == 0
