@@ -203,10 +203,14 @@ void launch(const Causal1dProblem &p, hipStream_t s)
 
 }  // namespace
 
+// Threads of a grid's first axis below 2^32, its second axis within 2^16.
+bool causal1d_supports(const Causal1dProblem &p)
+{
+    return seq_tiles(p.seq, TT) < (int64_t(1) << 24) && p.channels <= (1 << 23);
+}
+
 hipError_t launch_causal1d(const Causal1dProblem &p, hipStream_t s)
 {
-    if (seq_tiles(p.seq, TT) >= (int64_t(1) << 24) || p.channels > (1 << 23))
-        return hipErrorInvalidValue;
     if (p.dtype == CONV_BF16)
         launch<uint16_t>(p, s);
     else

@@ -142,6 +142,7 @@ struct Causal1dProblem {
     conv_dtype dtype;
 };
 
+bool causal1d_supports(const Causal1dProblem &p);
 hipError_t launch_causal1d(const Causal1dProblem &p, hipStream_t s);
 
 // A validated gated delta rule.

@@ -263,6 +263,8 @@ conv_status conv_causal1d_fwd(const void *x, int64_t x_stride, const void *w, co
     p.taps = taps;
     p.silu = silu;
     p.dtype = dtype;
+    if (!causal1d_supports(p))
+        return CONV_ERR_UNSUPPORTED;
     return launched(launch_causal1d(p, (hipStream_t)stream));
 }
 

@@ -6,7 +6,7 @@ import pytest
 
 import convolution_forward_amd as cf
 from convolution_forward_amd import build
-from test_mixer_abi import DELTA, lib  # noqa: F401  (fake addresses: nothing may be launched)
+from test_mixer_abi import CONV, DELTA, lib  # noqa: F401  (fake addresses: nothing may be launched)
 
 
 def test_conv_promises_no_more_alignment_than_is_checked(tmp_path):
@@ -37,3 +37,9 @@ def test_delta_past_a_grid_is_unsupported(lib, variant):  # noqa: F811
     assert cf.delta_rule_workspace(n, n, 2, 4, 64, 480, variant=variant) == 0
     assert cf.delta_rule_workspace(8 * n, n, 2, 4, 64, 256, variant=variant) == -1
     assert cf.delta_rule_workspace(8 * n, n, 2, 4, 64, 240, variant=variant) == 0
+
+
+@pytest.mark.parametrize("change", [dict(T=1 << 29, C=16, xs=16, ys=16), dict(C=(1 << 23) + 8, xs=1 << 24, ys=1 << 24)])
+def test_conv_past_a_grid_is_unsupported(lib, change):  # noqa: F811
+    call = {**CONV, "si": None, "so": None, **change}
+    assert lib.conv_causal1d_fwd(*call.values()) == cf.CONV_ERR_UNSUPPORTED
