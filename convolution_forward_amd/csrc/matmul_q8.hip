@@ -39,7 +39,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int KS = 128;                 // K bytes of a piece
 constexpr uint32_t OOB = 0x80000000u;
@@ -460,8 +459,6 @@ hipError_t launch_tiles(Q8Args &a, hipStream_t s)
     a.group = 8;
     a.stages = (a.pieces + SUB - 1) / SUB;
     const int64_t tiles = (int64_t)a.mt * a.nt;
-    if (tiles > (int64_t(1) << 30))
-        return hipErrorInvalidValue;
     const hipError_t attr = allow_lds<matmul_q8_kernel<MB, NB, WM, WN, SUB, NS, E4M3, OB, ALIGNED>>(lds);
     if (attr != hipSuccess)
         return attr;
@@ -469,6 +466,10 @@ hipError_t launch_tiles(Q8Args &a, hipStream_t s)
                        dim3(64 * WM * WN), lds, s, a);
     return hipGetLastError();
 }
+
+// Tiles, and whether a grid of them (whole eights of workgroups) stays below 2^32 threads.
+int64_t tiles_of(int64_t M, int N, int tm, int tn) { return ((M + tm - 1) / tm) * (((int64_t)N + tn - 1) / tn); }
+bool fits(int64_t workgroups, int threads) { return (workgroups + 7) / 8 * 8 * threads < (int64_t(1) << 32); }
 
 template <int MB, bool E4M3, bool OB, bool ALIGNED>
 hipError_t launch_few(const Q8Args &a, hipStream_t s)
@@ -484,9 +485,10 @@ hipError_t launch(Q8Args &a, hipStream_t s)
     // Up to 32 tokens the few-token form is the faster one (8 x 4096 x 4096:
     // 6.5 us against 9.4 on 64x64 tiles; 32: 9.0 against 9.7), past that the
     // tiles are (64 x 8192 x 4096: 13.9 us against 24).
-    if (a.M <= 16)
+    const bool few = fits(((int64_t)a.N + 15) / 16, 64 * SW);
+    if (a.M <= 16 && few)
         return launch_few<1, E4M3, OB, ALIGNED>(a, s);
-    if (a.M <= 32)
+    if (a.M <= 32 && few)
         return launch_few<2, E4M3, OB, ALIGNED>(a, s);
     // The tile whose rounds over the 256 compute units cost least. A round's
     // cost is its time at K = 4096 over the 64x64 tile's (int8, from 32x64 up:
@@ -496,8 +498,8 @@ hipError_t launch(Q8Args &a, hipStream_t s)
     // 4096: 64x128 14.7, 64x64 17.7, 128x128 19; 64 x 8192 x 4096: 32x64 11.0,
     // 64x64 12.5, in e4m3 13.9 and 16.1; 256 x 4096 x 4096: 64x64 9.2, 32x64 11.4.)
     auto cost = [&](int tm, int tn, int each) {
-        const int64_t tiles = (int64_t)((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn);
-        return (tiles + 255) / 256 * each;
+        const int64_t tiles = tiles_of(a.M, a.N, tm, tn);
+        return fits(tiles, 512) ? (tiles + 255) / 256 * each : INT64_MAX;
     };
     const int64_t costs[6] = {cost(256, 256, 48), cost(128, 256, 31), cost(128, 128, 20), cost(64, 128, 14),
                               cost(64, 64, 10), cost(32, 64, 9)};
@@ -517,10 +519,10 @@ hipError_t launch(Q8Args &a, hipStream_t s)
 
 }  // namespace
 
-// Every stride must let a tile's byte offsets stay below 2^31.
+// Every stride must let a tile's byte offsets stay below 2^31, and the largest tiles must fit a grid.
 bool matmul_q8_tiled_supports(const MatmulQ8Problem &p)
 {
-    return p.xs <= (1 << 22) && p.ws <= (1 << 22) && p.M <= (1 << 30);
+    return p.xs <= (1 << 22) && p.ws <= (1 << 22) && fits(tiles_of(p.M, p.N, 256, 256), 512);
 }
 
 hipError_t launch_matmul_q8(const MatmulQ8Problem &p, hipStream_t s)

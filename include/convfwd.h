@@ -378,8 +378,11 @@ CONVFWD_API conv_status conv_rms_norm_q8_fwd(const void *x, int64_t x_stride, co
  *   w        device [N,K], row stride w_stride >= K, q_dtype: one row an output channel.
  *   x_scale  device [M] fp32.   w_scale  device [N] fp32.   bias  device [N] fp32 or NULL.
  *   y        device [M,N], row stride y_stride >= N, y_dtype (CONV_F32 or CONV_BF16).
- *   variant  CONV_VARIANT_AUTO or _TILED (matrix cores), or _DIRECT (one
- *            thread per output); every variant takes every shape.
+ *   variant  CONV_VARIANT_TILED (matrix cores): x_stride and w_stride up to
+ *            2^22 and fewer than 2^23 tiles of 256 tokens by 256 channels,
+ *            CONV_ERR_UNSUPPORTED otherwise. CONV_VARIANT_DIRECT: one thread
+ *            per output, every shape. CONV_VARIANT_AUTO: the first, or the
+ *            second where the first does not take the shape.
  */
 CONVFWD_API conv_status conv_matmul_q8_fwd(const void *x, int64_t x_stride, const float *x_scale, const void *w,
                                            int64_t w_stride, const float *w_scale, const float *bias, void *y,

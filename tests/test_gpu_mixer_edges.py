@@ -116,3 +116,15 @@ def test_delta_outputs_hold_32_bits(variant, dtype):
                             initial_state=state.to(DEV), variant=variant)
     bound = 33 * ref.U * scale * (state[0, 0, 0].double() + 2 * v.double().abs())
     ref.check(o, scale * v.double(), bound, "o")
+
+
+@pytest.mark.parametrize("m", [2, 20, 40])
+def test_product_of_many_channels(m):
+    """More channels than the few-token form's grid holds (2^27), or a grid of small tiles; sums of 8 are exact."""
+    n, k = 2 ** 27 + 40, 8
+    gen = torch.Generator(device=DEV).manual_seed(410)
+    x, w = (torch.randint(-127, 128, (rows, k), generator=gen, device=DEV, dtype=I8) for rows in (m, n))
+    y = cf.matmul_q8(x, torch.ones(m, device=DEV), w, torch.ones(n, device=DEV))
+    for at in range(0, n, 2 ** 24):
+        part = slice(at, at + 2 ** 24)
+        assert torch.equal(y[:, part], (x.float() @ w[part].float().t()).to(BF))

@@ -6,7 +6,7 @@ import pytest
 
 import convolution_forward_amd as cf
 from convolution_forward_amd import build
-from test_mixer_abi import CONV, DELTA, lib  # noqa: F401  (fake addresses: nothing may be launched)
+from test_mixer_abi import CONV, DELTA, PRODUCT, lib  # noqa: F401  (fake addresses: nothing may be launched)
 
 
 def test_conv_promises_no_more_alignment_than_is_checked(tmp_path):
@@ -43,3 +43,9 @@ def test_delta_past_a_grid_is_unsupported(lib, variant):  # noqa: F811
 def test_conv_past_a_grid_is_unsupported(lib, change):  # noqa: F811
     call = {**CONV, "si": None, "so": None, **change}
     assert lib.conv_causal1d_fwd(*call.values()) == cf.CONV_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("change", [dict(M=1 << 23, N=1 << 17, ys=1 << 17), dict(xs=(1 << 22) + 1), dict(ws=(1 << 22) + 1)])
+def test_product_tiles_past_their_limits_are_unsupported(lib, change):  # noqa: F811
+    call = {**PRODUCT, "b": None, **change, "variant": cf.VARIANT_TILED}
+    assert lib.conv_matmul_q8_fwd(*call.values()) == cf.CONV_ERR_UNSUPPORTED
