@@ -362,4 +362,17 @@ def copy_bytes(src, dst, nbytes: int | None = None, wide: bool = False):
     return dst
 
 
-from .mixer import causal_conv1d, delta_rule_workspace, gated_delta_rule, matmul_q8, rms_norm_q8  # noqa: E402,F401
+_MIXER = ("causal_conv1d", "delta_rule_workspace", "gated_delta_rule", "matmul_q8", "rms_norm_q8")
+
+
+def __getattr__(name):
+    """The token-mixer calls, on first use: mixer.py imports torch, the rest does so only when called with tensors."""
+    if name not in _MIXER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import mixer
+    globals().update((n, getattr(mixer, n)) for n in _MIXER)
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_MIXER})

@@ -1,6 +1,7 @@
 """The token-mixer operators on the host: what the compiled code assumes, and the limits of what a call accepts."""
 import re
 import subprocess
+import sys
 
 import pytest
 
@@ -49,3 +50,12 @@ def test_conv_past_a_grid_is_unsupported(lib, change):  # noqa: F811
 def test_product_tiles_past_their_limits_are_unsupported(lib, change):  # noqa: F811
     call = {**PRODUCT, "b": None, **change, "variant": cf.VARIANT_TILED}
     assert lib.conv_matmul_q8_fwd(*call.values()) == cf.CONV_ERR_UNSUPPORTED
+
+
+def test_import_leaves_torch_alone():
+    """The C library's handle and constants need no torch; the mixer's names are there all the same."""
+    code = ("import sys, convolution_forward_amd as cf; assert 'torch' not in sys.modules; cf.load_library; "
+            "assert 'matmul_q8' in dir(cf) and not hasattr(cf, 'matmul_q9') and 'torch' not in sys.modules; "
+            "from convolution_forward_amd import rms_norm_q8; assert cf.rms_norm_q8 is rms_norm_q8 is cf.mixer.rms_norm_q8")
+    r = subprocess.run([sys.executable, "-c", code], cwd=build.ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
