@@ -4,11 +4,13 @@ binding of the token-mixer calls (_mixer.so, host code only), in-tree.
     python -m convolution_forward_amd.build
 
 Each source compiles to an object under _build/ (in parallel), then hipcc
-links the shared library into convolution_forward_amd/_lib/.
+links the shared library into convolution_forward_amd/_lib/. Without torch the
+C library is built alone.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
@@ -22,6 +24,7 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libconvfwd.so")
 BINDING = os.path.join(PKG, "binding", "mixer_binding.cpp")
 BINDING_PATH = os.path.join(LIB_DIR, "_mixer.so")
+BINDING_STAMP = os.path.join(BUILD_DIR, "_mixer.stamp")     # the command and torch that made it
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -61,6 +64,16 @@ def _up_to_date(src: str, obj: str) -> bool:
     return all(os.path.getmtime(d) < t for d in deps)
 
 
+def _binding_up_to_date(stamp: str) -> bool:
+    """The binding newer than what it includes, and made by the same command with the same torch."""
+    if not (os.path.exists(BINDING_PATH) and os.path.exists(BINDING_STAMP)):
+        return False
+    deps = [BINDING, os.path.abspath(__file__)] + [os.path.join(INCLUDE, h) for h in os.listdir(INCLUDE)]
+    t = os.path.getmtime(BINDING_PATH)
+    with open(BINDING_STAMP) as fh:
+        return fh.read() == stamp and all(os.path.getmtime(d) < t for d in deps)
+
+
 def _compile(src: str, incremental: bool = False) -> str:
     obj = os.path.join(BUILD_DIR, src + ".o")
     if incremental and _up_to_date(src, obj):
@@ -75,24 +88,28 @@ def _compile(src: str, incremental: bool = False) -> str:
     return obj
 
 
-def build_binding(incremental: bool = False) -> str:
-    """Compile the torch binding against the installed torch and link it to libconvfwd.so beside it."""
+def build_binding(incremental: bool = False) -> str | None:
+    """Compile the torch binding against the installed torch and link it to libconvfwd.so beside it; None without torch."""
     import sysconfig
+    if importlib.util.find_spec("torch") is None:
+        return None
+    import torch
     from torch.utils import cpp_extension
-    deps = [BINDING, os.path.abspath(__file__)] + [os.path.join(INCLUDE, h) for h in os.listdir(INCLUDE)]
-    if incremental and os.path.exists(BINDING_PATH) and \
-            all(os.path.getmtime(d) < os.path.getmtime(BINDING_PATH) for d in deps):
-        return BINDING_PATH
     dirs = cpp_extension.include_paths("cuda") + [sysconfig.get_paths()["include"], INCLUDE]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1",
            "-DUSE_ROCM=1"]
     cmd += [f"-isystem{d}" for d in dirs[:-1]] + ["-I" + INCLUDE, BINDING, "-o", BINDING_PATH + ".tmp", "-L" + LIB_DIR,
                                                   "-lconvfwd", "-Wl,-rpath,$ORIGIN"]
     cmd += [f"-L{d}" for d in cpp_extension.library_paths("cuda")] + ["-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+    stamp = "\n".join([torch.__version__, *cmd])
+    if incremental and _binding_up_to_date(stamp):
+        return BINDING_PATH
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for {BINDING}:\n{res.stdout}\n{res.stderr}")
     os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    with open(BINDING_STAMP, "w") as fh:
+        fh.write(stamp)
     return BINDING_PATH
 
 
@@ -110,9 +127,10 @@ def build(jobs: int | None = None, verbose: bool = False, incremental: bool = Fa
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
-    build_binding(incremental)
+    binding = build_binding(incremental)
     if verbose:
-        print(f"built {LIB_PATH} from {len(srcs)} sources, and {BINDING_PATH}")
+        print(f"built {LIB_PATH} from {len(srcs)} sources, " +
+              (f"and {binding}" if binding else "without the token-mixer binding: torch is not installed"))
     return LIB_PATH
 
 

@@ -1,4 +1,5 @@
 """The token-mixer operators on the host: what the compiled code assumes, and the limits of what a call accepts."""
+import importlib.util
 import re
 import subprocess
 import sys
@@ -59,3 +60,41 @@ def test_import_leaves_torch_alone():
             "from convolution_forward_amd import rms_norm_q8; assert cf.rms_norm_q8 is rms_norm_q8 is cf.mixer.rms_norm_q8")
     r = subprocess.run([sys.executable, "-c", code], cwd=build.ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_build_without_torch(monkeypatch, tmp_path):
+    """Without torch there is no binding to build, and the C library's build goes on."""
+    monkeypatch.setattr(build, "_compile", lambda src, incremental: src)
+    linked = []
+
+    def run(cmd, **kw):
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        linked.append(cmd)
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    monkeypatch.setitem(sys.modules, "torch", None)
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name: None)
+    monkeypatch.setattr(build, "LIB_DIR", str(tmp_path))
+    monkeypatch.setattr(build, "LIB_PATH", str(tmp_path / "libconvfwd.so"))
+    monkeypatch.setattr(build, "BINDING_PATH", str(tmp_path / "_mixer.so"))
+    build.build()
+    assert len(linked) == 1
+
+
+def test_incremental_build_notices_another_torch(monkeypatch, tmp_path):
+    import torch
+    made = []
+
+    def run(cmd, **kw):
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        made.append(cmd)
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    monkeypatch.setattr(build, "BINDING_PATH", str(tmp_path / "_mixer.so"))
+    monkeypatch.setattr(build, "BINDING_STAMP", str(tmp_path / "stamp"), raising=False)
+    for version, builds in (("1", 1), ("1", 1), ("2", 2)):
+        monkeypatch.setattr(torch, "__version__", version)
+        build.build_binding(incremental=True)
+        assert len(made) == builds
