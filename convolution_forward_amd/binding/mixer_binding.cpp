@@ -156,6 +156,13 @@ int64_t row_stride(const Tensor &t, const char *what, int64_t width, int64_t row
            t.scalar_type(), " with strides ", t.strides());
 }
 
+int small(int64_t v, const char *what)
+{
+    if (v > INT32_MAX)
+        refuse(what, " of ", v, " is too large");
+    return (int)v;
+}
+
 // (tokens, sequences) of a tensor [batch, length, ...] or [tokens, ...] whose last `tail` axes are not tokens.
 struct Seqs {
     int64_t tokens;
@@ -168,7 +175,7 @@ Seqs sequences(const Tensor &t, int64_t tail, const Tensor *offsets)
     if (dim == 2) {
         if (offsets)
             refuse("seq_offsets go with [tokens, ...] tensors");
-        return {t.size(0) * t.size(1), (int)t.size(0)};
+        return {t.size(0) * t.size(1), small(t.size(0), "a count of sequences")};
     }
     if (dim != 1)
         refuse("expected [batch, length, ...] or [tokens, ...], got ", t.sizes());
@@ -176,7 +183,7 @@ Seqs sequences(const Tensor &t, int64_t tail, const Tensor *offsets)
         return {t.size(0), 1};
     if (offsets->scalar_type() != at::kInt || offsets->dim() != 1 || offsets->numel() < 2 || !offsets->is_contiguous())
         refuse("seq_offsets must be a contiguous int32 tensor of num_seqs + 1 values");
-    return {t.size(0), (int)(offsets->numel() - 1)};
+    return {t.size(0), small(offsets->numel() - 1, "a count of sequences")};
 }
 
 // Slots of a state tensor [slots, *shape]; `slots`, if any, is what another has.
@@ -211,13 +218,6 @@ void head_strides(const Tensor &t, int64_t tokens, const char *what, int64_t hea
         refuse(what, ": shape ", t.sizes(), ", strides ", t.strides(), ", ", t.scalar_type(),
                " do not fit the other tensors");
     out[1] = t.stride(-2);
-}
-
-int small(int64_t v, const char *what)
-{
-    if (v > INT32_MAX)
-        refuse(what, " of ", v, " is too large");
-    return (int)v;
 }
 
 PyObject *status(conv_status st) { return PyLong_FromLong(st); }

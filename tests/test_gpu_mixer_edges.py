@@ -128,3 +128,9 @@ def test_product_of_many_channels(m):
     for at in range(0, n, 2 ** 24):
         part = slice(at, at + 2 ** 24)
         assert torch.equal(y[:, part], (x.float() @ w[part].float().t()).to(BF))
+
+
+def test_count_of_sequences_is_not_cut():
+    """2^32 + 1 empty sequences are more than the library counts, not one."""
+    with pytest.raises(ValueError, match="sequences"):
+        cf.causal_conv1d(torch.empty(2 ** 32 + 1, 0, 16, device=DEV), torch.ones(16, 2, device=DEV))
