@@ -130,7 +130,7 @@ __global__ __launch_bounds__(NT) void causal_conv1d_kernel(Causal1dProblem p)
 #pragma unroll
             for (int j = 0; j < K; ++j)
                 a = fmaf(w[j][i], win[j][i], a);
-            // The reciprocal is the instruction's, within 1 ulp.
+            // The reciprocal is the instruction's, within 1 ulp; exp's error is |a| 2^-24 of it, that of rounding a.
             f[i] = p.silu ? a * __builtin_amdgcn_rcpf(1.f + __expf(-a)) : a;
 #pragma unroll
             for (int j = 0; j < K - 1; ++j)

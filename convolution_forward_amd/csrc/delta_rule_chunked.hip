@@ -11,6 +11,8 @@
 //   S' = exp(G_63) S + K^T diag(r_i exp(G_63 - G_i)) U.
 // No exponent is ever positive for gates <= 0, and differences of G are taken
 // in 64 bits, so a strong gate early in a chunk costs the later ones nothing.
+// exp is the instruction's after a product with log2 e: its error, |x| 2^-24 of
+// the value, is that of rounding x itself to fp32.
 //
 // Two kernels. The first takes every chunk and key head at once and writes
 // what does not depend on S: T = (1 + A)^-1 diag(beta), P, the row factors, and
@@ -23,10 +25,11 @@
 // workgroups: no faster, 103 us for the six prompts.)
 //
 // 16384 tokens of one prompt, 16 key and 32 value heads of 128 x 128: the first
-// 124 us, 0.52 GB at 4.2 TB/s; the second 412-430 us, 256 chunks of 1.6-1.7 us
-// each, one workgroup a compute unit. There the chain of exchanges is the time
-// (matrix instructions: a fifth of it). With two workgroups a compute unit a
-// chunk of both takes 2.7 us, the loads' and LDS's paths half busy each.
+// 112-117 us, 0.52 GB at 4.5 TB/s; the second 458-484 us, 256 chunks of 1.8-1.9
+// us each, one workgroup a compute unit. There the chain of exchanges is most
+// of the time, and the output waves, which share its SIMDs, the rest: their
+// products of third parts cost 0.14 us a chunk. With two workgroups a compute
+// unit a chunk of both takes 3 us.
 //
 // Precision, bf16: operands (K, Q) are exact, every other operand of a product
 // is split into bf16 parts x = hi + mid + lo (each the nearest bf16 of what is
@@ -940,7 +943,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void d
 // rows a lane are the next product's operand as they lie, value e for step e,
 // so nothing is split and tokens keep their order; the waves, barriers and the
 // order of loads are those of the kernel above. 2047 tokens, 16 heads of 128 x
-// 128: 120 us with the preparation, token by token 1330. The instructions are
+// 128: 118 us with the preparation, token by token 1500. The instructions are
 // half of a chunk's 2.8 us. 128 registers (two spilled) for two workgroups a
 // compute unit: 8 sequences of 256 tokens, 32 heads, 167 -> 150 us.
 template <int DT>
@@ -1198,10 +1201,10 @@ hipError_t launch(const DeltaProblem &p, hipStream_t s)
                      (p.ost | p.osh) % 4 == 0;
     // One value head a workgroup while the chip holds them all at once, or
     // nearly (four a compute unit): 33 chunks of 32 heads, two a key head, took
-    // 78.4 us together and 76.7 apart, 65 chunks 135.7 and 146.2; 9 chunks of 16
-    // heads, four a key head, 37.2 and 27.0. In fp32 (two a compute unit, and
+    // 85.3 us together and 84.5 apart, 65 chunks 140 and 146; 9 chunks of 16
+    // heads, four a key head, 38.0 and 28.1. In fp32 (two a compute unit, and
     // more work that they would share): 17 chunks of 32 heads, two a key head,
-    // 81 together and 86 apart; of 16, four a key head, 78 and 72.
+    // 77.5 together and 83.3 apart; of 16, four a key head, 77.7 and 71.2.
     const int group = p.Hv / p.Hk;
     a.heads = numbers * p.Hv <= (F32 ? 512 : 1280) ? 1 : group;
     hipLaunchKernelGGL((delta_prepare_kernel<DT, F32>),

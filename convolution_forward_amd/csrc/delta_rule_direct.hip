@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void delta_direct_kernel(DeltaProblem p, int s
             rq *= __builtin_amdgcn_rsqf(rows_sum<CL>(qq) + UNIT_EPS);
         }
         kq = rows_sum<CL>(kq);
-        const float decay = __expf(x.g);
+        const float decay = __expf(x.g);        // off by |g| 2^-24 of it, and the roots above by 1 ulp
         float sk[4], sq[4], u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

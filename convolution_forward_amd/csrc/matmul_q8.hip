@@ -24,8 +24,9 @@
 // feed them (a wave of the largest tile reads 24 KB for 128x64x128 products):
 // int8 8192x8192x4096 in 231 us, 2.38 Pop/s (the library's product without
 // scales: 244). e4m3 runs at the bf16 instructions' rate and widens each
-// fragment beside them, a third of their time: 1111x2200x2064 in 20.7 us, one
-// round of tiles and the start and end of it.
+// fragment beside them, a third of their time: 8192x8192x4096 in 368-385 us,
+// 1.43-1.49 PFLOP/s; 1111x2200x2064 in 20.7 us, 162 tiles on 256 compute units
+// and the start and end of them.
 #include <type_traits>
 
 #include "common.h"

@@ -128,13 +128,13 @@ conv_status check_delta_sizes(int64_t tokens, int num_seqs, int Hk, int Hv, int 
     if (tokens > MAX_ROWS || num_seqs > MAX_ROWS || Dk > 256 || Dv > 65536 || Hv > 65535)
         return CONV_ERR_UNSUPPORTED;
     const bool can = delta_chunked_supports(tokens, num_seqs, Hk, Hv, Dk, Dv);
-    // Tokens a sequence from which chunks are faster. A lone sequence of 32
-    // heads of 128 x 128 takes 16 us by chunks up to 64 tokens, and token by
-    // token 15.6 for 16 of them, 18.6 for 20; once the chunks' workgroups share
-    // compute units, 8 such sequences take 38 us (token by token 33 for 24
-    // tokens, 42 for 32) and 64 take 200 (192 and 262).
-    // In fp32, where a chunk costs more: 22.6 us alone (28 tokens one by one
-    // 22.7), 59 for 8 sequences (48 tokens 56, 64 71), 360 to 400 for 64 (344, 454).
+    // Tokens a sequence, as the host knows them (the mean), from which chunks
+    // are faster. A lone sequence of 32 heads of 128 x 128 takes 16 us by chunks
+    // up to 64 tokens, and token by token 15.8 for 16 of them, 18.6 for 20; once
+    // the chunks' workgroups share compute units, 8 such sequences take 38 us
+    // (token by token 37 for 24 tokens, 47 for 32) and 64 take 220 (224 and 291).
+    // In fp32, where a chunk costs more: 23 us alone (28 tokens one by one 23.6),
+    // 59 for 8 sequences (48 tokens 62, 64 80), 372 to 407 for 64 (397, 520).
     const bool alone = (int64_t)num_seqs * Hv * ((Dv + 15) / 16) <= 256;
     const int least = dtype == CONV_F32 ? (alone ? 28 : 50) : alone ? 16 : 26;
     if (variant != CONV_VARIANT_AUTO && variant != CONV_VARIANT_DIRECT && variant != CONV_VARIANT_TILED)

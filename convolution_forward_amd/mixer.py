@@ -90,6 +90,9 @@ def gated_delta_rule(q, k, v, g, beta, scale=None, normalize: bool = False, seq_
     [slots, Hv, Dk, Dv] float32, possibly the same tensor. workspace: a uint8
     tensor of at least delta_rule_workspace(...) bytes; without it one is
     taken from torch's allocator for the call. Returns o like v.
+
+    VARIANT_AUTO chooses between chunks and single steps for the whole call,
+    by its mean length: a prompt is best kept apart from many single tokens.
     """
     r = (_binding or _load()).gated_delta_rule(q, k, v, g, beta, scale, normalize, seq_offsets, initial_state, final_state,
                                                slots, out, workspace, variant)

@@ -428,8 +428,16 @@ CONVFWD_API conv_status conv_causal1d_fwd(const void *x, int64_t x_stride, const
  *              256-byte aligned, used during the call only (NULL when that is 0).
  *   variant    CONV_VARIANT_DIRECT: token by token, any sizes with Dk <= 256.
  *              CONV_VARIANT_TILED: by chunks of 64 tokens on the matrix
- *              cores, Dk <= 128. CONV_VARIANT_AUTO picks by the sizes. Both
- *              compute in fp32 precision.
+ *              cores, Dk <= 128. Both compute in fp32 precision, and refuse
+ *              with CONV_ERR_UNSUPPORTED what their grids do not hold (some
+ *              2^26 waves). CONV_VARIANT_AUTO picks one for the whole call
+ *              from tokens / num_seqs, the only lengths known on the host: a
+ *              long prompt packed with many single tokens goes token by
+ *              token (2048 tokens with 128 single ones, 32 heads of 128 x
+ *              128, 1670 us; the two apart 77 and 100, by chunks 525).
+ *
+ * A value that is not finite, or leaves fp32's range, reaches no earlier
+ * token, no other head and no other sequence.
  */
 CONVFWD_API conv_status conv_delta_rule_fwd(const void *q, const int64_t *q_strides, const void *k,
                                             const int64_t *k_strides, const void *v, const int64_t *v_strides,
