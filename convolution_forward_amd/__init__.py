@@ -11,7 +11,7 @@ GPU, the call raises.
         strides free), F [KH,KW,Cin/groups,Cout] contiguous -> Y [N,Ho,Wo,Cout].
     conv_depthwise(x, w, bias=None, stride=1, padding=0, dilation=1, exact=True)
         Depthwise, X [N,C,H,W], w [C*mult,KH,KW] -> Y [N,C*mult,Ho,Wo].
-    rms_norm_q8, matmul_q8, causal_conv1d, gated_delta_rule
+    rms_norm_q8, matmul_q8, causal_conv1d, rotary, gated_delta_rule, selective_scan, selective_scan_heads
         The operators of a token mixer round a short causal convolution (mixer.py).
 
 padding is an int (all sides), a pair (rows, columns; the same before and
@@ -51,7 +51,8 @@ EXPORTED = ("conv2d_nhwc_fwd", "conv2d_nhwc_fwd_variant", "conv2d_nhwc_fwd_windo
             "conv2d_nhwc_window_auto_variant", "conv_depthwise_auto_variant", "conv_depthwise_window_auto_variant",
             "conv_out_size", "conv_out_size_window", "conv_status_str", "conv_copy_bytes", "conv_copy_bytes_wide",
             "conv_im2col_nhwc", "conv_rms_norm_q8_fwd", "conv_matmul_q8_fwd", "conv_causal1d_fwd",
-            "conv_delta_rule_fwd", "conv_delta_rule_workspace")
+            "conv_delta_rule_fwd", "conv_delta_rule_workspace", "conv_rotary_fwd", "conv_selective_scan_fwd",
+            "conv_selective_scan_workspace", "conv_selective_scan_heads_fwd", "conv_selective_scan_heads_workspace")
 
 
 class ConvWindow(ctypes.Structure):
@@ -130,6 +131,17 @@ def load_library():
     lib.conv_delta_rule_fwd.argtypes = [p] * 12 + [i, p, p, p, i64, i64] + [i] * 5 + [f32] + [i] * 3 + [p]
     lib.conv_delta_rule_workspace.restype = i64
     lib.conv_delta_rule_workspace.argtypes = [i64] + [i] * 7
+    lib.conv_rotary_fwd.restype = i
+    lib.conv_rotary_fwd.argtypes = [p, p, p, p, p, i] + [p] * 7 + [i64] + [i] * 4 + [f32, f32, i, i, p]
+    lib.conv_selective_scan_fwd.restype = i
+    lib.conv_selective_scan_fwd.argtypes = [p, i64, p, i64] + [p] * 7 + [i64, p, p, i64] + [p] * 4 + [i, p, i64, i64] + \
+        [i] * 7 + [p]
+    lib.conv_selective_scan_workspace.restype = i64
+    lib.conv_selective_scan_workspace.argtypes = [i64] + [i] * 6
+    lib.conv_selective_scan_heads_fwd.restype = i
+    lib.conv_selective_scan_heads_fwd.argtypes = [p, p, p, i64] + [p] * 15 + [i, p, i64, i64] + [i] * 8 + [p]
+    lib.conv_selective_scan_heads_workspace.restype = i64
+    lib.conv_selective_scan_heads_workspace.argtypes = [i64] + [i] * 7
     _lib = lib
     return lib
 
@@ -362,7 +374,9 @@ def copy_bytes(src, dst, nbytes: int | None = None, wide: bool = False):
     return dst
 
 
-_MIXER = ("causal_conv1d", "delta_rule_workspace", "gated_delta_rule", "matmul_q8", "rms_norm_q8")
+_MIXER = ("causal_conv1d", "delta_rule_workspace", "gated_delta_rule", "matmul_q8", "rms_norm_q8", "rotary",
+          "rotary_frequencies", "selective_scan", "selective_scan_heads", "selective_scan_heads_workspace",
+          "selective_scan_workspace")
 
 
 def __getattr__(name):

@@ -394,6 +394,171 @@ PyObject *gated_delta_rule(PyObject *const *a)
     return st != CONV_OK ? status(st) : wrap(std::move(o));
 }
 
+// A workspace of the caller's, or one of `bytes` from torch's allocator for the call.
+struct Space {
+    Tensor own;
+    void *at = nullptr;
+    int64_t bytes = 0;
+
+    Space(const Tensor *given, const Tensor &like, int64_t need)
+    {
+        if (given) {
+            bytes = given->numel();
+            at = vector(given, bytes, at::kByte, "workspace");
+        } else if (need > 0) {
+            own = fresh(like, {need}, at::kByte);
+            at = own.data_ptr();
+            bytes = need;
+        }
+    }
+};
+
+bool truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw python_error();
+    return v != 0;
+}
+
+// q, positions, frequencies, k, q_weight, k_weight, eps, interleaved, scale, out, k_out -> q or (q, k)
+PyObject *rotary(PyObject *const *a)
+{
+    const Tensor &q = tensor(a[0], "q"), &positions = tensor(a[1], "positions"), &freq = tensor(a[2], "frequencies");
+    const Tensor *k = maybe(a[3], "k"), *qw = maybe(a[4], "q_weight"), *kw = maybe(a[5], "k_weight"), *out = maybe(a[9], "out"),
+                 *kout = maybe(a[10], "k_out");
+    same_gpu(q, &positions, &freq, k, qw, kw, out, kout);
+    const at::ScalarType type = q.scalar_type();
+    const conv_dtype dt = float_code(type, "q");
+    if (q.dim() != 3 && q.dim() != 4)
+        refuse("q must be [tokens, heads, channels] or [batch, length, heads, channels], got ", q.sizes());
+    if (!k && (kw || kout))
+        refuse("k_weight and k_out go with k");
+    const int64_t Hq = q.size(-2), D = q.size(-1), tokens = q.dim() == 4 ? q.size(0) * q.size(1) : q.size(0);
+    const int64_t Hk = k && k->dim() >= 3 ? k->size(-2) : 0;
+    if (k && Hk == 0)
+        refuse("k must be [..., heads, channels] with a head at least, got ", k->sizes());
+    int64_t sq[2], sk[2], oq[2], ok[2];
+    head_strides(q, tokens, "q", Hq, D, type, sq);
+    if (k)
+        head_strides(*k, tokens, "k", Hk, D, type, sk);
+    if (out)
+        head_strides(*out, tokens, "out", Hq, D, type, oq);
+    if (kout)
+        head_strides(*kout, tokens, "k_out", Hk, D, type, ok);
+    if (positions.scalar_type() != at::kLong && positions.scalar_type() != at::kInt)
+        refuse("positions must be int64 or int32, got ", positions.scalar_type());
+    const void *pos = vector(&positions, tokens, positions.scalar_type(), "positions");
+    const int64_t pairs = freq.numel();
+    const auto *fp = static_cast<const float *>(vector(&freq, pairs, at::kFloat, "frequencies"));
+    const void *qwp = vector(qw, D, type, "q_weight"), *kwp = vector(kw, D, type, "k_weight");
+    const c10::DeviceGuard guard(q.device());
+    Tensor y = out ? *out : fresh(q, q.sizes(), type), z;
+    if (k)
+        z = kout ? *kout : fresh(*k, k->sizes(), type);
+    const conv_status st = conv_rotary_fwd(
+        ptr(q), sq, ptr(k), k ? sk : nullptr, pos, positions.scalar_type() == at::kLong ? 64 : 32, fp, qwp, kwp, ptr(y),
+        out ? oq : nullptr, k ? ptr(z) : nullptr, kout ? ok : nullptr, tokens, small(Hq, "a head count"),
+        small(Hk, "a head count"), small(D, "a head's width"), small(2 * pairs, "a rotated width"), (float)number(a[6]),
+        (float)number(a[8]), truth(a[7]), dt, stream_of(q));
+    if (st != CONV_OK)
+        return status(st);
+    if (!k)
+        return wrap(std::move(y));
+    PyObject *r = PyTuple_New(2);
+    if (!r)
+        throw python_error();
+    PyTuple_SET_ITEM(r, 0, wrap(std::move(y)));
+    PyTuple_SET_ITEM(r, 1, wrap(std::move(z)));
+    return r;
+}
+
+// x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, seq_offsets, initial_state, final_state, slots, out, workspace, variant
+// -> y
+PyObject *selective_scan(PyObject *const *a)
+{
+    const Tensor &x = tensor(a[0], "x"), &step = tensor(a[1], "dt"), &rate = tensor(a[2], "a"), &b = tensor(a[3], "b"),
+                 &c = tensor(a[4], "c");
+    const Tensor *skip = maybe(a[5], "skip"), *gate = maybe(a[6], "gate"), *bias = maybe(a[7], "dt_bias"),
+                 *offsets = maybe(a[9], "seq_offsets"), *si = maybe(a[10], "initial_state"), *so = maybe(a[11], "final_state"),
+                 *slots = maybe(a[12], "slots"), *out = maybe(a[13], "out"), *work = maybe(a[14], "workspace");
+    same_gpu(x, &step, &rate, &b, &c, skip, gate, bias, offsets, si, so, slots, out, work);
+    const at::ScalarType type = x.scalar_type();
+    const conv_dtype dt = float_code(type, "x");
+    const Seqs seq = sequences(x, 1, offsets);
+    const int64_t channels = x.size(-1);
+    if (rate.dim() != 2 || b.dim() != x.dim() + 1)
+        refuse("expected a [channels, states] and b [..., groups, states], got ", rate.sizes(), " and ", b.sizes());
+    const int64_t N = rate.size(1), groups = b.size(-2);
+    const auto *ap = static_cast<const float *>(vector(&rate, channels * N, at::kFloat, "a"));
+    int64_t sb[2], sc[2];
+    head_strides(b, seq.tokens, "b", groups, N, type, sb);
+    head_strides(c, seq.tokens, "c", groups, N, type, sc);
+    const int64_t xs = row_stride(x, "x", channels, seq.tokens, type), ds = row_stride(step, "dt", channels, seq.tokens, type);
+    const int64_t gs = gate ? row_stride(*gate, "gate", channels, seq.tokens, type) : 0;
+    const int64_t ys = out ? row_stride(*out, "out", channels, seq.tokens, type) : channels;
+    const auto *sp = static_cast<const float *>(vector(skip, channels, at::kFloat, "skip"));
+    const auto *tp = static_cast<const float *>(vector(bias, channels, at::kFloat, "dt_bias"));
+    const int64_t shape[2] = {channels, N};
+    const int64_t num = state(so, shape, at::kFloat, state(si, shape, at::kFloat, 0));
+    const auto *sl = static_cast<const int32_t *>(vector(slots, seq.count, at::kInt, "slots"));
+    const int ch = small(channels, "a channel count"), g = small(groups, "a group count"), n = small(N, "a state count"),
+              variant = (int)integer(a[15]);
+    const c10::DeviceGuard guard(x.device());
+    Tensor y = out ? *out : fresh(x, x.sizes(), type);
+    const Space space(work, x, work ? 0 : conv_selective_scan_workspace(seq.tokens, seq.count, ch, g, n, dt, variant));
+    const conv_status st = conv_selective_scan_fwd(
+        ptr(x), xs, ptr(step), ds, ap, ptr(b), sb, ptr(c), sc, sp, ptr(gate), gs, tp, ptr(y), ys,
+        static_cast<const int32_t *>(ptr(offsets)), static_cast<const float *>(ptr(si)), static_cast<float *>(ptr(so)), sl,
+        small(num, "a slot count"), space.at, space.bytes, seq.tokens, seq.count, ch, g, n, truth(a[8]), dt, variant,
+        stream_of(x));
+    return st != CONV_OK ? status(st) : wrap(std::move(y));
+}
+
+// As selective_scan, with x, gate and out [..., heads, channels], dt [..., heads], and a, skip and dt_bias [heads]
+PyObject *selective_scan_heads(PyObject *const *a)
+{
+    const Tensor &x = tensor(a[0], "x"), &step = tensor(a[1], "dt"), &rate = tensor(a[2], "a"), &b = tensor(a[3], "b"),
+                 &c = tensor(a[4], "c");
+    const Tensor *skip = maybe(a[5], "skip"), *gate = maybe(a[6], "gate"), *bias = maybe(a[7], "dt_bias"),
+                 *offsets = maybe(a[9], "seq_offsets"), *si = maybe(a[10], "initial_state"), *so = maybe(a[11], "final_state"),
+                 *slots = maybe(a[12], "slots"), *out = maybe(a[13], "out"), *work = maybe(a[14], "workspace");
+    same_gpu(x, &step, &rate, &b, &c, skip, gate, bias, offsets, si, so, slots, out, work);
+    const at::ScalarType type = x.scalar_type();
+    const conv_dtype dt = float_code(type, "x");
+    const Seqs seq = sequences(x, 2, offsets);
+    if (b.dim() != x.dim())
+        refuse("b must be [..., groups, states], got ", b.sizes());
+    const int64_t H = x.size(-2), P = x.size(-1), groups = b.size(-2), N = b.size(-1);
+    int64_t sx[2], sg[2], sy[2], sb[2], sc[2];
+    head_strides(x, seq.tokens, "x", H, P, type, sx);
+    head_strides(b, seq.tokens, "b", groups, N, type, sb);
+    head_strides(c, seq.tokens, "c", groups, N, type, sc);
+    if (gate)
+        head_strides(*gate, seq.tokens, "gate", H, P, type, sg);
+    if (out)
+        head_strides(*out, seq.tokens, "out", H, P, type, sy);
+    const int64_t ds = row_stride(step, "dt", H, seq.tokens, type);
+    const auto *ap = static_cast<const float *>(vector(&rate, H, at::kFloat, "a"));
+    const auto *sp = static_cast<const float *>(vector(skip, H, at::kFloat, "skip"));
+    const auto *tp = static_cast<const float *>(vector(bias, H, at::kFloat, "dt_bias"));
+    const int64_t shape[3] = {H, P, N};
+    const int64_t num = state(so, shape, at::kFloat, state(si, shape, at::kFloat, 0));
+    const auto *sl = static_cast<const int32_t *>(vector(slots, seq.count, at::kInt, "slots"));
+    const int h = small(H, "a head count"), p = small(P, "a head's width"), g = small(groups, "a group count"),
+              n = small(N, "a state count"), variant = (int)integer(a[15]);
+    const c10::DeviceGuard guard(x.device());
+    Tensor y = out ? *out : fresh(x, x.sizes(), type);
+    const Space space(work, x,
+                      work ? 0 : conv_selective_scan_heads_workspace(seq.tokens, seq.count, h, p, g, n, dt, variant));
+    const conv_status st = conv_selective_scan_heads_fwd(
+        ptr(x), sx, ptr(step), ds, ap, ptr(b), sb, ptr(c), sc, sp, ptr(gate), gate ? sg : nullptr, tp, ptr(y),
+        out ? sy : nullptr, static_cast<const int32_t *>(ptr(offsets)), static_cast<const float *>(ptr(si)),
+        static_cast<float *>(ptr(so)), sl, small(num, "a slot count"), space.at, space.bytes, seq.tokens, seq.count, h, p, g,
+        n, truth(a[8]), dt, variant, stream_of(x));
+    return st != CONV_OK ? status(st) : wrap(std::move(y));
+}
+
 template <PyObject *(*F)(PyObject *const *), int N>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -422,6 +587,9 @@ PyMethodDef methods[] = {
     method<matmul_q8, 8>("matmul_q8"),
     method<causal_conv1d, 9>("causal_conv1d"),
     method<gated_delta_rule, 14>("gated_delta_rule"),
+    method<rotary, 11>("rotary"),
+    method<selective_scan, 16>("selective_scan"),
+    method<selective_scan_heads, 16>("selective_scan_heads"),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -167,6 +167,60 @@ bool delta_chunked_supports(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk
 int64_t delta_chunked_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, conv_dtype dtype);
 hipError_t launch_delta_chunked(const DeltaProblem &p, hipStream_t s);
 
+// Validated head norms and rotation. Hk == 0: no keys.
+struct RotaryProblem {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t qst, qsh, kst, ksh, qot, qoh, kot, koh;     // token and head strides in elements
+    const void *qweight, *kweight;                      // NULL: no norm
+    const void *positions;                              // int64 if wide, else int32
+    const float *frequencies;
+    int64_t tokens;
+    int wide, Hq, Hk, D, rotated, interleaved;
+    float eps, scale;
+    conv_dtype dtype;
+};
+
+bool rotary_supports(int64_t tokens, int heads, int D);
+hipError_t launch_rotary(const RotaryProblem &p, hipStream_t s);
+
+// A validated selective scan with a decay for each channel and state.
+struct ScanProblem {
+    const void *x, *dt, *b, *c, *gate;
+    const float *a, *skip, *bias;
+    void *y;
+    int64_t xs, dts, gs, ys;                            // row strides in elements
+    int64_t bst, bsg, cst, csg;                         // token and group strides in elements
+    const float *state_in;
+    float *state_out;
+    Sequences seq;
+    void *workspace;
+    int channels, groups, N, softplus;
+    conv_dtype dtype;
+};
+
+bool scan_direct_supports(int num_seqs, int channels, int N);
+hipError_t launch_scan_direct(const ScanProblem &p, hipStream_t s);
+
+// A validated selective scan with one decay a head.
+struct HeadScanProblem {
+    const void *x, *dt, *b, *c, *gate;
+    const float *a, *skip, *bias;
+    void *y;
+    int64_t xst, xsh, gst, gsh, yst, ysh;               // token and head strides in elements
+    int64_t dts;                                        // token stride of dt
+    int64_t bst, bsg, cst, csg;                         // token and group strides in elements
+    const float *state_in;
+    float *state_out;
+    Sequences seq;
+    void *workspace;
+    int H, P, groups, N, softplus;
+    conv_dtype dtype;
+};
+
+bool heads_direct_supports(int num_seqs, int H, int P, int N);
+hipError_t launch_heads_direct(const HeadScanProblem &p, hipStream_t s);
+
 // Streaming copies used for bandwidth / counter calibration.
 hipError_t launch_copy_bytes(const void *src, void *dst, int64_t bytes, hipStream_t s);
 hipError_t launch_copy_wide(const void *src, void *dst, int64_t bytes, hipStream_t s);

@@ -1,5 +1,6 @@
 """Token-mixer operators: RMS norm with 8-bit output, 8-bit matrix product,
-causal convolution and gated delta rule over packed sequences.
+causal convolution, head norms with rotation, gated delta rule and selective
+scans over packed sequences.
 
 include/convfwd.h holds the definitions; the arguments are marshalled by a
 small compiled binding (binding/mixer_binding.cpp), since a single token's
@@ -13,6 +14,7 @@ from __future__ import annotations
 
 import importlib.machinery
 import importlib.util
+import math
 import os
 
 import torch
@@ -108,3 +110,122 @@ def delta_rule_workspace(tokens: int, num_seqs: int, Hk: int, Hv: int, Dk: int, 
     if code is None:
         raise ValueError(f"unsupported dtype {dtype}; use float32 or bfloat16")
     return int(load_library().conv_delta_rule_workspace(tokens, num_seqs, Hk, Hv, Dk, Dv, code, variant))
+
+
+def rotary(q, positions, frequencies, k=None, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+           scale: float = 1.0, out=None, k_out=None):
+    """Norms of queries and keys for each head, and their rotation by position (conv_rotary_fwd in include/convfwd.h).
+
+    q [tokens, Hq, D] or [batch, length, Hq, D] float32 or bfloat16, k likewise
+    with Hk heads; positions [tokens] int64 or int32 (a value a token, batches
+    one after the other); frequencies [R / 2] float32, as rotary_frequencies
+    makes them: the first R values of a head are rotated, in pairs i and
+    i + R/2, or 2i and 2i + 1 with interleaved. q_weight and k_weight [D] of
+    q's type: an RMS norm before the rotation; without one the values are
+    rotated as they are. scale multiplies what is rotated. out and k_out may be
+    q and k. Returns q's result, with k a pair.
+    """
+    r = (_binding or _load()).rotary(q, positions, frequencies, k, q_weight, k_weight, eps, interleaved, scale, out, k_out)
+    if type(r) is int:
+        _check(r, "conv_rotary_fwd")
+    return r
+
+
+def rotary_frequencies(rotated: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       trained: int = 0, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(frequencies [rotated / 2] float32, scale) for rotary: base ** (-2 i / rotated), stretched for long contexts.
+
+    scaling None: as they are. "linear": divided by factor. "base": the base
+    raised so that the slowest frequency is divided by factor and the fastest
+    is kept. "parts": frequencies of at most `slow` turns in `trained`
+    positions divided by factor, those of at least `fast` turns kept, and a ramp
+    over the turns' logarithm (over the index i) between; the scale is then
+    0.1 ln(factor) + 1. "wavelength": the same bounds, a ramp over the turns
+    themselves, and scale 1. Computed in 64 bits on the host.
+    """
+    if rotated <= 0 or rotated % 2:
+        raise ValueError(f"rotated {rotated}: a positive even number")
+    if scaling not in (None, "linear", "base", "parts", "wavelength"):
+        raise ValueError(f"scaling {scaling!r}: None, 'linear', 'base', 'parts' or 'wavelength'")
+    if not (base > 1.0 and factor >= 1.0):
+        raise ValueError(f"base {base} must be above 1 and factor {factor} at least 1")
+    if scaling in ("parts", "wavelength") and not (trained > 0 and fast > slow > 0.0):
+        raise ValueError(f"{scaling} needs trained > 0 and fast > slow > 0, got {trained}, {fast} and {slow}")
+    half = rotated // 2
+    if scaling == "base" and half > 1:
+        base *= factor ** (half / (half - 1))
+    f = [base ** (-i / half) for i in range(half)]
+    scale = 1.0
+    if scaling == "linear" or (scaling == "base" and half == 1):
+        f = [v / factor for v in f]
+    elif scaling in ("parts", "wavelength"):
+        if scaling == "parts":
+            # The index at which a frequency makes that many turns.
+            ends = [half * math.log(trained / (2 * math.pi * turns)) / math.log(base) for turns in (fast, slow)]
+            lo, hi = max(math.floor(ends[0]), 0), min(math.ceil(ends[1]), rotated - 1)
+            keep = [1.0 - min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(half)]
+            scale = 0.1 * math.log(factor) + 1.0
+        else:
+            keep = [min(max((trained * v / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0) for v in f]
+        f = [v * (k + (1.0 - k) / factor) for v, k in zip(f, keep)]
+    return torch.tensor(f, dtype=torch.float64).float().to(device), scale
+
+
+def selective_scan(x, dt, a, b, c, skip=None, gate=None, dt_bias=None, dt_softplus: bool = False, seq_offsets=None,
+                   initial_state=None, final_state=None, slots=None, out=None, workspace=None, variant: int = VARIANT_AUTO):
+    """The selective state space scan with a decay for each channel and state (conv_selective_scan_fwd in
+    include/convfwd.h).
+
+    x, dt, gate [batch, length, channels] or [tokens, channels] float32 or
+    bfloat16; a [channels, states] float32; b, c [..., groups, states] of x's
+    type, channels a multiple of groups; skip, dt_bias [channels] float32.
+    initial_state and final_state [slots, channels, states] float32, possibly
+    the same tensor. workspace: a uint8 tensor of at least
+    selective_scan_workspace(...) bytes; without it one is taken from torch's
+    allocator for the call. Returns y like x.
+    """
+    r = (_binding or _load()).selective_scan(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, seq_offsets, initial_state,
+                                             final_state, slots, out, workspace, variant)
+    if type(r) is int:
+        _check(r, "conv_selective_scan_fwd")
+    return r
+
+
+def selective_scan_heads(x, dt, a, b, c, skip=None, gate=None, dt_bias=None, dt_softplus: bool = False, seq_offsets=None,
+                         initial_state=None, final_state=None, slots=None, out=None, workspace=None,
+                         variant: int = VARIANT_AUTO):
+    """The selective state space scan with one decay a head (conv_selective_scan_heads_fwd in include/convfwd.h).
+
+    x, gate [batch, length, H, P] or [tokens, H, P] float32 or bfloat16;
+    dt [..., H] and b, c [..., groups, states] of x's type, H a multiple of
+    groups; a, skip, dt_bias [H] float32. initial_state and final_state
+    [slots, H, P, states] float32, possibly the same tensor. workspace: a uint8
+    tensor of at least selective_scan_heads_workspace(...) bytes; without it one
+    is taken from torch's allocator for the call. Returns y like x.
+    """
+    r = (_binding or _load()).selective_scan_heads(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, seq_offsets,
+                                                   initial_state, final_state, slots, out, workspace, variant)
+    if type(r) is int:
+        _check(r, "conv_selective_scan_heads_fwd")
+    return r
+
+
+def _float_code(dtype) -> int:
+    code = {torch.float32: CONV_F32, torch.bfloat16: CONV_BF16}.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+    return code
+
+
+def selective_scan_workspace(tokens: int, num_seqs: int, channels: int, groups: int, states: int, dtype=torch.bfloat16,
+                             variant: int = VARIANT_AUTO) -> int:
+    """Bytes of workspace selective_scan needs for these sizes (-1: the sizes are an error)."""
+    return int(load_library().conv_selective_scan_workspace(tokens, num_seqs, channels, groups, states, _float_code(dtype),
+                                                            variant))
+
+
+def selective_scan_heads_workspace(tokens: int, num_seqs: int, H: int, P: int, groups: int, states: int,
+                                   dtype=torch.bfloat16, variant: int = VARIANT_AUTO) -> int:
+    """Bytes of workspace selective_scan_heads needs for these sizes (-1: the sizes are an error)."""
+    return int(load_library().conv_selective_scan_heads_workspace(tokens, num_seqs, H, P, groups, states,
+                                                                  _float_code(dtype), variant))

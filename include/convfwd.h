@@ -11,7 +11,8 @@
  *
  * Two convolution operators, and at the end of this file the four operators
  * of a token mixer built round a short causal convolution (norm, 8-bit
- * product, causal convolution, gated delta rule):
+ * product, causal convolution, head norms and rotation, gated delta rule,
+ * selective scans):
  *
  *  - Dense NHWC cross-correlation, as fixed by "CMU DLSys Lecture 14:
  *    Convolutional Network Implementation", section 1 (the index contract):
@@ -309,8 +310,9 @@ CONVFWD_API conv_status conv_copy_bytes_wide(const void *src, void *dst, int64_t
  * convolution, here with 8-bit operands), runs the causal depthwise Conv1D
  * that "Convolution Is Wx+b Moving Across a Signal" names (section "Where
  * this shows up in models I work with") over each sequence, and moves a
- * per-head state along the sequence. These four calls are that layer. They
- * are forward operators; each has one form for prompts and for single tokens.
+ * state along the sequence, by the gated delta rule or a selective scan. These
+ * calls are that layer. They are forward operators; each has one form for
+ * prompts and for single tokens.
  *
  * Rules they share:
  *  - Tokens are rows, channels are adjacent. Strides are in elements.
@@ -452,6 +454,122 @@ CONVFWD_API conv_status conv_delta_rule_fwd(const void *q, const int64_t *q_stri
  * -1 where the sizes themselves are an error. Host-only. */
 CONVFWD_API int64_t conv_delta_rule_workspace(int64_t tokens, int num_seqs, int Hk, int Hv, int Dk, int Dv,
                                               conv_dtype dtype, int variant);
+
+/*
+ * conv_rotary_fwd -- norms of queries and keys for each head, and their
+ * rotation by position, in one pass.
+ *
+ * For each token t and head, in fp32 and rounded once:
+ *   n_j = x_j * rsqrt(mean_j(x_j^2) + eps) * weight_j      (n_j = x_j where the weight is NULL)
+ *   (a, b) -> scale * (a cos w - b sin w, b cos w + a sin w),  w = positions[t] * frequencies[i]
+ * for the pairs i < rotated / 2 of n's first `rotated` values: (n_i,
+ * n_{i + rotated/2}), or (n_2i, n_{2i+1}) with interleaved != 0. The values
+ * from `rotated` on are n_j. The angle is reduced in 64 bits, so that far
+ * positions keep their precision; a frequency or position of any sign will do.
+ * A head of zeros stays zeros also without an eps.
+ *
+ *   q          device [tokens, Hq, D], `dtype` (CONV_F32 or CONV_BF16);
+ *              strides: host arrays (token, head) in elements, NULL =
+ *              contiguous. Channels are adjacent. D <= 512.
+ *   k          device [tokens, Hk, D] likewise; Hk == 0: no keys (k, k_out,
+ *              their strides and k_weight are then ignored).
+ *   positions  device [tokens], int32 or int64 (position_bits 32 or 64).
+ *   frequencies  device [rotated / 2] fp32, radians a position.
+ *   q_weight, k_weight  device [D], `dtype`, or NULL.
+ *   q_out, k_out  device, shapes of q and k. Each may be its input (same
+ *              pointer and strides); they may be columns of one buffer of
+ *              rows, as q and k may.
+ * Errors: CONV_ERR_SHAPE for an odd `rotated` or one past D.
+ */
+CONVFWD_API conv_status conv_rotary_fwd(const void *q, const int64_t *q_strides, const void *k,
+                                        const int64_t *k_strides, const void *positions, int position_bits,
+                                        const float *frequencies, const void *q_weight, const void *k_weight,
+                                        void *q_out, const int64_t *qo_strides, void *k_out,
+                                        const int64_t *ko_strides, int64_t tokens, int Hq, int Hk, int D,
+                                        int rotated, float eps, float scale, int interleaved, conv_dtype dtype,
+                                        void *stream);
+
+/*
+ * conv_selective_scan_fwd -- the selective state space scan with a decay for
+ * each channel and state, over packed sequences.
+ *
+ * For each sequence and channel, h [N] in fp32 and token by token:
+ *   d = dt_t + dt_bias, with softplus != 0 log(1 + exp(dt_t + dt_bias))
+ *   h[n] = exp(d a[n]) h[n] + d x_t b_t[n]
+ *   y_t = (sum_n c_t[n] h[n] + skip x_t) * gate_t / (1 + exp(-gate_t))
+ * Channel i reads b and c of group i / (channels / groups). Without skip its
+ * term, and without a gate its factor, is left out.
+ *
+ *   x, dt, gate, y  device [tokens, channels], `dtype` (CONV_F32 or CONV_BF16), a row stride each. gate may be NULL.
+ *   a          device, contiguous [channels, N] fp32; negative for a decay. N <= 256.
+ *   b, c       device [tokens, groups, N], `dtype`; strides: host arrays
+ *              (token, group) in elements, NULL = contiguous.
+ *   skip, dt_bias  device [channels] fp32, or NULL.
+ *   state_in, state_out  device, contiguous [num_slots, channels, N] fp32.
+ *   workspace  device memory of at least conv_selective_scan_workspace
+ *              bytes, 256-byte aligned, used during the call only (NULL when
+ *              that is 0).
+ *   variant    CONV_VARIANT_DIRECT: token by token. CONV_VARIANT_AUTO: the same.
+ *
+ * A value that is not finite, or leaves fp32's range, reaches no earlier
+ * token and no other sequence.
+ */
+CONVFWD_API conv_status conv_selective_scan_fwd(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride,
+                                                const float *a, const void *b, const int64_t *b_strides,
+                                                const void *c, const int64_t *c_strides, const float *skip,
+                                                const void *gate, int64_t gate_stride, const float *dt_bias, void *y,
+                                                int64_t y_stride, const int32_t *seq_offsets, const float *state_in,
+                                                float *state_out, const int32_t *slots, int num_slots,
+                                                void *workspace, int64_t workspace_bytes, int64_t tokens,
+                                                int num_seqs, int channels, int groups, int N, int softplus,
+                                                conv_dtype dtype, int variant, void *stream);
+
+/* Bytes of workspace conv_selective_scan_fwd needs for these sizes (0: none),
+ * or -1 where the sizes themselves are an error. Host-only. */
+CONVFWD_API int64_t conv_selective_scan_workspace(int64_t tokens, int num_seqs, int channels, int groups, int N,
+                                                  conv_dtype dtype, int variant);
+
+/*
+ * conv_selective_scan_heads_fwd -- the selective state space scan with one
+ * decay a head, over packed sequences.
+ *
+ * For each sequence and head, S [P,N] in fp32 and token by token:
+ *   d = dt_t + dt_bias, with softplus != 0 log(1 + exp(dt_t + dt_bias))
+ *   S = exp(d a) S + d x_t b_t^T
+ *   y_t = (S c_t + skip x_t) * gate_t / (1 + exp(-gate_t))
+ * Head h reads b and c of group h / (H / groups). Without skip its term, and
+ * without a gate its factor, is left out.
+ *
+ *   x, gate, y  device [tokens, H, P], `dtype` (CONV_F32 or CONV_BF16);
+ *              strides: host arrays (token, head) in elements, NULL =
+ *              contiguous. Channels are adjacent. gate may be NULL.
+ *   dt         device [tokens, H], `dtype`, row stride dt_stride.
+ *   a, skip, dt_bias  device [H] fp32; skip and dt_bias may be NULL. a is negative for a decay.
+ *   b, c       device [tokens, groups, N], `dtype`, strides likewise (token, group). N <= 256.
+ *   state_in, state_out  device, contiguous [num_slots, H, P, N] fp32.
+ *   workspace  device memory of at least conv_selective_scan_heads_workspace
+ *              bytes, 256-byte aligned, used during the call only (NULL when
+ *              that is 0).
+ *   variant    CONV_VARIANT_DIRECT: token by token. CONV_VARIANT_AUTO: the same.
+ *
+ * A value that is not finite, or leaves fp32's range, reaches no earlier
+ * token, no other group and no other sequence.
+ */
+CONVFWD_API conv_status conv_selective_scan_heads_fwd(const void *x, const int64_t *x_strides, const void *dt,
+                                                      int64_t dt_stride, const float *a, const void *b,
+                                                      const int64_t *b_strides, const void *c,
+                                                      const int64_t *c_strides, const float *skip, const void *gate,
+                                                      const int64_t *gate_strides, const float *dt_bias, void *y,
+                                                      const int64_t *y_strides, const int32_t *seq_offsets,
+                                                      const float *state_in, float *state_out, const int32_t *slots,
+                                                      int num_slots, void *workspace, int64_t workspace_bytes,
+                                                      int64_t tokens, int num_seqs, int H, int P, int groups, int N,
+                                                      int softplus, conv_dtype dtype, int variant, void *stream);
+
+/* Bytes of workspace conv_selective_scan_heads_fwd needs for these sizes (0:
+ * none), or -1 where the sizes themselves are an error. Host-only. */
+CONVFWD_API int64_t conv_selective_scan_heads_workspace(int64_t tokens, int num_seqs, int H, int P, int groups, int N,
+                                                        conv_dtype dtype, int variant);
 
 #ifdef __cplusplus
 }
