@@ -220,6 +220,9 @@ struct HeadScanProblem {
 
 bool heads_direct_supports(int num_seqs, int H, int P, int N);
 hipError_t launch_heads_direct(const HeadScanProblem &p, hipStream_t s);
+bool heads_chunked_supports(int64_t tokens, int num_seqs, int H, int P, int groups, int N, conv_dtype dtype);
+int64_t heads_chunked_workspace(int64_t tokens, int num_seqs, int H, int P, int groups, int N, conv_dtype dtype);
+hipError_t launch_heads_chunked(const HeadScanProblem &p, hipStream_t s);
 
 // Streaming copies used for bandwidth / counter calibration.
 hipError_t launch_copy_bytes(const void *src, void *dst, int64_t bytes, hipStream_t s);

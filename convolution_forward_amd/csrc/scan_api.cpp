@@ -56,8 +56,9 @@ conv_status check_heads_sizes(int64_t tokens, int num_seqs, int H, int P, int gr
         return CONV_ERR_DTYPE;
     if (tokens > MAX_ROWS || num_seqs > MAX_ROWS || H > 65535 || P > 65536 || N > 256 || !known_variant(variant))
         return CONV_ERR_UNSUPPORTED;
-    *tiled = variant == CONV_VARIANT_TILED;
-    return (*tiled ? false : heads_direct_supports(num_seqs, H, P, N)) ? CONV_OK : CONV_ERR_UNSUPPORTED;
+    const bool can = heads_chunked_supports(tokens, num_seqs, H, P, groups, N, dtype);
+    *tiled = variant == CONV_VARIANT_TILED || (variant == CONV_VARIANT_AUTO && can && tokens > 12 * (int64_t)num_seqs);
+    return (*tiled ? can : heads_direct_supports(num_seqs, H, P, N)) ? CONV_OK : CONV_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -220,7 +221,7 @@ int64_t conv_selective_scan_heads_workspace(int64_t tokens, int num_seqs, int H,
     bool tiled;
     if (check_heads_sizes(tokens, num_seqs, H, P, groups, N, dtype, variant, &tiled) != CONV_OK)
         return -1;
-    return 0;
+    return tiled ? heads_chunked_workspace(tokens, num_seqs, H, P, groups, N, dtype) : 0;
 }
 
 conv_status conv_selective_scan_heads_fwd(const void *x, const int64_t *x_strides, const void *dt, int64_t dt_stride,
@@ -299,7 +300,7 @@ conv_status conv_selective_scan_heads_fwd(const void *x, const int64_t *x_stride
     p.N = N;
     p.softplus = softplus;
     p.dtype = dtype;
-    return launched(launch_heads_direct(p, (hipStream_t)stream));
+    return launched(tiled ? launch_heads_chunked(p, (hipStream_t)stream) : launch_heads_direct(p, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,893 @@
+// The selective scan with one decay a head, by chunks of 64 tokens on the
+// matrix cores, bf16 or fp32 operands, in fp32 precision.
+//
+// Inside a chunk let L_i be the sum of the exponents d a up to token i and S
+// [P,N] the state before the chunk. The 64 steps are
+//   Y  = diag(exp L) C S^T + M X,   M_ij = exp(L_i - L_j) d_j (c_i . b_j) for j <= i, else 0
+//   S' = exp(L_63) S + X^T diag(d_j exp(L_63 - L_j)) B
+// with the skipped input on M's diagonal. Sums and differences of L are taken
+// in 64 bits, so a strong decay early in a chunk costs the later ones nothing.
+//
+// A wave owns 16 CT rows of S (columns of X) of one head and keeps them in its
+// accumulators from chunk to chunk; as they leave one product they are the
+// operand of the next. Four such waves of one group share the chunk's B and C in
+// LDS, and the c . b of M, which each head in the workgroup turns into its own M.
+//
+// Long sequences are cut into segments of `seg` tokens where there are too few
+// heads to fill the chip: a first kernel makes the state that each segment but
+// a sequence's last leaves of nothing (the first one's: of the sequence's own
+// state), the second one puts together the state before its segment from those
+// of the segments before it.
+//
+// Precision: bf16 operands (B, C, X) are exact; every other operand (S, M, X
+// with its factors) and each fp32 one is split into three bf16 parts, x = hi +
+// mid + lo, 24 bits together, and the products of parts above 2^-24 are added
+// in fp32: three for an exact operand times a split one, six for two split ones.
+//
+// Values that are not finite: a zero of M times a NaN would carry it to earlier
+// tokens. So values of X, B and the step sizes that are not finite are read as
+// zeros and their token is noted; outputs from it on, and the state, are set to
+// NaN: a row of a head (X), a head (the step size) or a group (B).
+#include <type_traits>
+
+#include "common.h"
+#include "eight_bit.h"
+#include "internal.h"
+#include "scan_math.h"
+#include "sequences.h"
+
+namespace convfwd {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int Q = 64;                   // tokens of a chunk
+constexpr int NT = 256;
+constexpr int WAVES = 4;
+constexpr int NEVER = 0x7fffffff;
+constexpr int FRAG = 1024;              // 64 lanes x 16 bytes
+constexpr int MFRAGS = 6;               // 16 x 32 blocks of a lower triangle of 64
+
+struct HeadsArgs {
+    HeadScanProblem p;
+    float *states;          // workspace: a state for each segment number ...
+    float *decays;          // ... and its decay for each head
+    int seg;                // tokens of a segment
+    int units;              // segment numbers x groups
+    int slices;             // slices of 16 CT columns a head
+    int jobs;               // slices that a workgroup takes (waves past them help with what is shared)
+    int wgs;                // workgroups of a segment and group
+    int heads;              // most heads a workgroup's jobs belong to
+};
+
+// What a chunk's exponents come to for one head.
+struct __align__(16) Factors {
+    double L[Q];            // in units of log 2
+    float step[Q];          // d
+    float row[Q];           // 2^(L - L_31)
+    float col[Q];           // 2^(L_31 - L) d
+    float up[Q];            // 2^L
+    float tail[Q];          // 2^(L_63 - L) d
+    float total;            // 2^L_63
+    int wide;               // row and col may leave fp32's range
+    int bad;                // first token whose step is not finite
+    int pad;
+};
+
+// A barrier for LDS traffic only: __syncthreads would also wait for the loads
+// of the next chunk that are in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Eight values as bf16 parts, the nearest bf16 of what the parts before left.
+__device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&part)[3])
+{
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        float a = x[2 * h], b = x[2 * h + 1];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const bf16x2 t = __builtin_convertvector((f32x2{a, b}), bf16x2);
+            part[i][2 * h] = t[0];
+            part[i][2 * h + 1] = t[1];
+            if (i < 2) {
+                const uint32_t u = __builtin_bit_cast(uint32_t, t);
+                a -= __uint_as_float(u << 16);
+                b -= __uint_as_float(u & 0xffff0000u);
+            }
+        }
+    }
+}
+
+// acc += a b, each of one exact part or three.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 product(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 acc)
+{
+#pragma unroll
+    for (int k = 2; k >= 0; --k)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (k - i >= 0 && k - i < NB)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[k - i], acc, 0, 0, 0);
+    return acc;
+}
+
+// Four values of a column: of each 16 lanes, lane i gets value i % 4 of the
+// places of lanes i / 4, 4 + i / 4, 8 + i / 4 and 12 + i / 4.
+__device__ __forceinline__ bf16x4 transposed(const void *place)
+{
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                          (__attribute__((address_space(3))) i16x4 *)(place)));
+}
+
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// 2^x to an ulp or two whatever x is (the instruction's error grows with |x| only through its argument's rounding).
+__device__ __forceinline__ float power2(double x)
+{
+    const double n = rint(x);
+    return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
+}
+
+// Whether any of a piece's values is infinite or NaN: an exponent of all ones carries into the bit above it.
+template <bool F32>
+__device__ __forceinline__ uint32_t not_finite(const u32x4 &v)
+{
+    constexpr uint32_t E = F32 ? 0x7f800000u : 0x7f807f80u, ONE = F32 ? 0x00800000u : 0x00800080u;
+    return (((v[0] & E) + ONE) | ((v[1] & E) + ONE) | ((v[2] & E) + ONE) | ((v[3] & E) + ONE)) & ~(E | (ONE - 1)) &
+           (F32 ? 0x80000000u : 0x80008000u);
+}
+
+// KN steps of 32 states (N up to 32 KN), CT tiles of 16 columns a wave.
+// FULL: outputs and final states; else the states that segments leave. VEC:
+// 16-byte pieces of x, b, c and gate, and of states (a host rule).
+template <class T, int KN, int CT, bool FULL, bool VEC>
+struct Chunks {
+    static constexpr bool F32 = std::is_same<T, float>::value;
+    static constexpr int XP = F32 ? 3 : 1;          // parts of an operand as it lies in memory
+    static constexpr int E = 16 / sizeof(T);        // values of a piece
+    static constexpr int NP = 32 * KN, RC = 4 * KN; // states of a row in LDS, in pieces of eight
+    static constexpr int PB = 8 * KN / E;           // pieces of B, and of C, a thread
+    static constexpr int CW = 16 * CT;              // columns of a wave
+    static constexpr int PX = Q * CW / E / 64;      // pieces of X a lane
+    // LDS: B, C (each XP parts), then X of each wave (XP parts) which M takes the place of, then the factors and notes.
+    static constexpr int BBYTES = Q * NP * 2, XBYTES = Q * CW * 2;
+    static constexpr int C_AT = XP * BBYTES, X_AT = (FULL ? 2 : 1) * XP * BBYTES;
+
+    static __host__ __device__ int shared_at(int heads)
+    {
+        const int x = WAVES * XP * XBYTES, m = FULL ? heads * MFRAGS * 3 * FRAG : 0;
+        return X_AT + (x > m ? x : m);
+    }
+    static __host__ __device__ int lds(int heads)
+    {
+        return shared_at(heads) + 2 * heads * (int)sizeof(Factors) + WAVES * CW * 4 + 16;
+    }
+
+    // Byte of a row's piece, in an order in which neither the rows of a
+    // fragment nor the four rows of a transposed read meet in a bank.
+    static __device__ __forceinline__ int b_place(int row, int piece)
+    {
+        const int s = RC == 8 ? ((row >> 1) & 1) * 4 + ((row >> 3) & 3) : (row & 3) * 4 + ((row >> 3) & 3);
+        return (row * RC + (piece ^ s)) * 16;
+    }
+    static __device__ __forceinline__ int c_place(int row, int piece)
+    {
+        return (row * RC + (piece ^ (RC == 8 ? (row >> 1) & 7 : row & 15))) * 16;
+    }
+
+    static __device__ __forceinline__ void run(const HeadsArgs &a)
+    {
+        const HeadScanProblem &p = a.p;
+        extern __shared__ __align__(16) uint8_t lds_[];
+        uint8_t *const bs = lds_, *const cs = lds_ + C_AT, *const xm = lds_ + X_AT;
+        uint8_t *const after = lds_ + shared_at(a.heads);
+        Factors *const factors = reinterpret_cast<Factors *>(after);                    // [2][heads]
+        int *const badcol = reinterpret_cast<int *>(after + 2 * a.heads * sizeof(Factors));
+        int *const badb = badcol + WAVES * CW;                                           // [2]
+
+        // Workgroup i runs on XCD i % 8: those of one segment and group, which
+        // read the same B and C, go to one XCD and meet in its L2.
+        const int at = (int)blockIdx.x >> 3;
+        const int wg = at % a.wgs, unit = at / a.wgs * 8 + ((int)blockIdx.x & 7);
+        if (unit >= a.units)
+            return;
+        const int group = unit % p.groups, number = unit / p.groups;
+        const SeqTile tile = seq_tile(p.seq, a.seg, number);
+        const int64_t t0 = (int64_t)tile.index * a.seg;
+        if (t0 >= tile.len && tile.index != 0)
+            return;
+        const bool last = t0 + a.seg >= tile.len;
+        if (!FULL && last)
+            return;
+        const int64_t first = tile.begin + t0;
+        const int len = (int)(last ? tile.len - t0 : a.seg);
+        const int chunks = (len + Q - 1) / Q;
+
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int g = lane >> 4, c = lane & 15;
+        const int per = p.H / p.groups, group_jobs = per * a.slices;
+        const int job0 = wg * a.jobs, job1 = min(job0 + a.jobs, group_jobs);
+        const int head0 = job0 / a.slices, heads = (job1 - 1) / a.slices - head0 + 1;    // of this workgroup, in the group
+        const bool mine = job0 + w < job1;          // whether this wave has columns
+        const int job = mine ? job0 + w : job0;
+        const int hi = job / a.slices - head0;      // its head, of the workgroup's
+        const int h = group * per + head0 + hi;
+        const int col0 = job % a.slices * CW;
+
+        // ---- Loads.
+        const T *xp = static_cast<const T *>(p.x) + first * p.xst + h * p.xsh + col0;
+        const T *gp = p.gate ? static_cast<const T *>(p.gate) + first * p.gst + h * p.gsh + col0 : xp;
+        const int64_t gst = p.gate ? p.gst : p.xst;
+        const T *bp = static_cast<const T *>(p.b) + first * p.bst + group * p.bsg;
+        const T *cp = static_cast<const T *>(p.c) + first * p.cst + group * p.csg;
+        T *yp = static_cast<T *>(p.y) + first * p.yst + h * p.ysh + col0;
+        // Wave w < heads makes the factors of head head0 + w.
+        const int fh = group * per + head0 + min(w, heads - 1);
+        const T *dp = static_cast<const T *>(p.dt) + first * p.dts + fh;
+        const double rate = (double)p.a[fh] * 1.4426950408889634074;
+        const float bias = p.bias ? p.bias[fh] : 0.f;
+        const int cols = p.P - col0;                // columns there are, from the wave's first
+
+        u32x4 bv[PB], cv[FULL ? PB : 1], xv[PX];
+        T dv;
+        // A piece of a row; the values that are not there are zeros.
+        auto piece = [&](const T *row, int col, int width) __attribute__((always_inline)) {
+            if constexpr (VEC) {
+                return *reinterpret_cast<const u32x4 *>(row + (col < width ? col : 0));
+            } else {
+                T v[E] __attribute__((aligned(16))) = {};
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (col + e < width)
+                        v[e] = row[col + e];
+                return *reinterpret_cast<const u32x4 *>(v);
+            }
+        };
+        auto load_x = [&](int ch) __attribute__((always_inline)) {
+            const int rows = min(len - ch * Q, Q);
+            const T *base = xp + (int64_t)ch * Q * p.xst;
+#pragma unroll
+            for (int i = 0; i < PX; ++i) {
+                const int row = (i * 64 + lane) / (CW / E), col = (i * 64 + lane) % (CW / E) * E;
+                xv[i] = piece(base + min(row, rows - 1) * p.xst, col, cols);
+            }
+            dv = dp[(int64_t)(ch * Q + min(lane, rows - 1)) * p.dts];
+        };
+        auto load_bc = [&](int ch) __attribute__((always_inline)) {
+            const int rows = min(len - ch * Q, Q);
+            const T *bb = bp + (int64_t)ch * Q * p.bst, *cb = cp + (int64_t)ch * Q * p.cst;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const int row = (i * NT + tid) / (NP / E), col = (i * NT + tid) % (NP / E) * E;
+                bv[i] = piece(bb + min(row, rows - 1) * p.bst, col, p.N);
+                if constexpr (FULL)
+                    cv[i] = piece(cb + min(row, rows - 1) * p.cst, col, p.N);
+            }
+        };
+        // A piece's parts into LDS: in bf16 the piece itself, in fp32 half a piece of each part.
+        auto put = [&](uint8_t *at16, int part_bytes, const u32x4 &v, int half) __attribute__((always_inline)) {
+            if constexpr (F32) {
+                const f32x4 f = __builtin_bit_cast(f32x4, v);
+                f32x4 left = f;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const bf16x4 t = __builtin_convertvector(left, bf16x4);
+                    *reinterpret_cast<bf16x4 *>(at16 + i * part_bytes + 8 * half) = t;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        left[e] -= (float)t[e];
+                }
+            } else {
+                *reinterpret_cast<u32x4 *>(at16) = v;
+            }
+        };
+        // First bad value of a piece's columns -> note(column).
+        auto look = [&](u32x4 &v, auto note) {
+            T e[E] __attribute__((aligned(16)));
+            *reinterpret_cast<u32x4 *>(e) = v;
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (!(fabsf(load_as_f32(&e[i])) < INFINITY)) {
+                    note(i);
+                    e[i] = T(0);
+                }
+            v = *reinterpret_cast<const u32x4 *>(e);
+        };
+        auto put_bc = [&](int ch) __attribute__((always_inline)) {
+            const int rows = min(len - ch * Q, Q);
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const int row = (i * NT + tid) / (NP / E), col = (i * NT + tid) % (NP / E) * E;
+                u32x4 v = bv[i];
+                if (row >= rows || col >= p.N)
+                    v = u32x4{0, 0, 0, 0};
+                if (not_finite<F32>(v))
+                    look(v, [&](int) { atomicMin(badb + (ch & 1), row); });
+                put(bs + b_place(row, col / 8), BBYTES, v, col / 4 & 1);
+                if constexpr (FULL) {
+                    u32x4 u = cv[i];
+                    if (col >= p.N)
+                        u = u32x4{0, 0, 0, 0};
+                    put(cs + c_place(row, col / 8), BBYTES, u, col / 4 & 1);
+                }
+            }
+        };
+        // X of the wave's columns through its own part of LDS, as 8 tokens of a column a lane.
+        bf16x8 xf[2][CT][XP];
+        auto put_x = [&](int ch) __attribute__((always_inline)) {
+            const int rows = min(len - ch * Q, Q);
+            uint8_t *const own = xm + w * XP * XBYTES;
+#pragma unroll
+            for (int i = 0; i < PX; ++i) {
+                const int row = (i * 64 + lane) / (CW / E), col = (i * 64 + lane) % (CW / E) * E;
+                u32x4 v = xv[i];
+                if (row >= rows || col >= cols)
+                    v = u32x4{0, 0, 0, 0};
+                if (not_finite<F32>(v))
+                    look(v, [&](int e) { atomicMin(badcol + w * CW + col + e, row); });
+                put(own + row * CW * 2 + col / 8 * 16, XBYTES, v, col / 4 & 1);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int i = 0; i < XP; ++i) {
+                        // Tile ct holds columns 8 q + 4 ct + (0 .. 3) (one tile: 4 q + ..), q = c / 4.
+                        const uint8_t *t = own + i * XBYTES + (32 * s + 8 * g + (c >> 2)) * CW * 2 + (c & 3) * 8 * CT + 8 * ct;
+                        xf[s][ct][i] = join(transposed(t), transposed(t + 4 * CW * 2));
+                    }
+        };
+        double exponent = 0.0;      // of the whole segment, in wave w < heads
+        auto make_factors = [&](int ch) __attribute__((always_inline)) {
+            if (w >= heads)
+                return;
+            Factors &f = factors[(ch & 1) * a.heads + w];
+            float d = step_size(load_as_f32(&dv) + bias, p.softplus);
+            // Exponents past +-10000 are 0 and infinity either way.
+            double e = fmin(fmax((double)d * rate, -1e4), 1e4);
+            const bool here = lane < len - ch * Q;
+            const bool bad = here && !(fabsf(d) < INFINITY);
+            const uint64_t bads = __ballot(bad);
+            if (!here || bad) {
+                d = 0.f;
+                e = 0.0;
+            }
+#pragma unroll
+            for (int i = 1; i < 64; i <<= 1) {
+                const double o = __shfl_up(e, i);
+                if (lane >= i)
+                    e += o;
+            }
+            const double mid = __shfl(e, 31), end = __shfl(e, 63);
+            exponent += end;
+            const bool wide = __any(!(fabs(e - mid) <= 60.0));
+            f.tail[lane] = power2(end - e) * d;
+            if constexpr (FULL) {
+                f.L[lane] = e;
+                f.step[lane] = d;
+                f.row[lane] = power2(e - mid);
+                f.col[lane] = power2(mid - e) * d;
+                f.up[lane] = power2(e);
+            }
+            if (lane == 0) {
+                f.total = power2(end);
+                f.wide = wide;
+                f.bad = bads ? __builtin_ctzll(bads) : NEVER;
+            }
+        };
+
+        if (tid < WAVES * CW)
+            badcol[tid] = NEVER;
+        if (tid < 2)
+            badb[tid] = NEVER;
+
+        // ---- The state before the segment. Column p of a tile (of lane c) is
+        // row p of S; a lane has 4 rows n of each of 2 KN tiles, which
+        // interleave, so that a pair of them is 8 adjacent n.
+        const int prow[2] = {col0 + (CT == 2 ? 8 * (c >> 2) + (c & 3) : c), col0 + 8 * (c >> 2) + 4 + (c & 3)};
+        const int64_t head_state = (int64_t)p.P * p.N;
+        auto state_at = [&](const float *s, int64_t index, int ct, int nt) {
+            return s + (index * p.H + h) * head_state + (int64_t)prow[ct] * p.N + 32 * (nt >> 1) + 8 * g + 4 * (nt & 1);
+        };
+        auto read4 = [&](const float *s, int ct, int nt) __attribute__((always_inline)) {
+            const int n = 32 * (nt >> 1) + 8 * g + 4 * (nt & 1);
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            if (prow[ct] < p.P && n < p.N) {
+                if constexpr (VEC) {
+                    v = *reinterpret_cast<const f32x4 *>(s);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < p.N)
+                            v[e] = s[e];
+                }
+            }
+            return v;
+        };
+        f32x4 S[2 * KN][CT];
+        auto write_state = [&](float *s, int64_t index) __attribute__((always_inline)) {
+#pragma unroll
+            for (int nt = 0; nt < 2 * KN; ++nt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const int n = 32 * (nt >> 1) + 8 * g + 4 * (nt & 1);
+                    float *to = const_cast<float *>(state_at(s, index, ct, nt));
+                    if (mine && prow[ct] < p.P && n < p.N) {
+                        if constexpr (VEC) {
+                            *reinterpret_cast<f32x4 *>(to) = S[nt][ct];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (n + e < p.N)
+                                    to[e] = S[nt][ct][e];
+                        }
+                    }
+                }
+        };
+        const int slot = p.state_in || p.state_out ? seq_slot(p.seq, tile.n) : -1;
+        const int64_t first_number = number - tile.index;
+        const int64_t last_number = first_number + (tile.len > 0 ? (tile.len - 1) / a.seg : 0);
+        bool held = false;          // whether S may hold anything
+#pragma unroll
+        for (int nt = 0; nt < 2 * KN; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                S[nt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (tile.index == 0 && (!FULL || last)) {
+            if (p.state_in && slot >= 0) {
+                held = true;
+#pragma unroll
+                for (int nt = 0; nt < 2 * KN; ++nt)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        S[nt][ct] = read4(state_at(p.state_in, slot, ct, nt), ct, nt);
+            }
+            // A sequence of several segments: what its last one may overwrite
+            // before its first one has read it is kept in the place of the
+            // state that the last one does not leave.
+            if (!FULL)
+                write_state(a.states, last_number);
+        } else if (FULL) {
+            held = true;
+            const int64_t from = tile.index == 0 ? last_number : first_number;
+#pragma unroll
+            for (int nt = 0; nt < 2 * KN; ++nt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    S[nt][ct] = read4(state_at(a.states, from, ct, nt), ct, nt);
+            for (int64_t k = first_number + 1; k < number; ++k) {
+                const float by = a.decays[k * p.H + h];
+#pragma unroll
+                for (int nt = 0; nt < 2 * KN; ++nt)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        const f32x4 v = read4(state_at(a.states, k, ct, nt), ct, nt);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            S[nt][ct][e] = fmaf(by, S[nt][ct][e], v[e]);
+                    }
+            }
+        }
+
+        if (chunks > 0) {
+            load_x(0);
+            load_bc(0);
+            make_factors(0);
+        }
+        lds_barrier();              // the notes are set
+        for (int ch = 0; ch < chunks; ++ch) {
+            const int rows = min(len - ch * Q, Q);
+            if constexpr (!VEC) {
+                if (ch > 0)
+                    load_bc(ch);
+            }
+            put_bc(ch);
+            put_x(ch);
+            lds_barrier();
+            const Factors *const fs = factors + (ch & 1) * a.heads;
+            if (ch + 1 < chunks) {
+                load_x(ch + 1);
+                if constexpr (VEC)
+                    load_bc(ch + 1);
+            }
+            if (tid == 0)
+                badb[(ch + 1) & 1] = NEVER;     // last read before the barrier that ended the chunk before
+            // The gate (x in its place where there is none) of the columns V g + .. of tokens 16 it + c.
+            constexpr int V = 4 * CT;
+            struct Gate {
+                T v[V] __attribute__((aligned(V * sizeof(T) < 16 ? V * sizeof(T) : 16)));
+            };
+            Gate gate[FULL ? 4 : 1];
+            f32x4 acc[4][CT];
+            if constexpr (FULL) {
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const T *gr = gp + ((int64_t)ch * Q + min(16 * it + c, rows - 1)) * gst;
+                    if constexpr (VEC) {
+                        __builtin_memcpy(&gate[it], __builtin_assume_aligned(gr + (V * g < cols ? V * g : 0), alignof(Gate)),
+                                         sizeof(Gate));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            gate[it].v[e] = gr[V * g + e < cols ? V * g + e : 0];
+                    }
+                }
+                // M^T's blocks: tokens i of tile `it` as columns, 32 tokens j of step s as rows, two interleaving
+                // tiles, so that a lane has 8 adjacent j of one i: an operand of the product with X.
+                auto block = [&](int it, int s, int f) __attribute__((always_inline)) {
+                    f32x4 raw[2];
+                    raw[0] = raw[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < KN; ++ks) {
+                        bf16x8 cf[XP], bf[XP];
+#pragma unroll
+                        for (int i = 0; i < XP; ++i)
+                            cf[i] = *reinterpret_cast<const bf16x8 *>(cs + i * BBYTES + c_place(16 * it + c, 4 * ks + g));
+#pragma unroll
+                        for (int tj = 0; tj < 2; ++tj) {
+#pragma unroll
+                            for (int i = 0; i < XP; ++i)
+                                bf[i] = *reinterpret_cast<const bf16x8 *>(
+                                    bs + i * BBYTES + b_place(32 * s + 8 * (c >> 2) + 4 * tj + (c & 3), 4 * ks + g));
+                            raw[tj] = product(bf, cf, raw[tj]);
+                        }
+                    }
+                    const int ti = 16 * it + c, tj0 = 32 * s + 8 * g;
+                    for (int k = 0; k < heads; ++k) {
+                        const Factors &fk = fs[k];
+                        float m[8];
+                        if (!fk.wide) {
+                            const float r = fk.row[ti];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                m[e] = raw[e >> 2][e & 3] * fk.col[tj0 + e] * r;
+                        } else {
+                            const double Li = fk.L[ti];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                m[e] = raw[e >> 2][e & 3] * fk.step[tj0 + e] * power2(Li - fk.L[tj0 + e]);
+                        }
+                        if (it >> 1 == s) {
+                            const float own = p.skip ? p.skip[group * per + head0 + k] : 0.f;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                m[e] = tj0 + e <= ti ? m[e] : 0.f;
+                                m[e] = tj0 + e == ti ? m[e] + own : m[e];
+                            }
+                        }
+                        bf16x8 part[3];
+                        split8(m, part);
+#pragma unroll
+                        for (int i = 0; i < 3; ++i)
+                            reinterpret_cast<bf16x8 *>(xm + ((k * MFRAGS + f) * 3 + i) * FRAG)[lane] = part[i];
+                    }
+                };
+                // Blocks (1,0) (2,0) (3,0)+(0,0) (3,1)+(2,1) of waves 0 to 3.
+                const int it1 = w < 3 ? w + 1 : 3, s1 = w == 3, it2 = w == 2 ? 0 : 2, s2 = w == 3;
+                block(it1, s1, w < 2 ? w : 2 * w - 2);
+                if (w >= 2)
+                    block(it2, s2, 2 * w - 1);
+
+                // Y^T: S C^T.
+#pragma unroll
+                for (int it = 0; it < 4; ++it)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        acc[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (held) {
+#pragma unroll
+                    for (int ks = 0; ks < KN; ++ks) {
+                        bf16x8 sp[CT][3];
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) {
+                            float v[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                v[e] = S[2 * ks + (e >> 2)][ct][e & 3];
+                            split8(v, sp[ct]);
+                        }
+#pragma unroll
+                        for (int it = 0; it < 4; ++it) {
+                            bf16x8 cf[XP];
+#pragma unroll
+                            for (int i = 0; i < XP; ++i)
+                                cf[i] = *reinterpret_cast<const bf16x8 *>(cs + i * BBYTES + c_place(16 * it + c, 4 * ks + g));
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct)
+                                acc[it][ct] = product(sp[ct], cf, acc[it][ct]);
+                        }
+                    }
+                }
+                lds_barrier();
+            }
+            const Factors &f = fs[hi];
+            const int bad_all = min(f.bad, badb[ch & 1]);
+            const bool bad = bad_all != NEVER || __any(badcol[w * CW + (lane & (CW - 1))] != NEVER);
+            if constexpr (FULL) {
+                const uint8_t *const ms = xm + hi * MFRAGS * 3 * FRAG;
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const float up = f.up[16 * it + c];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        acc[it][ct] *= up;
+#pragma unroll
+                    for (int s = 0; s <= it >> 1; ++s) {
+                        // Block (it, s) is number 0 1 2 4 for (1,0) (2,0) (3,0) (3,1), 3 for (0,0) and 5 for (2,1).
+                        const int fr = it == 0 ? 3 : s == 0 ? it - 1 : it == 3 ? 4 : 5;
+                        bf16x8 mf[3];
+#pragma unroll
+                        for (int i = 0; i < 3; ++i)
+                            mf[i] = reinterpret_cast<const bf16x8 *>(ms + (fr * 3 + i) * FRAG)[lane];
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+                            acc[it][ct] = product(xf[s][ct], mf, acc[it][ct]);
+                    }
+                    const int t = 16 * it + c;
+                    const int64_t tok = (int64_t)ch * Q + min(t, rows - 1);
+                    const int at0 = V * g;
+                    float y[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        y[e] = acc[it][e >> 2][e & 3];
+                    if (p.gate) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            y[e] *= silu(load_as_f32(&gate[it].v[e]));
+                    }
+                    if (bad) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            if (t >= min(bad_all, badcol[w * CW + at0 + e]))
+                                y[e] = NAN;
+                    }
+                    if (mine && t < rows) {
+                        T *yr = yp + tok * p.yst + at0;
+                        Gate o;
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            store_rne(&o.v[e], y[e]);
+                        if constexpr (VEC) {
+                            if (at0 < cols)
+                                __builtin_memcpy(__builtin_assume_aligned(yr, alignof(Gate)), &o, sizeof(o));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < V; ++e)
+                                if (at0 + e < cols)
+                                    yr[e] = o.v[e];
+                        }
+                    }
+                }
+            }
+            if (ch + 1 < chunks)
+                make_factors(ch + 1);
+
+            // S' = total S + B^T (tail x).
+            const float total = f.total;
+#pragma unroll
+            for (int nt = 0; nt < 2 * KN; ++nt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    S[nt][ct] = held ? S[nt][ct] * total : S[nt][ct];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                bf16x8 xw[CT][3];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float x = (float)xf[s][ct][0][e];
+                        if constexpr (F32)
+                            x = x + (float)xf[s][ct][1][e] + (float)xf[s][ct][2][e];
+                        v[e] = x * f.tail[32 * s + 8 * g + e];
+                    }
+                    split8(v, xw[ct]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < 2 * KN; ++nt) {
+                    bf16x8 bt[XP];
+#pragma unroll
+                    for (int i = 0; i < XP; ++i) {
+                        const int row = 32 * s + 8 * g + (c >> 2), pc = 4 * (nt >> 1) + (c & 3);
+                        const uint8_t *b0 = bs + i * BBYTES + 8 * (nt & 1);
+                        bt[i] = join(transposed(b0 + b_place(row, pc)), transposed(b0 + b_place(row + 4, pc)));
+                    }
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        S[nt][ct] = product(bt, xw[ct], S[nt][ct]);
+                }
+            }
+            held = true;
+            if (bad) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    if (bad_all != NEVER || badcol[w * CW + prow[ct] - col0] != NEVER)
+#pragma unroll
+                        for (int nt = 0; nt < 2 * KN; ++nt)
+                            S[nt][ct] = f32x4{NAN, NAN, NAN, NAN};
+                if (lane < CW)
+                    badcol[w * CW + lane] = NEVER;
+            }
+            lds_barrier();
+        }
+        if (FULL && last && p.state_out && slot >= 0)
+            write_state(p.state_out, slot);
+        if (!FULL) {
+            write_state(a.states, number);
+            if (w < heads && lane == 0)
+                a.decays[(int64_t)number * p.H + fh] = power2(exponent);
+        }
+    }
+};
+
+template <class T, int KN, int CT, bool FULL, bool VEC>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(std::is_same<T, float>::value || KN > 4 ? 1 : 2))) void
+heads_chunk_kernel(HeadsArgs a)
+{
+    Chunks<T, KN, CT, FULL, VEC>::run(a);
+}
+
+constexpr int LDS_MOST = 160 * 1024;
+
+// How a call is laid out: everything that follows from its sizes alone.
+struct Plan {
+    int kn, ct, slices, jobs, wgs, heads, seg;
+    int64_t numbers;        // segments, numbered as in sequences.h
+    bool parts;             // segments are shorter than a sequence may be
+};
+
+int most_heads(int jobs, int slices)
+{
+    return slices % jobs == 0 ? 1 : jobs % slices == 0 ? jobs / slices : (jobs - 2) / slices + 2;
+}
+
+int lds_bytes(bool f32, int kn, int heads)
+{
+    if (f32)
+        return kn == 2 ? Chunks<float, 2, 1, true, true>::lds(heads) : Chunks<float, 4, 1, true, true>::lds(heads);
+    return kn == 2   ? Chunks<uint16_t, 2, 2, true, true>::lds(heads)
+           : kn == 4 ? Chunks<uint16_t, 4, 2, true, true>::lds(heads)
+                     : Chunks<uint16_t, 8, 1, true, true>::lds(heads);
+}
+
+bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype dtype, Plan *l)
+{
+    const bool f32 = dtype == CONV_F32;
+    if (N > (f32 ? 128 : 256))
+        return false;
+    l->kn = N <= 64 ? 2 : N <= 128 ? 4 : 8;
+    l->ct = f32 || l->kn == 8 ? 1 : 2;
+    l->slices = (P + 16 * l->ct - 1) / (16 * l->ct);
+    l->jobs = WAVES;
+    l->heads = most_heads(l->jobs, l->slices);
+    while (lds_bytes(f32, l->kn, l->heads) > LDS_MOST) {
+        l->jobs /= 2;
+        l->heads = most_heads(l->jobs, l->slices);
+    }
+    const int64_t group_jobs = (int64_t)(H / groups) * l->slices;
+    if (group_jobs > (1 << 22))
+        return false;
+    l->wgs = (int)((group_jobs + l->jobs - 1) / l->jobs);
+    // Segments such that some 512 workgroups have one, but at most 16 to the longest sequence there can be (a
+    // segment reads the states of all before it), and none of less than 256 tokens.
+    const int64_t longest = s.offsets ? s.tokens : s.each;
+    int64_t seg = s.tokens * l->wgs * groups / 512;
+    seg = seg > longest / 16 ? seg : longest / 16;
+    seg = seg > 256 ? seg : 256;
+    seg = (seg + Q - 1) / Q * Q;
+    l->parts = seg < longest;
+    if (!l->parts)
+        seg = (longest + Q) / Q * Q;
+    if (seg > (1 << 30))
+        return false;
+    l->seg = (int)seg;
+    l->numbers = seq_tiles(s, l->seg);
+    // Threads of the grid below 2^32.
+    return (l->numbers * groups + 7) / 8 * 8 * l->wgs < (int64_t(1) << 24);
+}
+
+Sequences sequences_of(int64_t tokens, int num_seqs, bool equal)
+{
+    Sequences s = {};
+    static const int32_t some = 0;
+    s.offsets = equal ? nullptr : &some;        // only whether there are offsets counts here
+    s.num_seqs = num_seqs;
+    s.tokens = tokens;
+    s.each = tokens / num_seqs;
+    return s;
+}
+
+int64_t space(const Plan &l, int H, int P, int N)
+{
+    if (!l.parts)
+        return 0;
+    const int64_t states = (l.numbers * H * P * N * 4 + 255) / 256 * 256;
+    return states + (l.numbers * H * 4 + 255) / 256 * 256;
+}
+
+template <class T, int KN, int CT, bool FULL>
+hipError_t launch_pass(const HeadsArgs &a, unsigned grid, bool vec, hipStream_t s)
+{
+    const int lds = Chunks<T, KN, CT, FULL, true>::lds(a.heads);
+    hipError_t e;
+    if (vec) {
+        e = allow_lds<heads_chunk_kernel<T, KN, CT, FULL, true>>(LDS_MOST);
+        if (e == hipSuccess)
+            hipLaunchKernelGGL((heads_chunk_kernel<T, KN, CT, FULL, true>), dim3(grid), dim3(NT), lds, s, a);
+    } else {
+        e = allow_lds<heads_chunk_kernel<T, KN, CT, FULL, false>>(LDS_MOST);
+        if (e == hipSuccess)
+            hipLaunchKernelGGL((heads_chunk_kernel<T, KN, CT, FULL, false>), dim3(grid), dim3(NT), lds, s, a);
+    }
+    return e == hipSuccess ? hipGetLastError() : e;
+}
+
+template <class T, int KN, int CT>
+hipError_t launch(const HeadsArgs &a, bool parts, bool vec, hipStream_t s)
+{
+    const unsigned grid = (unsigned)((a.units + 7) / 8 * 8 * a.wgs);
+    if (parts) {
+        const hipError_t e = launch_pass<T, KN, CT, false>(a, grid, vec, s);
+        if (e != hipSuccess)
+            return e;
+    }
+    return launch_pass<T, KN, CT, true>(a, grid, vec, s);
+}
+
+}  // namespace
+
+bool heads_chunked_supports(int64_t tokens, int num_seqs, int H, int P, int groups, int N, conv_dtype dtype)
+{
+    Plan l;
+    return make_plan(sequences_of(tokens, num_seqs, false), H, P, groups, N, dtype, &l) &&
+           make_plan(sequences_of(tokens, num_seqs, true), H, P, groups, N, dtype, &l);
+}
+
+int64_t heads_chunked_workspace(int64_t tokens, int num_seqs, int H, int P, int groups, int N, conv_dtype dtype)
+{
+    Plan packed, equal;         // the larger of the two ways in which the sequences may lie
+    make_plan(sequences_of(tokens, num_seqs, false), H, P, groups, N, dtype, &packed);
+    make_plan(sequences_of(tokens, num_seqs, true), H, P, groups, N, dtype, &equal);
+    const int64_t x = space(packed, H, P, N), y = space(equal, H, P, N);
+    return x > y ? x : y;
+}
+
+hipError_t launch_heads_chunked(const HeadScanProblem &p, hipStream_t s)
+{
+    Plan l;
+    make_plan(p.seq, p.H, p.P, p.groups, p.N, p.dtype, &l);
+    HeadsArgs a;
+    a.p = p;
+    a.states = static_cast<float *>(p.workspace);
+    a.decays = a.states + (l.numbers * p.H * p.P * p.N + 63) / 64 * 64;
+    a.seg = l.seg;
+    a.units = (int)(l.numbers * p.groups);
+    a.slices = l.slices;
+    a.jobs = l.jobs;
+    a.wgs = l.wgs;
+    a.heads = l.heads;
+    const int64_t e = p.dtype == CONV_F32 ? 4 : 2;
+    const uintptr_t strides = (uintptr_t)((p.xst | p.xsh | p.yst | p.ysh | p.bst | p.bsg | p.cst | p.csg) * e) |
+                              (p.gate ? (uintptr_t)((p.gst | p.gsh) * e) : 0);
+    const uintptr_t at = (uintptr_t)p.x | (uintptr_t)p.y | (uintptr_t)p.b | (uintptr_t)p.c | (uintptr_t)p.gate |
+                         (uintptr_t)p.state_in | (uintptr_t)p.state_out;
+    const bool vec = (strides | at) % 16 == 0 && p.P % (16 / e) == 0 && p.N % (16 / e) == 0;
+    if (p.dtype == CONV_F32)
+        return l.kn == 2 ? launch<float, 2, 1>(a, l.parts, vec, s) : launch<float, 4, 1>(a, l.parts, vec, s);
+    return l.kn == 2   ? launch<uint16_t, 2, 2>(a, l.parts, vec, s)
+           : l.kn == 4 ? launch<uint16_t, 4, 2>(a, l.parts, vec, s)
+                       : launch<uint16_t, 8, 1>(a, l.parts, vec, s);
+}
+
+}  // namespace convfwd

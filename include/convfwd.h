@@ -550,7 +550,12 @@ CONVFWD_API int64_t conv_selective_scan_workspace(int64_t tokens, int num_seqs, 
  *   workspace  device memory of at least conv_selective_scan_heads_workspace
  *              bytes, 256-byte aligned, used during the call only (NULL when
  *              that is 0).
- *   variant    CONV_VARIANT_DIRECT: token by token. CONV_VARIANT_AUTO: the same.
+ *   variant    CONV_VARIANT_DIRECT: token by token. CONV_VARIANT_TILED: by
+ *              chunks of 64 tokens on the matrix cores, N <= 128 in fp32. Both
+ *              compute in fp32 precision, and refuse with
+ *              CONV_ERR_UNSUPPORTED what their grids do not hold.
+ *              CONV_VARIANT_AUTO picks one for the whole call from tokens /
+ *              num_seqs, the only lengths known on the host.
  *
  * A value that is not finite, or leaves fp32's range, reaches no earlier
  * token, no other group and no other sequence.

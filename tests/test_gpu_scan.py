@@ -66,9 +66,35 @@ def test_channels(C, G, N, lens, dtype):
 @pytest.mark.parametrize("lens", RAGGED, ids=str)
 @pytest.mark.parametrize("H,P,G,N", [(1, 1, 1, 1), (2, 5, 1, 3), (4, 16, 2, 16), (3, 64, 1, 64), (4, 33, 4, 100), (6, 64, 2, 128),
                                      (2, 80, 1, 30), (2, 128, 2, 200), (1, 24, 1, 256)])
-def test_heads(H, P, G, N, lens, dtype):
+@pytest.mark.parametrize("variant", [DIRECT, TILED])
+def test_heads(H, P, G, N, lens, dtype, variant):
+    if variant == TILED and dtype == F32 and N > 128:
+        pytest.skip("chunks of fp32 take up to 128 states")
     ins = head_inputs(sum(lens), H, P, G, N, dtype, H + P + N)
-    check(cf.selective_scan_heads, ins, lens, rnd((len(lens), H, P, N), 1))
+    check(cf.selective_scan_heads, ins, lens, rnd((len(lens), H, P, N), 1), variant)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens,H,P,G,N", [([700, 3, 0, 297], 2, 32, 1, 64), ([1000], 1, 64, 1, 128), ([5000], 1, 16, 1, 16),
+                                          ([256, 512, 257], 3, 40, 3, 128), ([900, 900], 2, 20, 1, 30)], ids=str)
+def test_heads_in_segments(lens, H, P, G, N, dtype):
+    """Sequences past one segment, states updated in place; without offsets where they are equally long."""
+    ins, st = head_inputs(sum(lens), H, P, G, N, dtype, 21), rnd((len(lens), H, P, N), 22)
+    y0, by, h0, bh = ref.heads(*ins, True, lens, st)
+    x, dt, a, b, c, skip, gate, bias = gpu(ins)
+    kw = dict(skip=skip, dt_bias=bias, dt_softplus=True, variant=TILED)
+    pool = st.to(DEV)
+    y = cf.selective_scan_heads(x, dt, a, b, c, gate=gate, seq_offsets=seqs(lens, DEV), initial_state=pool, final_state=pool,
+                                **kw)
+    mixer_ref.check(y, y0, by, "y", dtype)
+    mixer_ref.check(pool, h0, bh, "state", F32)
+    if len(set(lens)) == 1:
+        n = len(lens)
+        x, dt, b, c, gate = (t.unflatten(0, (n, -1)) for t in (x, dt, b, c, gate))
+        pool = st.to(DEV)
+        y = cf.selective_scan_heads(x, dt, a, b, c, gate=gate, initial_state=pool, final_state=pool, **kw)
+        mixer_ref.check(y.flatten(0, 1), y0, by, "equal, y", dtype)
+        mixer_ref.check(pool, h0, bh, "equal, state", F32)
 
 
 @pytest.mark.parametrize("softplus", [False, True])
@@ -186,12 +212,13 @@ def test_channels_not_finite(which, at, value, dtype):
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("at", [0, 37, 63, 64, 99])
 @pytest.mark.parametrize("which", ["x", "dt", "b", "c", "state"])
-def test_heads_not_finite(which, at, value, dtype):
+@pytest.mark.parametrize("variant", [DIRECT, TILED])
+def test_heads_not_finite(variant, which, at, value, dtype):
     """What is not finite reaches no earlier token, no other row of a head (dt: no other head; b, c: no other group) and
     no other sequence."""
     ins = list(head_inputs(130, 4, 32, 2, 64, dtype, 9))
     lens, st = [100, 30], rnd((2, 4, 32, 64), 10)
-    clean, new0 = run(cf.selective_scan_heads, ins, lens, st)
+    clean, new0 = run(cf.selective_scan_heads, ins, lens, st, variant)
     bad = list(ins)
     i = dict(x=0, dt=1, b=3, c=4).get(which)
     hit = torch.zeros(130, 4, 32, dtype=torch.bool)
@@ -212,7 +239,7 @@ def test_heads_not_finite(which, at, value, dtype):
         else:
             bad[i][at, 1, 5] = value
             hit[at:100, 1, 5] = held[0, 1, 5] = True
-    y, new = run(cf.selective_scan_heads, bad, lens, st)
+    y, new = run(cf.selective_scan_heads, bad, lens, st, variant)
     assert torch.equal(y.cpu()[~hit], clean.cpu()[~hit]) and torch.equal(new.cpu()[~held], new0.cpu()[~held])
     if which != "state" and not (which == "dt" and value > 0):
         assert not torch.isfinite(y.cpu()[at][hit[at]]).any()
@@ -229,10 +256,13 @@ def test_strong_decays_and_steps():
         ins[1][40] = 3000.0
         ins[1][50:60] = -200.0          # steps of zero
         ins[1][66] = 60.0
-        check(fn, ins, lens, rnd((2,) + shape, 12))
+        variants = [AUTO, DIRECT] + [TILED] * (fn is cf.selective_scan_heads)
+        for v in variants:
+            check(fn, ins, lens, rnd((2,) + shape, 12), v)
         ins[1] = ins[1].clamp(-3, 0.5)
         ins[2] = -0.05 * ins[2]         # growth
-        check(fn, ins, lens, rnd((2,) + shape, 12))
+        for v in variants:
+            check(fn, ins, lens, rnd((2,) + shape, 12), v)
 
 
 def test_refusals():
