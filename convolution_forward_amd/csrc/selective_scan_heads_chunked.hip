@@ -49,8 +49,6 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int Q = 64;                   // tokens of a chunk
-constexpr int NT = 256;
-constexpr int WAVES = 4;
 constexpr int NEVER = 0x7fffffff;
 constexpr int FRAG = 1024;              // 64 lanes x 16 bytes
 constexpr int MFRAGS = 6;               // 16 x 32 blocks of a lower triangle of 64
@@ -67,18 +65,20 @@ struct HeadsArgs {
     int heads;              // most heads a workgroup's jobs belong to
 };
 
-// What a chunk's exponents come to for one head.
+// What a chunk's exponents come to for one head: what M needs, and what the
+// products after it do, while the next chunk's are made.
 struct __align__(16) Factors {
     double L[Q];            // in units of log 2
     float step[Q];          // d
     float row[Q];           // 2^(L - L_31)
     float col[Q];           // 2^(L_31 - L) d
-    float up[Q];            // 2^L
-    float tail[Q];          // 2^(L_63 - L) d
-    float total;            // 2^L_63
-    int wide;               // row and col may leave fp32's range
-    int bad;                // first token whose step is not finite
-    int pad;
+    struct __align__(16) {
+        float up[Q];        // 2^L
+        float tail[Q];      // 2^(L_63 - L) d
+        float total;        // 2^L_63
+        int wide;           // row and col may leave fp32's range
+        int bad;            // first token whose step is not finite
+    } of[2];
 };
 
 // A barrier for LDS traffic only: __syncthreads would also wait for the loads
@@ -86,6 +86,9 @@ struct __align__(16) Factors {
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // Eight values as bf16 parts, the nearest bf16 of what the parts before left.
+// (A remainder is one v_dot2_f32_bf16 with (-1, 0) too, exactly, but those
+// share the matrix cores: beside a wave of matrix instructions one takes 22
+// clocks, a subtraction or mask 8.6.)
 __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&part)[3])
 {
 #pragma unroll
@@ -128,6 +131,24 @@ __device__ __forceinline__ bf16x4 transposed(const void *place)
 
 __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
+// A double from another lane (a DPP control), or zero: lanes shifted from
+// outside their row of 16, and rows that ROWS leaves out.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ double of_lane(double v, int lane)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, lane), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // 2^x to an ulp or two whatever x is (the instruction's error grows with |x| only through its argument's rounding).
 __device__ __forceinline__ float power2(double x)
 {
@@ -147,18 +168,24 @@ __device__ __forceinline__ uint32_t not_finite(const u32x4 &v)
 // KN steps of 32 states (N up to 32 KN), CT tiles of 16 columns a wave.
 // FULL: outputs and final states; else the states that segments leave. VEC:
 // 16-byte pieces of x, b, c and gate, and of states (a host rule).
-template <class T, int KN, int CT, bool FULL, bool VEC>
+template <class T, int KN, int CT, int WAVES, bool FULL, bool VEC>
 struct Chunks {
+    static constexpr int NT = 64 * WAVES;
     static constexpr bool F32 = std::is_same<T, float>::value;
     static constexpr int XP = F32 ? 3 : 1;          // parts of an operand as it lies in memory
     static constexpr int E = 16 / sizeof(T);        // values of a piece
     static constexpr int NP = 32 * KN, RC = 4 * KN; // states of a row in LDS, in pieces of eight
-    static constexpr int PB = 8 * KN / E;           // pieces of B, and of C, a thread
+    static constexpr int PB = Q * NP / E / NT;      // pieces of B, and of C, a thread
     static constexpr int CW = 16 * CT;              // columns of a wave
     static constexpr int PX = Q * CW / E / 64;      // pieces of X a lane
     // LDS: B, C (each XP parts), then X of each wave (XP parts) which M takes the place of, then the factors and notes.
-    static constexpr int BBYTES = Q * NP * 2, XBYTES = Q * CW * 2;
-    static constexpr int C_AT = XP * BBYTES, X_AT = (FULL ? 2 : 1) * XP * BBYTES;
+    // Rows of C are a piece longer than their states, so that 16 of them begin in 16 different groups of four banks;
+    // those of B four pieces, and each eight of them another, which keeps apart both the rows 8 i + j (i, j < 4) of a
+    // fragment and the four pieces of four rows of a transposed read. (Pieces exchanged within a row would do so
+    // without the room, but then every place is an address of its own, and they took 50 registers.)
+    static constexpr int BROW = (RC + 4) * 16, CROW = (RC + 1) * 16;
+    static constexpr int BBYTES = Q * BROW + Q / 8 * 16, CBYTES = Q * CROW, XBYTES = Q * CW * 2;
+    static constexpr int C_AT = XP * BBYTES, X_AT = C_AT + (FULL ? XP * CBYTES : 0);
 
     static __host__ __device__ int shared_at(int heads)
     {
@@ -167,20 +194,11 @@ struct Chunks {
     }
     static __host__ __device__ int lds(int heads)
     {
-        return shared_at(heads) + 2 * heads * (int)sizeof(Factors) + WAVES * CW * 4 + 16;
+        return shared_at(heads) + heads * (int)sizeof(Factors) + WAVES * CW * 4 + 16;
     }
 
-    // Byte of a row's piece, in an order in which neither the rows of a
-    // fragment nor the four rows of a transposed read meet in a bank.
-    static __device__ __forceinline__ int b_place(int row, int piece)
-    {
-        const int s = RC == 8 ? ((row >> 1) & 1) * 4 + ((row >> 3) & 3) : (row & 3) * 4 + ((row >> 3) & 3);
-        return (row * RC + (piece ^ s)) * 16;
-    }
-    static __device__ __forceinline__ int c_place(int row, int piece)
-    {
-        return (row * RC + (piece ^ (RC == 8 ? (row >> 1) & 7 : row & 15))) * 16;
-    }
+    static __host__ __device__ constexpr int b_place(int row, int piece) { return row * BROW + (row >> 3) * 16 + piece * 16; }
+    static __host__ __device__ constexpr int c_place(int row, int piece) { return row * CROW + piece * 16; }
 
     static __device__ __forceinline__ void run(const HeadsArgs &a)
     {
@@ -188,8 +206,8 @@ struct Chunks {
         extern __shared__ __align__(16) uint8_t lds_[];
         uint8_t *const bs = lds_, *const cs = lds_ + C_AT, *const xm = lds_ + X_AT;
         uint8_t *const after = lds_ + shared_at(a.heads);
-        Factors *const factors = reinterpret_cast<Factors *>(after);                    // [2][heads]
-        int *const badcol = reinterpret_cast<int *>(after + 2 * a.heads * sizeof(Factors));
+        Factors *const factors = reinterpret_cast<Factors *>(after);                    // [heads]
+        int *const badcol = reinterpret_cast<int *>(after + a.heads * sizeof(Factors));
         int *const badb = badcol + WAVES * CW;                                           // [2]
 
         // Workgroup i runs on XCD i % 8: those of one segment and group, which
@@ -200,19 +218,22 @@ struct Chunks {
             return;
         const int group = unit % p.groups, number = unit / p.groups;
         const SeqTile tile = seq_tile(p.seq, a.seg, number);
-        const int64_t t0 = (int64_t)tile.index * a.seg;
-        if (t0 >= tile.len && tile.index != 0)
+        // (The same in all lanes, which the compiler has to be told: descriptors follow from it.)
+        const int index = __builtin_amdgcn_readfirstlane(tile.index);
+        const int whole = __builtin_amdgcn_readfirstlane((int)tile.len);
+        const int64_t t0 = (int64_t)index * a.seg;
+        if (t0 >= whole && index != 0)
             return;
-        const bool last = t0 + a.seg >= tile.len;
+        const bool last = t0 + a.seg >= whole;
         if (!FULL && last)
             return;
-        const int64_t first = tile.begin + t0;
-        const int len = (int)(last ? tile.len - t0 : a.seg);
+        const int64_t first = __builtin_amdgcn_readfirstlane((int)tile.begin) + t0;
+        const int len = last ? whole - (int)t0 : a.seg;
         const int chunks = (len + Q - 1) / Q;
 
-        const int tid = threadIdx.x, lane = tid & 63;
-        const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int g = lane >> 4, c = lane & 15;
+        int tid = threadIdx.x, lane = tid & 63;
+        int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+        int g = lane >> 4, c = lane & 15;
         const int per = p.H / p.groups, group_jobs = per * a.slices;
         const int job0 = wg * a.jobs, job1 = min(job0 + a.jobs, group_jobs);
         const int head0 = job0 / a.slices, heads = (job1 - 1) / a.slices - head0 + 1;    // of this workgroup, in the group
@@ -223,6 +244,18 @@ struct Chunks {
         const int col0 = job % a.slices * CW;
 
         // ---- Loads.
+        // VEC: through buffer descriptors of a chunk's rows that there are, whose
+        // end turns loads past it into zeros and drops stores (a host rule keeps
+        // a chunk within 2^31 bytes and rows from overlapping). A lane's offset
+        // of a column that is not there is past any end.
+        constexpr uint32_t NOWHERE = 0x80000000u;
+        auto view = [&](const T *base, int64_t stride, int rows, int width) __attribute__((always_inline)) {
+            const int end = rows > 0 ? (rows - 1) * (int)stride + width : 0;
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(base), 0, (uint32_t)(end * (int)sizeof(T)), 0x00020000);
+        };
+        auto offset_of = [&](int row, int col, int64_t stride, int width) __attribute__((always_inline)) {
+            return col < width ? (uint32_t)((row * (int)stride + col) * (int)sizeof(T)) : NOWHERE;
+        };
         const T *xp = static_cast<const T *>(p.x) + first * p.xst + h * p.xsh + col0;
         const T *gp = p.gate ? static_cast<const T *>(p.gate) + first * p.gst + h * p.gsh + col0 : xp;
         const int64_t gst = p.gate ? p.gst : p.xst;
@@ -236,41 +269,74 @@ struct Chunks {
         const float bias = p.bias ? p.bias[fh] : 0.f;
         const int cols = p.P - col0;                // columns there are, from the wave's first
 
+        // The gate (x in its place where there is none) of the columns V g + .. of tokens 16 it + c.
+        constexpr int V = 4 * CT;
+        struct Gate {
+            T v[V] __attribute__((aligned(V * sizeof(T) < 16 ? V * sizeof(T) : 16)));
+        };
         u32x4 bv[PB], cv[FULL ? PB : 1], xv[PX];
+        Gate gate[FULL ? 4 : 1];
         T dv;
+        uint32_t xo = offset_of(lane / (CW / E), lane % (CW / E) * E, p.xst, cols);
+        uint32_t bo = offset_of(tid / (NP / E), tid % (NP / E) * E, p.bst, p.N);
+        uint32_t co = offset_of(tid / (NP / E), tid % (NP / E) * E, p.cst, p.N);
+        uint32_t go = offset_of(c, V * g, gst, cols);
         // A piece of a row; the values that are not there are zeros.
         auto piece = [&](const T *row, int col, int width) __attribute__((always_inline)) {
-            if constexpr (VEC) {
-                return *reinterpret_cast<const u32x4 *>(row + (col < width ? col : 0));
-            } else {
-                T v[E] __attribute__((aligned(16))) = {};
+            T v[E] __attribute__((aligned(16))) = {};
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (col + e < width)
-                        v[e] = row[col + e];
-                return *reinterpret_cast<const u32x4 *>(v);
-            }
+            for (int e = 0; e < E; ++e)
+                if (col + e < width)
+                    v[e] = row[col + e];
+            return *reinterpret_cast<const u32x4 *>(v);
         };
-        auto load_x = [&](int ch) __attribute__((always_inline)) {
+        // What a chunk loads: pieces of X, B, C and the gate, in this order. One at a time: a load holds its wave some
+        // 150 clocks, which the products before it fill. Chunks past the last one load nothing.
+        constexpr int LOADS = PX + PB + (FULL ? PB + 4 : 0);
+        auto load = [&](int ch, int k) __attribute__((always_inline)) {
             const int rows = min(len - ch * Q, Q);
-            const T *base = xp + (int64_t)ch * Q * p.xst;
-#pragma unroll
-            for (int i = 0; i < PX; ++i) {
-                const int row = (i * 64 + lane) / (CW / E), col = (i * 64 + lane) % (CW / E) * E;
-                xv[i] = piece(base + min(row, rows - 1) * p.xst, col, cols);
-            }
-            dv = dp[(int64_t)(ch * Q + min(lane, rows - 1)) * p.dts];
-        };
-        auto load_bc = [&](int ch) __attribute__((always_inline)) {
-            const int rows = min(len - ch * Q, Q);
-            const T *bb = bp + (int64_t)ch * Q * p.bst, *cb = cp + (int64_t)ch * Q * p.cst;
-#pragma unroll
-            for (int i = 0; i < PB; ++i) {
+            const int64_t at0 = (int64_t)ch * Q;
+            if (k < PX) {
+                const T *base = xp + at0 * p.xst;
+                const int row = (k * 64 + lane) / (CW / E), col = (k * 64 + lane) % (CW / E) * E;
+                if constexpr (VEC)
+                    xv[k] = __builtin_amdgcn_raw_buffer_load_b128(view(base, p.xst, rows, cols),
+                                                                  xo + k * (64 * E / CW * (int)sizeof(T)) * (int)p.xst, 0, 0);
+                else if (rows > 0)
+                    xv[k] = piece(base + min(row, rows - 1) * p.xst, col, cols);
+            } else if (k < PX + (FULL ? 2 : 1) * PB) {
+                const int i = (k - PX) % PB;
+                const bool of_b = k < PX + PB;
+                const int64_t st = of_b ? p.bst : p.cst;
+                const T *base = (of_b ? bp : cp) + at0 * st;
                 const int row = (i * NT + tid) / (NP / E), col = (i * NT + tid) % (NP / E) * E;
-                bv[i] = piece(bb + min(row, rows - 1) * p.bst, col, p.N);
-                if constexpr (FULL)
-                    cv[i] = piece(cb + min(row, rows - 1) * p.cst, col, p.N);
+                u32x4 &to = of_b ? bv[i] : cv[FULL ? i : 0];
+                if constexpr (VEC)
+                    to = __builtin_amdgcn_raw_buffer_load_b128(
+                        view(base, st, rows, p.N), (of_b ? bo : co) + i * (NT * E / NP * (int)sizeof(T)) * (int)st, 0, 0);
+                else if (rows > 0)
+                    to = piece(base + min(row, rows - 1) * st, col, p.N);
+            } else {
+                const int it = k - PX - 2 * PB;
+                const T *base = gp + at0 * gst;
+                if constexpr (VEC) {
+                    const auto r = view(base, gst, rows, cols);
+                    const uint32_t o = go + it * (16 * (int)sizeof(T)) * (int)gst;
+                    if constexpr (sizeof(Gate) == 16)
+                        gate[it] = __builtin_bit_cast(Gate, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+                    else
+                        gate[it] = __builtin_bit_cast(Gate, __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, 0));
+                } else if (rows > 0) {
+                    const T *gr = base + min(16 * it + c, rows - 1) * gst;
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        gate[it].v[e] = gr[V * g + e < cols ? V * g + e : 0];
+                }
             }
+        };
+        auto load_step = [&](int ch) __attribute__((always_inline)) {
+            const int64_t t = min(ch * Q + lane, len - 1);
+            dv = dp[t * p.dts];
         };
         // A piece's parts into LDS: in bf16 the piece itself, in fp32 half a piece of each part.
         auto put = [&](uint8_t *at16, int part_bytes, const u32x4 &v, int half) __attribute__((always_inline)) {
@@ -289,8 +355,8 @@ struct Chunks {
                 *reinterpret_cast<u32x4 *>(at16) = v;
             }
         };
-        // First bad value of a piece's columns -> note(column).
-        auto look = [&](u32x4 &v, auto note) {
+        // Values that are not finite -> zeros, and note(their column).
+        auto look = [&](u32x4 &v, auto note) __attribute__((always_inline)) {
             T e[E] __attribute__((aligned(16)));
             *reinterpret_cast<u32x4 *>(e) = v;
 #pragma unroll
@@ -303,21 +369,24 @@ struct Chunks {
         };
         auto put_bc = [&](int ch) __attribute__((always_inline)) {
             const int rows = min(len - ch * Q, Q);
+            uint32_t odd = 0;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                if (!VEC && (i * NT + tid) / (NP / E) >= rows)
+                    bv[i] = u32x4{0, 0, 0, 0};
+                odd |= not_finite<F32>(bv[i]);
+            }
+            if (__any(odd != 0)) {
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+                    look(bv[i], [&](int) { atomicMin(badb + (ch & 1), (i * NT + tid) / (NP / E)); });
+            }
 #pragma unroll
             for (int i = 0; i < PB; ++i) {
                 const int row = (i * NT + tid) / (NP / E), col = (i * NT + tid) % (NP / E) * E;
-                u32x4 v = bv[i];
-                if (row >= rows || col >= p.N)
-                    v = u32x4{0, 0, 0, 0};
-                if (not_finite<F32>(v))
-                    look(v, [&](int) { atomicMin(badb + (ch & 1), row); });
-                put(bs + b_place(row, col / 8), BBYTES, v, col / 4 & 1);
-                if constexpr (FULL) {
-                    u32x4 u = cv[i];
-                    if (col >= p.N)
-                        u = u32x4{0, 0, 0, 0};
-                    put(cs + c_place(row, col / 8), BBYTES, u, col / 4 & 1);
-                }
+                put(bs + b_place(row, col / 8), BBYTES, bv[i], col / 4 & 1);
+                if constexpr (FULL)
+                    put(cs + c_place(row, col / 8), CBYTES, cv[i], col / 4 & 1);
             }
         };
         // X of the wave's columns through its own part of LDS, as 8 tokens of a column a lane.
@@ -325,15 +394,24 @@ struct Chunks {
         auto put_x = [&](int ch) __attribute__((always_inline)) {
             const int rows = min(len - ch * Q, Q);
             uint8_t *const own = xm + w * XP * XBYTES;
+            uint32_t odd = 0;
+#pragma unroll
+            for (int i = 0; i < PX; ++i) {
+                if (!VEC && (i * 64 + lane) / (CW / E) >= rows)
+                    xv[i] = u32x4{0, 0, 0, 0};
+                odd |= not_finite<F32>(xv[i]);
+            }
+            if (__any(odd != 0)) {
+#pragma unroll
+                for (int i = 0; i < PX; ++i) {
+                    const int row = (i * 64 + lane) / (CW / E), col = (i * 64 + lane) % (CW / E) * E;
+                    look(xv[i], [&](int e) { atomicMin(badcol + w * CW + col + e, row); });
+                }
+            }
 #pragma unroll
             for (int i = 0; i < PX; ++i) {
                 const int row = (i * 64 + lane) / (CW / E), col = (i * 64 + lane) % (CW / E) * E;
-                u32x4 v = xv[i];
-                if (row >= rows || col >= cols)
-                    v = u32x4{0, 0, 0, 0};
-                if (not_finite<F32>(v))
-                    look(v, [&](int e) { atomicMin(badcol + w * CW + col + e, row); });
-                put(own + row * CW * 2 + col / 8 * 16, XBYTES, v, col / 4 & 1);
+                put(own + row * CW * 2 + col / 8 * 16, XBYTES, xv[i], col / 4 & 1);
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
@@ -351,7 +429,8 @@ struct Chunks {
         auto make_factors = [&](int ch) __attribute__((always_inline)) {
             if (w >= heads)
                 return;
-            Factors &f = factors[(ch & 1) * a.heads + w];
+            Factors &f = factors[w];
+            auto &of = f.of[ch & 1];
             float d = step_size(load_as_f32(&dv) + bias, p.softplus);
             // Exponents past +-10000 are 0 and infinity either way.
             double e = fmin(fmax((double)d * rate, -1e4), 1e4);
@@ -362,27 +441,28 @@ struct Chunks {
                 d = 0.f;
                 e = 0.0;
             }
-#pragma unroll
-            for (int i = 1; i < 64; i <<= 1) {
-                const double o = __shfl_up(e, i);
-                if (lane >= i)
-                    e += o;
-            }
-            const double mid = __shfl(e, 31), end = __shfl(e, 63);
+            // Sums up to each lane: within 16 lanes, then of the rows of 16 before.
+            e += moved<0x111, 0xf>(e);
+            e += moved<0x112, 0xf>(e);
+            e += moved<0x114, 0xf>(e);
+            e += moved<0x118, 0xf>(e);
+            e += moved<0x142, 0xa>(e);
+            e += moved<0x143, 0xc>(e);
+            const double mid = of_lane(e, 31), end = of_lane(e, 63);
             exponent += end;
             const bool wide = __any(!(fabs(e - mid) <= 60.0));
-            f.tail[lane] = power2(end - e) * d;
+            of.tail[lane] = power2(end - e) * d;
             if constexpr (FULL) {
                 f.L[lane] = e;
                 f.step[lane] = d;
                 f.row[lane] = power2(e - mid);
                 f.col[lane] = power2(mid - e) * d;
-                f.up[lane] = power2(e);
+                of.up[lane] = power2(e);
             }
             if (lane == 0) {
-                f.total = power2(end);
-                f.wide = wide;
-                f.bad = bads ? __builtin_ctzll(bads) : NEVER;
+                of.total = power2(end);
+                of.wide = wide;
+                of.bad = bads ? __builtin_ctzll(bads) : NEVER;
             }
         };
 
@@ -394,84 +474,104 @@ struct Chunks {
         // ---- The state before the segment. Column p of a tile (of lane c) is
         // row p of S; a lane has 4 rows n of each of 2 KN tiles, which
         // interleave, so that a pair of them is 8 adjacent n.
-        const int prow[2] = {col0 + (CT == 2 ? 8 * (c >> 2) + (c & 3) : c), col0 + 8 * (c >> 2) + 4 + (c & 3)};
-        const int64_t head_state = (int64_t)p.P * p.N;
-        auto state_at = [&](const float *s, int64_t index, int ct, int nt) {
-            return s + (index * p.H + h) * head_state + (int64_t)prow[ct] * p.N + 32 * (nt >> 1) + 8 * g + 4 * (nt & 1);
-        };
-        auto read4 = [&](const float *s, int ct, int nt) __attribute__((always_inline)) {
-            const int n = 32 * (nt >> 1) + 8 * g + 4 * (nt & 1);
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            if (prow[ct] < p.P && n < p.N) {
-                if constexpr (VEC) {
-                    v = *reinterpret_cast<const f32x4 *>(s);
-                } else {
+        f32x4 S[2 * KN][CT];
+        // each(S, pointer) for what there is of the state at s, by pieces of four. (The lane's number is made anew, or
+        // the addresses of the first visit would be kept through the chunks for the last.)
+        auto visit = [&](const float *s, int64_t index, auto each) __attribute__((always_inline)) {
+            int l = lane;
+            asm volatile("" : "+v"(l));
+            const int gg = l >> 4, cc = l & 15;
+            const float *base = s + (index * p.H + h) * p.P * p.N;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < p.N)
-                            v[e] = s[e];
+            for (int ct = 0; ct < CT; ++ct) {
+                const int row = col0 + (CT == 2 ? 8 * (cc >> 2) + 4 * ct + (cc & 3) : cc);
+                if (row < p.P) {
+#pragma unroll
+                    for (int nt = 0; nt < 2 * KN; ++nt) {
+                        const int n = 32 * (nt >> 1) + 8 * gg + 4 * (nt & 1);
+                        if (n < p.N)
+                            each(S[nt][ct], base + (int64_t)row * p.N + n, p.N - n);
+                    }
                 }
+            }
+        };
+        auto read4 = [&](const float *s, int left) __attribute__((always_inline)) {
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (VEC) {
+                v = *reinterpret_cast<const f32x4 *>(s);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left)
+                        v[e] = s[e];
             }
             return v;
         };
-        f32x4 S[2 * KN][CT];
         auto write_state = [&](float *s, int64_t index) __attribute__((always_inline)) {
+            if (!mine)
+                return;
+            visit(s, index, [&](const f32x4 &v, const float *at_, int left) __attribute__((always_inline)) {
+                float *to = const_cast<float *>(at_);
+                if constexpr (VEC) {
+                    *reinterpret_cast<f32x4 *>(to) = v;
+                } else {
 #pragma unroll
-            for (int nt = 0; nt < 2 * KN; ++nt)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    const int n = 32 * (nt >> 1) + 8 * g + 4 * (nt & 1);
-                    float *to = const_cast<float *>(state_at(s, index, ct, nt));
-                    if (mine && prow[ct] < p.P && n < p.N) {
-                        if constexpr (VEC) {
-                            *reinterpret_cast<f32x4 *>(to) = S[nt][ct];
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (n + e < p.N)
-                                    to[e] = S[nt][ct][e];
-                        }
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left)
+                            to[e] = v[e];
                 }
+            });
+        };
+        // The workspace's states lie as the lanes hold them: whole lines at a time, nothing to compare.
+        auto kept = [&](int k, int nt, int ct) __attribute__((always_inline)) {
+            const int64_t at0 = (((int64_t)k * p.H + h) * a.slices + job % a.slices) * (2 * KN * CT) + nt * CT + ct;
+            return reinterpret_cast<f32x4 *>(a.states) + at0 * 64 + lane;
+        };
+        auto keep = [&](int k) __attribute__((always_inline)) {
+            if (mine)
+#pragma unroll
+                for (int nt = 0; nt < 2 * KN; ++nt)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        *kept(k, nt, ct) = S[nt][ct];
         };
         const int slot = p.state_in || p.state_out ? seq_slot(p.seq, tile.n) : -1;
-        const int64_t first_number = number - tile.index;
-        const int64_t last_number = first_number + (tile.len > 0 ? (tile.len - 1) / a.seg : 0);
+        const int first_number = number - index;
+        const int last_number = first_number + (whole > 0 ? (whole - 1) / a.seg : 0);
         bool held = false;          // whether S may hold anything
 #pragma unroll
         for (int nt = 0; nt < 2 * KN; ++nt)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
                 S[nt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (tile.index == 0 && (!FULL || last)) {
+        if (index == 0 && (!FULL || last)) {
             if (p.state_in && slot >= 0) {
                 held = true;
-#pragma unroll
-                for (int nt = 0; nt < 2 * KN; ++nt)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-                        S[nt][ct] = read4(state_at(p.state_in, slot, ct, nt), ct, nt);
+                visit(p.state_in, slot, [&](f32x4 &v, const float *s, int left) __attribute__((always_inline)) {
+                    v = read4(s, left);
+                });
             }
             // A sequence of several segments: what its last one may overwrite
             // before its first one has read it is kept in the place of the
             // state that the last one does not leave.
             if (!FULL)
-                write_state(a.states, last_number);
+                keep(last_number);
         } else if (FULL) {
             held = true;
-            const int64_t from = tile.index == 0 ? last_number : first_number;
+            const int from = index == 0 ? last_number : first_number;
 #pragma unroll
             for (int nt = 0; nt < 2 * KN; ++nt)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    S[nt][ct] = read4(state_at(a.states, from, ct, nt), ct, nt);
-            for (int64_t k = first_number + 1; k < number; ++k) {
-                const float by = a.decays[k * p.H + h];
+                    S[nt][ct] = *kept(from, nt, ct);
+#pragma unroll 2
+            for (int k = first_number + 1; k < number; ++k) {
+                const float by = a.decays[(int64_t)k * p.H + h];
 #pragma unroll
                 for (int nt = 0; nt < 2 * KN; ++nt)
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) {
-                        const f32x4 v = read4(state_at(a.states, k, ct, nt), ct, nt);
+                        const f32x4 v = *kept(k, nt, ct);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             S[nt][ct][e] = fmaf(by, S[nt][ct][e], v[e]);
@@ -480,51 +580,50 @@ struct Chunks {
         }
 
         if (chunks > 0) {
-            load_x(0);
-            load_bc(0);
+            load_step(0);
+#pragma unroll
+            for (int k = 0; k < LOADS; ++k)
+                load(0, k);
             make_factors(0);
+            load_step(1);
         }
+        // The head whose M this wave has a share of (there are 1, 2 or 4 a workgroup, or fewer at a group's end), and its skip.
+        const int mh = w & (a.heads - 1);
+        float skip = 0.f;
+        if (FULL && p.skip && mh < heads)
+            skip = p.skip[group * per + head0 + mh];
         lds_barrier();              // the notes are set
         for (int ch = 0; ch < chunks; ++ch) {
             const int rows = min(len - ch * Q, Q);
-            if constexpr (!VEC) {
-                if (ch > 0)
-                    load_bc(ch);
-            }
+            // The lane's place is made anew: addresses and comparisons that follow from it are cheaper made again than
+            // kept from chunk to chunk (in spilled registers: 87 of them).
+            asm volatile("" : "+v"(tid), "+s"(w));
+            lane = tid & 63;
+            g = lane >> 4;
+            c = lane & 15;
+            asm("" : "+v"(xo), "+v"(bo), "+v"(co), "+v"(go));
             put_bc(ch);
             put_x(ch);
+            const bool wide = FULL && __builtin_amdgcn_readfirstlane(factors[mh].of[ch & 1].wide) != 0;
             lds_barrier();
-            const Factors *const fs = factors + (ch & 1) * a.heads;
-            if (ch + 1 < chunks) {
-                load_x(ch + 1);
-                if constexpr (VEC)
-                    load_bc(ch + 1);
-            }
             if (tid == 0)
                 badb[(ch + 1) & 1] = NEVER;     // last read before the barrier that ended the chunk before
-            // The gate (x in its place where there is none) of the columns V g + .. of tokens 16 it + c.
-            constexpr int V = 4 * CT;
-            struct Gate {
-                T v[V] __attribute__((aligned(V * sizeof(T) < 16 ? V * sizeof(T) : 16)));
-            };
-            Gate gate[FULL ? 4 : 1];
             f32x4 acc[4][CT];
             if constexpr (FULL) {
-#pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const T *gr = gp + ((int64_t)ch * Q + min(16 * it + c, rows - 1)) * gst;
-                    if constexpr (VEC) {
-                        __builtin_memcpy(&gate[it], __builtin_assume_aligned(gr + (V * g < cols ? V * g : 0), alignof(Gate)),
-                                         sizeof(Gate));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < V; ++e)
-                            gate[it].v[e] = gr[V * g + e < cols ? V * g + e : 0];
-                    }
-                }
                 // M^T's blocks: tokens i of tile `it` as columns, 32 tokens j of step s as rows, two interleaving
                 // tiles, so that a lane has 8 adjacent j of one i: an operand of the product with X.
-                auto block = [&](int it, int s, int f) __attribute__((always_inline)) {
+                // Blocks (1,0) (2,0) (3,0) (0,0) (3,1) (2,1) go round the waves of a head.
+                const Factors &fm = factors[mh];
+                for (int f = mh < heads ? w / a.heads : MFRAGS; f < MFRAGS; f += WAVES / a.heads) {
+                    const int it = f < 3 ? f + 1 : f == 3 ? 0 : 7 - f, s = f >= 4;
+                    const int ti = 16 * it + c, tj0 = 32 * s + 8 * g;
+                    const uint8_t *const c0 = cs + c_place(ti, g);
+                    const uint8_t *const b0 = bs + b_place(32 * s + 8 * (c >> 2) + (c & 3), g);
+                    const float r = fm.row[ti];
+                    float col[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        col[e] = fm.col[tj0 + e];
                     f32x4 raw[2];
                     raw[0] = raw[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -532,51 +631,39 @@ struct Chunks {
                         bf16x8 cf[XP], bf[XP];
 #pragma unroll
                         for (int i = 0; i < XP; ++i)
-                            cf[i] = *reinterpret_cast<const bf16x8 *>(cs + i * BBYTES + c_place(16 * it + c, 4 * ks + g));
+                            cf[i] = *reinterpret_cast<const bf16x8 *>(c0 + i * CBYTES + c_place(0, 4 * ks));
 #pragma unroll
                         for (int tj = 0; tj < 2; ++tj) {
 #pragma unroll
                             for (int i = 0; i < XP; ++i)
-                                bf[i] = *reinterpret_cast<const bf16x8 *>(
-                                    bs + i * BBYTES + b_place(32 * s + 8 * (c >> 2) + 4 * tj + (c & 3), 4 * ks + g));
+                                bf[i] = *reinterpret_cast<const bf16x8 *>(b0 + i * BBYTES + b_place(4 * tj, 4 * ks));
                             raw[tj] = product(bf, cf, raw[tj]);
                         }
                     }
-                    const int ti = 16 * it + c, tj0 = 32 * s + 8 * g;
-                    for (int k = 0; k < heads; ++k) {
-                        const Factors &fk = fs[k];
-                        float m[8];
-                        if (!fk.wide) {
-                            const float r = fk.row[ti];
+                    float m[8];
+                    if (!wide) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                m[e] = raw[e >> 2][e & 3] * fk.col[tj0 + e] * r;
-                        } else {
-                            const double Li = fk.L[ti];
+                        for (int e = 0; e < 8; ++e)
+                            m[e] = raw[e >> 2][e & 3] * col[e] * r;
+                    } else {
+                        const double Li = fm.L[ti];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                m[e] = raw[e >> 2][e & 3] * fk.step[tj0 + e] * power2(Li - fk.L[tj0 + e]);
-                        }
-                        if (it >> 1 == s) {
-                            const float own = p.skip ? p.skip[group * per + head0 + k] : 0.f;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                m[e] = tj0 + e <= ti ? m[e] : 0.f;
-                                m[e] = tj0 + e == ti ? m[e] + own : m[e];
-                            }
-                        }
-                        bf16x8 part[3];
-                        split8(m, part);
-#pragma unroll
-                        for (int i = 0; i < 3; ++i)
-                            reinterpret_cast<bf16x8 *>(xm + ((k * MFRAGS + f) * 3 + i) * FRAG)[lane] = part[i];
+                        for (int e = 0; e < 8; ++e)
+                            m[e] = raw[e >> 2][e & 3] * fm.step[tj0 + e] * power2(Li - fm.L[tj0 + e]);
                     }
-                };
-                // Blocks (1,0) (2,0) (3,0)+(0,0) (3,1)+(2,1) of waves 0 to 3.
-                const int it1 = w < 3 ? w + 1 : 3, s1 = w == 3, it2 = w == 2 ? 0 : 2, s2 = w == 3;
-                block(it1, s1, w < 2 ? w : 2 * w - 2);
-                if (w >= 2)
-                    block(it2, s2, 2 * w - 1);
+                    if (it >> 1 == s) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            m[e] = tj0 + e <= ti ? m[e] : 0.f;
+                            m[e] = tj0 + e == ti ? m[e] + skip : m[e];
+                        }
+                    }
+                    bf16x8 part[3];
+                    split8(m, part);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        reinterpret_cast<bf16x8 *>(xm + ((mh * MFRAGS + f) * 3 + i) * FRAG)[lane] = part[i];
+                }
 
                 // Y^T: S C^T.
 #pragma unroll
@@ -585,6 +672,7 @@ struct Chunks {
                     for (int ct = 0; ct < CT; ++ct)
                         acc[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
                 if (held) {
+                    const uint8_t *const c0 = cs + c_place(c, g);
 #pragma unroll
                     for (int ks = 0; ks < KN; ++ks) {
                         bf16x8 sp[CT][3];
@@ -601,7 +689,7 @@ struct Chunks {
                             bf16x8 cf[XP];
 #pragma unroll
                             for (int i = 0; i < XP; ++i)
-                                cf[i] = *reinterpret_cast<const bf16x8 *>(cs + i * BBYTES + c_place(16 * it + c, 4 * ks + g));
+                                cf[i] = *reinterpret_cast<const bf16x8 *>(c0 + i * CBYTES + c_place(16 * it, 4 * ks));
 #pragma unroll
                             for (int ct = 0; ct < CT; ++ct)
                                 acc[it][ct] = product(sp[ct], cf, acc[it][ct]);
@@ -610,11 +698,13 @@ struct Chunks {
                 }
                 lds_barrier();
             }
-            const Factors &f = fs[hi];
+            const auto &f = factors[hi].of[ch & 1];
             const int bad_all = min(f.bad, badb[ch & 1]);
             const bool bad = bad_all != NEVER || __any(badcol[w * CW + (lane & (CW - 1))] != NEVER);
             if constexpr (FULL) {
-                const uint8_t *const ms = xm + hi * MFRAGS * 3 * FRAG;
+                // Y^T: M X on top, then the gate, for all tiles at once: a branch inside would keep each tile's latencies
+                // apart.
+                const uint8_t *const ms = xm + hi * MFRAGS * 3 * FRAG + lane * 16;
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
                     const float up = f.up[16 * it + c];
@@ -628,52 +718,59 @@ struct Chunks {
                         bf16x8 mf[3];
 #pragma unroll
                         for (int i = 0; i < 3; ++i)
-                            mf[i] = reinterpret_cast<const bf16x8 *>(ms + (fr * 3 + i) * FRAG)[lane];
+                            mf[i] = *reinterpret_cast<const bf16x8 *>(ms + (fr * 3 + i) * FRAG);
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct)
                             acc[it][ct] = product(xf[s][ct], mf, acc[it][ct]);
                     }
-                    const int t = 16 * it + c;
-                    const int64_t tok = (int64_t)ch * Q + min(t, rows - 1);
-                    const int at0 = V * g;
-                    float y[V];
+                }
+                if (p.gate) {
+#pragma unroll
+                    for (int it = 0; it < 4; ++it)
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            acc[it][e >> 2][e & 3] *= silu(load_as_f32(&gate[it].v[e]));
+                }
+                if (bad) {
+#pragma unroll
+                    for (int it = 0; it < 4; ++it)
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            if (16 * it + c >= min(bad_all, badcol[w * CW + V * g + e]))
+                                acc[it][e >> 2][e & 3] = NAN;
+                }
+                T *yb = yp + (int64_t)ch * Q * p.yst;
+                const auto yr = view(yb, p.yst, mine ? rows : 1, mine ? cols : 0);
+                const uint32_t yo = offset_of(c, V * g, p.yst, cols);
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    // Columns V g + .. of token 16 it + c.
+                    Gate o;
 #pragma unroll
                     for (int e = 0; e < V; ++e)
-                        y[e] = acc[it][e >> 2][e & 3];
-                    if (p.gate) {
+                        store_rne(&o.v[e], acc[it][e >> 2][e & 3]);
+                    const int t = 16 * it + c;
+                    if constexpr (VEC) {
+                        const uint32_t at0 = yo + it * (16 * (int)sizeof(T)) * (int)p.yst;
+                        if constexpr (sizeof(Gate) == 16)
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o), yr, at0, 0, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), yr, at0, 0, 0);
+                    } else if (mine && t < rows) {
 #pragma unroll
                         for (int e = 0; e < V; ++e)
-                            y[e] *= silu(load_as_f32(&gate[it].v[e]));
-                    }
-                    if (bad) {
-#pragma unroll
-                        for (int e = 0; e < V; ++e)
-                            if (t >= min(bad_all, badcol[w * CW + at0 + e]))
-                                y[e] = NAN;
-                    }
-                    if (mine && t < rows) {
-                        T *yr = yp + tok * p.yst + at0;
-                        Gate o;
-#pragma unroll
-                        for (int e = 0; e < V; ++e)
-                            store_rne(&o.v[e], y[e]);
-                        if constexpr (VEC) {
-                            if (at0 < cols)
-                                __builtin_memcpy(__builtin_assume_aligned(yr, alignof(Gate)), &o, sizeof(o));
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < V; ++e)
-                                if (at0 + e < cols)
-                                    yr[e] = o.v[e];
-                        }
+                            if (V * g + e < cols)
+                                yb[t * p.yst + V * g + e] = o.v[e];
                     }
                 }
             }
             if (ch + 1 < chunks)
                 make_factors(ch + 1);
+            load_step(ch + 2);
 
             // S' = total S + B^T (tail x).
             const float total = f.total;
+            const uint8_t *const b0 = bs + b_place(8 * g + (c >> 2), c & 3);
 #pragma unroll
             for (int nt = 0; nt < 2 * KN; ++nt)
 #pragma unroll
@@ -696,12 +793,16 @@ struct Chunks {
                 }
 #pragma unroll
                 for (int nt = 0; nt < 2 * KN; ++nt) {
+                    // The next chunk's loads, spread over these products.
+                    const int step = s * 2 * KN + nt;
+#pragma unroll
+                    for (int k = step * LOADS / (4 * KN); k < (step + 1) * LOADS / (4 * KN); ++k)
+                        load(ch + 1, k);
                     bf16x8 bt[XP];
 #pragma unroll
                     for (int i = 0; i < XP; ++i) {
-                        const int row = 32 * s + 8 * g + (c >> 2), pc = 4 * (nt >> 1) + (c & 3);
-                        const uint8_t *b0 = bs + i * BBYTES + 8 * (nt & 1);
-                        bt[i] = join(transposed(b0 + b_place(row, pc)), transposed(b0 + b_place(row + 4, pc)));
+                        const uint8_t *const at0 = b0 + i * BBYTES + b_place(32 * s, 4 * (nt >> 1)) + 8 * (nt & 1);
+                        bt[i] = join(transposed(at0), transposed(at0 + b_place(4, 0)));
                     }
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
@@ -712,7 +813,7 @@ struct Chunks {
             if (bad) {
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    if (bad_all != NEVER || badcol[w * CW + prow[ct] - col0] != NEVER)
+                    if (bad_all != NEVER || badcol[w * CW + (CT == 2 ? 8 * (c >> 2) + 4 * ct + (c & 3) : c)] != NEVER)
 #pragma unroll
                         for (int nt = 0; nt < 2 * KN; ++nt)
                             S[nt][ct] = f32x4{NAN, NAN, NAN, NAN};
@@ -724,41 +825,52 @@ struct Chunks {
         if (FULL && last && p.state_out && slot >= 0)
             write_state(p.state_out, slot);
         if (!FULL) {
-            write_state(a.states, number);
+            keep(number);
             if (w < heads && lane == 0)
                 a.decays[(int64_t)number * p.H + fh] = power2(exponent);
         }
     }
 };
 
-template <class T, int KN, int CT, bool FULL, bool VEC>
-__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(std::is_same<T, float>::value || KN > 4 ? 1 : 2))) void
-heads_chunk_kernel(HeadsArgs a)
+// bf16: eight waves of 16 columns; four a SIMD, from two workgroups, where the
+// registers allow. fp32, whose operands take three times the LDS: four waves.
+template <class T>
+constexpr int WAVES = std::is_same<T, float>::value ? 4 : 8;
+
+template <class T, int KN, bool FULL, bool VEC>
+__global__ __launch_bounds__(64 * WAVES<T>)
+    __attribute__((amdgpu_waves_per_eu(std::is_same<T, float>::value ? 1 : KN > 4 ? 2 : 4))) void heads_chunk_kernel(HeadsArgs a)
 {
-    Chunks<T, KN, CT, FULL, VEC>::run(a);
+    Chunks<T, KN, 1, WAVES<T>, FULL, VEC>::run(a);
 }
 
 constexpr int LDS_MOST = 160 * 1024;
 
 // How a call is laid out: everything that follows from its sizes alone.
 struct Plan {
-    int kn, ct, slices, jobs, wgs, heads, seg;
+    int kn, slices, jobs, wgs, heads, seg;
     int64_t numbers;        // segments, numbered as in sequences.h
     bool parts;             // segments are shorter than a sequence may be
 };
 
+// Heads that `jobs` slices in a row may belong to, as a power of two.
 int most_heads(int jobs, int slices)
 {
-    return slices % jobs == 0 ? 1 : jobs % slices == 0 ? jobs / slices : (jobs - 2) / slices + 2;
+    const int most = slices % jobs == 0 ? 1 : jobs % slices == 0 ? jobs / slices : (jobs - 2) / slices + 2;
+    int n = 1;
+    while (n < most)
+        n *= 2;
+    return n;
 }
 
 int lds_bytes(bool f32, int kn, int heads)
 {
     if (f32)
-        return kn == 2 ? Chunks<float, 2, 1, true, true>::lds(heads) : Chunks<float, 4, 1, true, true>::lds(heads);
-    return kn == 2   ? Chunks<uint16_t, 2, 2, true, true>::lds(heads)
-           : kn == 4 ? Chunks<uint16_t, 4, 2, true, true>::lds(heads)
-                     : Chunks<uint16_t, 8, 1, true, true>::lds(heads);
+        return kn == 2 ? Chunks<float, 2, 1, WAVES<float>, true, true>::lds(heads)
+                       : Chunks<float, 4, 1, WAVES<float>, true, true>::lds(heads);
+    return kn == 2   ? Chunks<uint16_t, 2, 1, WAVES<uint16_t>, true, true>::lds(heads)
+           : kn == 4 ? Chunks<uint16_t, 4, 1, WAVES<uint16_t>, true, true>::lds(heads)
+                     : Chunks<uint16_t, 8, 1, WAVES<uint16_t>, true, true>::lds(heads);
 }
 
 bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype dtype, Plan *l)
@@ -767,9 +879,8 @@ bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype d
     if (N > (f32 ? 128 : 256))
         return false;
     l->kn = N <= 64 ? 2 : N <= 128 ? 4 : 8;
-    l->ct = f32 || l->kn == 8 ? 1 : 2;
-    l->slices = (P + 16 * l->ct - 1) / (16 * l->ct);
-    l->jobs = WAVES;
+    l->slices = (P + 15) / 16;
+    l->jobs = f32 ? WAVES<float> : WAVES<uint16_t>;
     l->heads = most_heads(l->jobs, l->slices);
     while (lds_bytes(f32, l->kn, l->heads) > LDS_MOST) {
         l->jobs /= 2;
@@ -808,41 +919,34 @@ Sequences sequences_of(int64_t tokens, int num_seqs, bool equal)
     return s;
 }
 
-int64_t space(const Plan &l, int H, int P, int N)
+// Floats of the workspace's states, as the lanes hold them.
+int64_t state_floats(const Plan &l, int H) { return l.numbers * H * l.slices * 16 * (32 * l.kn); }
+
+int64_t space(const Plan &l, int H)
 {
-    if (!l.parts)
-        return 0;
-    const int64_t states = (l.numbers * H * P * N * 4 + 255) / 256 * 256;
-    return states + (l.numbers * H * 4 + 255) / 256 * 256;
+    return l.parts ? (state_floats(l, H) + (l.numbers * H + 63) / 64 * 64) * 4 : 0;
 }
 
-template <class T, int KN, int CT, bool FULL>
-hipError_t launch_pass(const HeadsArgs &a, unsigned grid, bool vec, hipStream_t s)
+template <class T, int KN, bool FULL, bool VEC>
+hipError_t launch_pass(const HeadsArgs &a, hipStream_t s)
 {
-    const int lds = Chunks<T, KN, CT, FULL, true>::lds(a.heads);
-    hipError_t e;
-    if (vec) {
-        e = allow_lds<heads_chunk_kernel<T, KN, CT, FULL, true>>(LDS_MOST);
-        if (e == hipSuccess)
-            hipLaunchKernelGGL((heads_chunk_kernel<T, KN, CT, FULL, true>), dim3(grid), dim3(NT), lds, s, a);
-    } else {
-        e = allow_lds<heads_chunk_kernel<T, KN, CT, FULL, false>>(LDS_MOST);
-        if (e == hipSuccess)
-            hipLaunchKernelGGL((heads_chunk_kernel<T, KN, CT, FULL, false>), dim3(grid), dim3(NT), lds, s, a);
-    }
-    return e == hipSuccess ? hipGetLastError() : e;
+    const hipError_t e = allow_lds<heads_chunk_kernel<T, KN, FULL, VEC>>(LDS_MOST);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL((heads_chunk_kernel<T, KN, FULL, VEC>), dim3((unsigned)((a.units + 7) / 8 * 8 * a.wgs)),
+                       dim3(64 * WAVES<T>), (Chunks<T, KN, 1, WAVES<T>, FULL, VEC>::lds(a.heads)), s, a);
+    return hipGetLastError();
 }
 
-template <class T, int KN, int CT>
+template <class T, int KN>
 hipError_t launch(const HeadsArgs &a, bool parts, bool vec, hipStream_t s)
 {
-    const unsigned grid = (unsigned)((a.units + 7) / 8 * 8 * a.wgs);
     if (parts) {
-        const hipError_t e = launch_pass<T, KN, CT, false>(a, grid, vec, s);
+        const hipError_t e = vec ? launch_pass<T, KN, false, true>(a, s) : launch_pass<T, KN, false, false>(a, s);
         if (e != hipSuccess)
             return e;
     }
-    return launch_pass<T, KN, CT, true>(a, grid, vec, s);
+    return vec ? launch_pass<T, KN, true, true>(a, s) : launch_pass<T, KN, true, false>(a, s);
 }
 
 }  // namespace
@@ -859,7 +963,7 @@ int64_t heads_chunked_workspace(int64_t tokens, int num_seqs, int H, int P, int 
     Plan packed, equal;         // the larger of the two ways in which the sequences may lie
     make_plan(sequences_of(tokens, num_seqs, false), H, P, groups, N, dtype, &packed);
     make_plan(sequences_of(tokens, num_seqs, true), H, P, groups, N, dtype, &equal);
-    const int64_t x = space(packed, H, P, N), y = space(equal, H, P, N);
+    const int64_t x = space(packed, H), y = space(equal, H);
     return x > y ? x : y;
 }
 
@@ -870,7 +974,7 @@ hipError_t launch_heads_chunked(const HeadScanProblem &p, hipStream_t s)
     HeadsArgs a;
     a.p = p;
     a.states = static_cast<float *>(p.workspace);
-    a.decays = a.states + (l.numbers * p.H * p.P * p.N + 63) / 64 * 64;
+    a.decays = a.states + state_floats(l, p.H);
     a.seg = l.seg;
     a.units = (int)(l.numbers * p.groups);
     a.slices = l.slices;
@@ -882,12 +986,15 @@ hipError_t launch_heads_chunked(const HeadScanProblem &p, hipStream_t s)
                               (p.gate ? (uintptr_t)((p.gst | p.gsh) * e) : 0);
     const uintptr_t at = (uintptr_t)p.x | (uintptr_t)p.y | (uintptr_t)p.b | (uintptr_t)p.c | (uintptr_t)p.gate |
                          (uintptr_t)p.state_in | (uintptr_t)p.state_out;
-    const bool vec = (strides | at) % 16 == 0 && p.P % (16 / e) == 0 && p.N % (16 / e) == 0;
+    const int64_t far = int64_t(1) << 22;       // 64 rows stay below 2^30 bytes
+    auto rows_fit = [&](int64_t stride, int width) { return stride >= width && stride < far; };
+    const bool vec = (strides | at) % 16 == 0 && p.P % (16 / e) == 0 && p.N % (16 / e) == 0 && rows_fit(p.xst, p.P) &&
+                     rows_fit(p.yst, p.P) && rows_fit(p.bst, p.N) && rows_fit(p.cst, p.N) && (!p.gate || rows_fit(p.gst, p.P));
     if (p.dtype == CONV_F32)
-        return l.kn == 2 ? launch<float, 2, 1>(a, l.parts, vec, s) : launch<float, 4, 1>(a, l.parts, vec, s);
-    return l.kn == 2   ? launch<uint16_t, 2, 2>(a, l.parts, vec, s)
-           : l.kn == 4 ? launch<uint16_t, 4, 2>(a, l.parts, vec, s)
-                       : launch<uint16_t, 8, 1>(a, l.parts, vec, s);
+        return l.kn == 2 ? launch<float, 2>(a, l.parts, vec, s) : launch<float, 4>(a, l.parts, vec, s);
+    return l.kn == 2   ? launch<uint16_t, 2>(a, l.parts, vec, s)
+           : l.kn == 4 ? launch<uint16_t, 4>(a, l.parts, vec, s)
+                       : launch<uint16_t, 8>(a, l.parts, vec, s);
 }
 
 }  // namespace convfwd
