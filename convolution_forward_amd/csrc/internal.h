@@ -201,6 +201,9 @@ struct ScanProblem {
 
 bool scan_direct_supports(int num_seqs, int channels, int N);
 hipError_t launch_scan_direct(const ScanProblem &p, hipStream_t s);
+bool scan_tiled_supports(int64_t tokens, int num_seqs, int channels, int groups, int N);
+int64_t scan_tiled_workspace(int64_t tokens, int num_seqs, int channels, int groups, int N);
+hipError_t launch_scan_tiled(const ScanProblem &p, hipStream_t s);
 
 // A validated selective scan with one decay a head.
 struct HeadScanProblem {

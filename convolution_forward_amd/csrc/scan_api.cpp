@@ -41,8 +41,9 @@ conv_status check_scan_sizes(int64_t tokens, int num_seqs, int channels, int gro
         return CONV_ERR_DTYPE;
     if (tokens > MAX_ROWS || num_seqs > MAX_ROWS || channels > (1 << 23) || N > 256 || !known_variant(variant))
         return CONV_ERR_UNSUPPORTED;
-    *tiled = variant == CONV_VARIANT_TILED;
-    return (*tiled ? false : scan_direct_supports(num_seqs, channels, N)) ? CONV_OK : CONV_ERR_UNSUPPORTED;
+    const bool can = scan_tiled_supports(tokens, num_seqs, channels, groups, N);
+    *tiled = variant == CONV_VARIANT_TILED || (variant == CONV_VARIANT_AUTO && can && tokens > 24 * (int64_t)num_seqs);
+    return (*tiled ? can : scan_direct_supports(num_seqs, channels, N)) ? CONV_OK : CONV_ERR_UNSUPPORTED;
 }
 
 conv_status check_heads_sizes(int64_t tokens, int num_seqs, int H, int P, int groups, int N, conv_dtype dtype, int variant,
@@ -139,7 +140,7 @@ int64_t conv_selective_scan_workspace(int64_t tokens, int num_seqs, int channels
     bool tiled;
     if (check_scan_sizes(tokens, num_seqs, channels, groups, N, dtype, variant, &tiled) != CONV_OK)
         return -1;
-    return 0;
+    return tiled ? scan_tiled_workspace(tokens, num_seqs, channels, groups, N) : 0;
 }
 
 conv_status conv_selective_scan_fwd(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const float *a,
@@ -212,7 +213,7 @@ conv_status conv_selective_scan_fwd(const void *x, int64_t x_stride, const void 
     p.N = N;
     p.softplus = softplus;
     p.dtype = dtype;
-    return launched(launch_scan_direct(p, (hipStream_t)stream));
+    return launched(tiled ? launch_scan_tiled(p, (hipStream_t)stream) : launch_scan_direct(p, (hipStream_t)stream));
 }
 
 int64_t conv_selective_scan_heads_workspace(int64_t tokens, int num_seqs, int H, int P, int groups, int N, conv_dtype dtype,

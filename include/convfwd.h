@@ -509,8 +509,14 @@ CONVFWD_API conv_status conv_rotary_fwd(const void *q, const int64_t *q_strides,
  *   workspace  device memory of at least conv_selective_scan_workspace
  *              bytes, 256-byte aligned, used during the call only (NULL when
  *              that is 0).
- *   variant    CONV_VARIANT_DIRECT: token by token. CONV_VARIANT_AUTO: the same.
+ *   variant    CONV_VARIANT_DIRECT: token by token. CONV_VARIANT_TILED: by
+ *              tiles of 128 tokens, N <= 32. Both compute in fp32, and refuse
+ *              with CONV_ERR_UNSUPPORTED what their grids do not hold.
+ *              CONV_VARIANT_AUTO picks one for the whole call from tokens /
+ *              num_seqs, the only lengths known on the host.
  *
+ * d a <= 0, a decay, is the scan's use. A state may grow too, but where it
+ * grows past 2^100 within a tile the outputs from there on are unspecified.
  * A value that is not finite, or leaves fp32's range, reaches no earlier
  * token and no other sequence.
  */
@@ -557,6 +563,8 @@ CONVFWD_API int64_t conv_selective_scan_workspace(int64_t tokens, int num_seqs, 
  *              CONV_VARIANT_AUTO picks one for the whole call from tokens /
  *              num_seqs, the only lengths known on the host.
  *
+ * d a <= 0, a decay, is the scan's use. A state may grow too, but where it
+ * grows past 2^100 within a chunk the outputs from there on are unspecified.
  * A value that is not finite, or leaves fp32's range, reaches no earlier
  * token, no other group and no other sequence.
  */

@@ -57,9 +57,34 @@ RAGGED = [[1], [5], [3, 0, 1, 9], [64, 63, 65, 1, 0, 2]]
 @pytest.mark.parametrize("lens", RAGGED, ids=str)
 @pytest.mark.parametrize("C,G,N", [(1, 1, 1), (5, 1, 3), (24, 2, 16), (70, 1, 16), (9, 3, 5), (33, 1, 8), (12, 2, 33),
                                    (8, 1, 64), (6, 1, 100), (4, 2, 200), (3, 1, 256)])
-def test_channels(C, G, N, lens, dtype):
+@pytest.mark.parametrize("variant", [DIRECT, TILED])
+def test_channels(C, G, N, lens, dtype, variant):
+    if variant == TILED and N > 32:
+        pytest.skip("tiles take up to 32 states")
     ins = channel_inputs(sum(lens), C, G, N, dtype, C + N)
-    check(cf.selective_scan, ins, lens, rnd((len(lens), C, N), 1))
+    check(cf.selective_scan, ins, lens, rnd((len(lens), C, N), 1), variant)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens,C,G,N", [([700, 3, 0, 297], 40, 1, 16), ([1000], 20, 2, 8), ([3000], 5, 1, 32),
+                                        ([256, 512, 257], 34, 1, 13), ([900, 900], 64, 1, 16)], ids=str)
+def test_channels_in_segments(lens, C, G, N, dtype):
+    """Sequences past one segment, states updated in place; without offsets where they are equally long."""
+    ins, st = channel_inputs(sum(lens), C, G, N, dtype, 21), rnd((len(lens), C, N), 22)
+    y0, by, h0, bh = ref.channels(*ins, True, lens, st)
+    x, dt, a, b, c, skip, gate, bias = gpu(ins)
+    kw = dict(skip=skip, dt_bias=bias, dt_softplus=True, variant=TILED)
+    pool = st.to(DEV)
+    y = cf.selective_scan(x, dt, a, b, c, gate=gate, seq_offsets=seqs(lens, DEV), initial_state=pool, final_state=pool, **kw)
+    mixer_ref.check(y, y0, by, "y", dtype)
+    mixer_ref.check(pool, h0, bh, "state", F32)
+    if len(set(lens)) == 1:
+        n = len(lens)
+        x, dt, b, c, gate = (t.unflatten(0, (n, -1)) for t in (x, dt, b, c, gate))
+        pool = st.to(DEV)
+        y = cf.selective_scan(x, dt, a, b, c, gate=gate, initial_state=pool, final_state=pool, **kw)
+        mixer_ref.check(y.flatten(0, 1), y0, by, "equal, y", dtype)
+        mixer_ref.check(pool, h0, bh, "equal, state", F32)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -159,10 +184,12 @@ def test_no_tokens(which):
     fn, ins, shape = cases()[which]
     x, dt, a, b, c, skip, gate, bias = gpu(ins)
     st, new = rnd((2,) + shape, 8).to(DEV), torch.zeros((2,) + shape, device=DEV)
-    y = fn(x[:0], dt[:0], a, b[:0], c[:0], seq_offsets=seqs([0, 0], DEV), initial_state=st, final_state=new)
-    assert y.shape[0] == 0 and torch.equal(new, st)
-    fn(x[:0], dt[:0], a, b[:0], c[:0], seq_offsets=seqs([0, 0], DEV), final_state=new)
-    assert (new == 0).all()
+    for variant in (DIRECT, TILED):
+        kw = dict(seq_offsets=seqs([0, 0], DEV), variant=variant)
+        y = fn(x[:0], dt[:0], a, b[:0], c[:0], initial_state=st, final_state=new, **kw)
+        assert y.shape[0] == 0 and torch.equal(new, st)
+        fn(x[:0], dt[:0], a, b[:0], c[:0], final_state=new, **kw)
+        assert (new == 0).all()
     fn(x[:0], dt[:0], a, b[:0], c[:0])
 
 
@@ -170,21 +197,23 @@ def test_no_tokens(which):
 def test_rows_behind_the_last_sequence_stay(which):
     fn, ins, shape = cases()[which]
     x, dt, a, b, c, skip, gate, bias = gpu(ins)
-    out = torch.full_like(x, 7.0)
-    fn(x, dt, a, b, c, seq_offsets=seqs([30, 40], DEV), out=out, final_state=torch.zeros((2,) + shape, device=DEV))
-    assert (out[70:] == 7).all() and not (out[:70] == 7).all(-1).any()
-    assert torch.equal(out[:70], fn(x[:70], dt[:70], a, b[:70], c[:70], seq_offsets=seqs([30, 40], DEV)))
+    for variant in (DIRECT, TILED):
+        out, kw = torch.full_like(x, 7.0), dict(seq_offsets=seqs([30, 40], DEV), dt_softplus=True, variant=variant)
+        fn(x, dt, a, b, c, out=out, final_state=torch.zeros((2,) + shape, device=DEV), **kw)
+        assert (out[70:] == 7).all() and not (out[:70] == 7).all(-1).any()
+        assert torch.equal(out[:70], fn(x[:70], dt[:70], a, b[:70], c[:70], **kw))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("at", [0, 37, 63, 64, 99])
 @pytest.mark.parametrize("which", ["x", "dt", "b", "c", "state"])
-def test_channels_not_finite(which, at, value, dtype):
+@pytest.mark.parametrize("variant", [DIRECT, TILED])
+def test_channels_not_finite(variant, which, at, value, dtype):
     """What is not finite reaches no earlier token, no other channel (b, c: no other group) and no other sequence."""
     ins = list(channel_inputs(130, 24, 2, 16, dtype, 9))
     lens, st = [100, 30], rnd((2, 24, 16), 10)
-    clean, new0 = run(cf.selective_scan, ins, lens, st)
+    clean, new0 = run(cf.selective_scan, ins, lens, st, variant)
     bad = list(ins)
     i = dict(x=0, dt=1, b=3, c=4).get(which)
     hit = torch.zeros(130, 24, dtype=torch.bool)        # where outputs may differ
@@ -202,7 +231,7 @@ def test_channels_not_finite(which, at, value, dtype):
         else:
             bad[i][at, 5] = value
             hit[at:100, 5] = held[0, 5] = True
-    y, new = run(cf.selective_scan, bad, lens, st)
+    y, new = run(cf.selective_scan, bad, lens, st, variant)
     assert torch.equal(y.cpu()[~hit], clean.cpu()[~hit]) and torch.equal(new.cpu()[~held], new0.cpu()[~held])
     if which != "state" and not (which == "dt" and value > 0):      # an infinite step size forgets the state: 0 b x is NaN
         assert not torch.isfinite(y.cpu()[at][hit[at]]).any()
@@ -256,12 +285,11 @@ def test_strong_decays_and_steps():
         ins[1][40] = 3000.0
         ins[1][50:60] = -200.0          # steps of zero
         ins[1][66] = 60.0
-        variants = [AUTO, DIRECT] + [TILED] * (fn is cf.selective_scan_heads)
-        for v in variants:
+        for v in (DIRECT, TILED):
             check(fn, ins, lens, rnd((2,) + shape, 12), v)
         ins[1] = ins[1].clamp(-3, 0.5)
         ins[2] = -0.05 * ins[2]         # growth
-        for v in variants:
+        for v in (DIRECT, TILED):
             check(fn, ins, lens, rnd((2,) + shape, 12), v)
 
 
