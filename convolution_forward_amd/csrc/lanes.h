@@ -38,4 +38,22 @@ __device__ __forceinline__ float lanes_sum(float v)
     return v;
 }
 
+// Sums of U values (2 or 4) over each aligned group of U lanes: lane u of the
+// group gets the sum of the values u. 3 and 9 instructions, against 2 and 8 for
+// all sums in all lanes.
+template <int U>
+__device__ __forceinline__ float lanes_scatter(const float (&v)[U], int lane)
+{
+    static_assert(U == 2 || U == 4, "pairs or fours");
+    const bool odd = lane & 1;
+    const float a = (odd ? v[1] : v[0]) + lane_moved<0xB1>(odd ? v[0] : v[1]);
+    if constexpr (U == 2) {
+        return a;
+    } else {
+        const float b = (odd ? v[3] : v[2]) + lane_moved<0xB1>(odd ? v[2] : v[3]);
+        const bool upper = lane & 2;
+        return (upper ? b : a) + lane_moved<0x4E>(upper ? a : b);
+    }
+}
+
 }  // namespace convfwd

@@ -12,7 +12,9 @@
 // A workgroup takes `toks` tokens. Its threads first write their cosines and
 // sines to LDS, one angle a thread (a token's 32 to 48 heads would make each of
 // them as often, at some 60 instructions), then groups of L lanes go over the
-// heads, `toks` groups side by side on one token each.
+// heads, `toks` groups side by side on one token each. 16384 tokens of 32 and 8
+// heads of 128, bf16, with norms: 65 us, 0.34 GB at 5.15 TB/s (a plain copy:
+// 5.1). 8 tokens: 5.8 us, a launch.
 //
 // An angle is the exact product (a double holds 29 bits of position times 24
 // of frequency) as turns, reduced in 64 bits to an eighth of a turn round a
@@ -64,6 +66,18 @@ __device__ __forceinline__ Piece<T, V> load_piece(const T *p)
     return t;
 }
 
+// STREAM: past the caches, for outputs that would push each other out of them.
+template <bool STREAM, class T, int V>
+__device__ __forceinline__ void store_piece(T *p, const Piece<T, V> &t)
+{
+    if constexpr (V > 1 && STREAM) {
+        typedef uint32_t Words __attribute__((ext_vector_type(V * sizeof(T) / 4)));
+        __builtin_nontemporal_store(__builtin_bit_cast(Words, t), reinterpret_cast<Words *>(p));
+    } else {
+        __builtin_memcpy(__builtin_assume_aligned(p, V * sizeof(T)), &t, sizeof(t));
+    }
+}
+
 struct RotaryArgs {
     RotaryProblem p;
     int toks;               // tokens of a workgroup
@@ -71,7 +85,7 @@ struct RotaryArgs {
 };
 
 // L lanes a head, NU units of two pieces of V values a lane.
-template <class T, int V, int L, int NU, bool INTER>
+template <class T, int V, int L, int NU, bool INTER, bool STREAM>
 __global__ __launch_bounds__(NT) void rotary_kernel(RotaryArgs a)
 {
     const RotaryProblem &p = a.p;
@@ -208,9 +222,9 @@ __global__ __launch_bounds__(NT) void rotary_kernel(RotaryArgs a)
                     store_rne(&o[1].v[i], f[u][1][i]);
                 }
                 if (has0[u])
-                    __builtin_memcpy(__builtin_assume_aligned(y + at0[u], V * sizeof(T)), &o[0], sizeof(o[0]));
+                    store_piece<STREAM>(y + at0[u], o[0]);
                 if (has1[u])
-                    __builtin_memcpy(__builtin_assume_aligned(y + at1[u], V * sizeof(T)), &o[1], sizeof(o[1]));
+                    store_piece<STREAM>(y + at1[u], o[1]);
             }
         }
     }
@@ -225,14 +239,25 @@ void launch_units(const RotaryProblem &p, hipStream_t s)
     // Few tokens: one a workgroup, and only as many heads as it has groups, so
     // that the heads spread over the compute units.
     const bool few = p.tokens * (int64_t)total <= 4096;
+    // (Otherwise 4 tokens: 2 take the 16384 tokens below 81 us, 8 take them 69, but 1024 tokens 12.7 against 9.7.)
     a.toks = few ? 1 : (groups < 4 ? groups : 4);
     a.heads = few ? groups : total;
     const dim3 grid((unsigned)((p.tokens + a.toks - 1) / a.toks), (unsigned)((total + a.heads - 1) / a.heads));
     const size_t lds = (size_t)a.toks * p.rotated * sizeof(float);
-    if (p.interleaved)
-        hipLaunchKernelGGL((rotary_kernel<T, V, L, NU, true>), grid, dim3(NT), lds, s, a);
+    // Outputs past 64 MB leave the caches before a reader comes: streaming
+    // stores, 16384 tokens of 40 heads of 128 in 65 us against 72. Smaller ones
+    // stay: 4096 tokens of 18 heads of 256, written where the call before
+    // wrote, in 16 us, streamed in 21. (Buffers that are all out of the caches
+    // would gain by streaming at any size: 40 MB 16 against 23.)
+    const bool stream = V > 1 && p.tokens * total * p.D * (int64_t)sizeof(T) > (int64_t(64) << 20);
+    if (p.interleaved && stream)
+        hipLaunchKernelGGL((rotary_kernel<T, V, L, NU, true, V != 1>), grid, dim3(NT), lds, s, a);
+    else if (p.interleaved)
+        hipLaunchKernelGGL((rotary_kernel<T, V, L, NU, true, false>), grid, dim3(NT), lds, s, a);
+    else if (stream)
+        hipLaunchKernelGGL((rotary_kernel<T, V, L, NU, false, V != 1>), grid, dim3(NT), lds, s, a);
     else
-        hipLaunchKernelGGL((rotary_kernel<T, V, L, NU, false>), grid, dim3(NT), lds, s, a);
+        hipLaunchKernelGGL((rotary_kernel<T, V, L, NU, false, false>), grid, dim3(NT), lds, s, a);
 }
 
 // Whether pieces of V values hold whole pairs and lie where a load of V values may.

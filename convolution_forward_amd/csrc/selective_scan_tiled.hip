@@ -74,6 +74,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
     __shared__ __align__(16) float bs[TILE][NP], cs[FULL ? TILE : 1][NP];
     __shared__ f32x4 fold[WAVES][2][64];                // decay of a wave's tokens, state they add
     __shared__ f32x4 carry[64];                         // the state before the tile
+    __shared__ __align__(16) float biases[CH], skips[CH];
 
     // Workgroup i runs on XCD i % 8: neighbouring channels, which share lines of x, go to one XCD.
     const int xcd = (int)blockIdx.x & 7, around = (a.slices + 7) / 8;
@@ -123,18 +124,34 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
     };
     Piece<T, EC> xv, dv, gv;
     Piece<T, EB> bv, cv;
+    // A tile's rows lie within 2^31 bytes of its first one (VEC: a host rule): one address for all lanes, and a lane's
+    // offset by one multiplication of 24 bits.
+    auto row_of = [&](const T *base, int64_t stride, int t, int r) __attribute__((always_inline)) {
+        base += (int64_t)t * TILE * stride;
+        if constexpr (VEC)
+            return reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) +
+                                               __umul24((uint32_t)r, (uint32_t)stride * (uint32_t)sizeof(T)));
+        else
+            return base + r * stride;
+    };
     auto load = [&](int t) __attribute__((always_inline)) {
-        const int64_t r = min(t * TILE + tok, len - 1), rb = min(t * TILE + btok, len - 1);
-        row_piece(xv, xp + r * p.xs, cc, end);
-        row_piece(dv, dp + r * p.dts, cc, end);
-        row_piece(bv, bp + rb * p.bst, bn, p.N);
+        const int rows = min(len - t * TILE, TILE);
+        const int r = min(tok, rows - 1), rb = min(btok, rows - 1);
+        row_piece(xv, row_of(xp, p.xs, t, r), cc, end);
+        row_piece(dv, row_of(dp, p.dts, t, r), cc, end);
+        row_piece(bv, row_of(bp, p.bst, t, rb), bn, p.N);
         if constexpr (FULL) {
-            row_piece(gv, gp + r * gs, cc, end);
-            row_piece(cv, cp + rb * p.cst, bn, p.N);
+            row_piece(gv, row_of(gp, gs, t, r), cc, end);
+            row_piece(cv, row_of(cp, p.cst, t, rb), bn, p.N);
         }
     };
     if (tiles > 0)
         load(0);
+    if (tid < CH) {
+        const int ci = begin + tid < end ? begin + tid : begin;
+        biases[tid] = p.bias ? p.bias[ci] : 0.f;
+        skips[tid] = p.skip ? p.skip[ci] : 0.f;
+    }
 
     // ---- The lane's rates and the state before the segment.
     const int64_t sat = (int64_t)(live ? c : 0) * p.N + n0;
@@ -173,6 +190,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
         carry[lane] = h;
     }
 
+    lds_barrier();                  // biases and skips are there
     float total = 0.f;              // sum of the steps of the wave's tokens so far
     for (int t = 0; t < tiles; ++t) {
         const int rows = min(len - t * TILE, TILE);
@@ -187,21 +205,44 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
         bn = tid * EB % NP;
         // ---- 1.
         const bool there = tok < rows;
-        float x[EC];
+        float x[EC], d[EC], dx[EC], bf[EB], cf[EB];
 #pragma unroll
         for (int i = 0; i < EC; ++i) {
-            const int ci = cc + i < end ? cc + i : 0;
-            const float d = step_size(load_as_f32(&dv.v[i]) + (p.bias ? p.bias[ci] : 0.f), p.softplus);
             x[i] = load_as_f32(&xv.v[i]);
-            steps[tok][ch0 + i] = there ? f32x2{d, d * x[i]} : f32x2{0.f, 0.f};
+            d[i] = step_size(load_as_f32(&dv.v[i]) + biases[ch0 + i], p.softplus);
+            dx[i] = d[i] * x[i];
         }
 #pragma unroll
         for (int i = 0; i < EB; ++i) {
-            const bool in = btok < rows && bn + i < p.N;
-            bs[btok][bn + i] = in ? load_as_f32(&bv.v[i]) : 0.f;
-            if constexpr (FULL)
-                cs[btok][bn + i] = in ? load_as_f32(&cv.v[i]) : 0.f;
+            bf[i] = load_as_f32(&bv.v[i]);
+            cf[i] = FULL ? load_as_f32(&cv.v[i]) : 0.f;
         }
+        if (rows < TILE || p.N < NP) {      // zeros for what is not there
+#pragma unroll
+            for (int i = 0; i < EC; ++i)
+                d[i] = there ? d[i] : 0.f, dx[i] = there ? dx[i] : 0.f;
+#pragma unroll
+            for (int i = 0; i < EB; ++i) {
+                const bool in = btok < rows && bn + i < p.N;
+                bf[i] = in ? bf[i] : 0.f;
+                cf[i] = in ? cf[i] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < EC; i += 2)
+            *reinterpret_cast<f32x4 *>(&steps[tok][ch0 + i]) = f32x4{d[i], dx[i], d[i + 1], dx[i + 1]};
+        auto put = [&](float *to, const float(&v)[EB]) __attribute__((always_inline)) {
+            if constexpr (EB >= 4) {
+#pragma unroll
+                for (int i = 0; i < EB; i += 4)
+                    *reinterpret_cast<f32x4 *>(to + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+            } else {
+                *reinterpret_cast<f32x2 *>(to) = f32x2{v[0], v[1]};
+            }
+        };
+        put(&bs[btok][bn], bf);
+        if constexpr (FULL)
+            put(&cs[btok][bn], cf);
         Piece<T, EC> gate = gv;
         lds_barrier();
         if (t + 1 < tiles)
@@ -235,28 +276,47 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
         h = before;
         const int upto = FULL ? w : WAVES;
         if (FULL || w == WAVES - 1)
-            for (int j = 0; j < upto; ++j) {
-                const f32x4 pj = fold[j][0][lane], hj = fold[j][1][lane];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    h[i] = fmaf(pj[i], h[i], hj[i]);
-            }
+            for (int j0 = 0; j0 < (FULL ? WAVES - 1 : WAVES); j0 += 2)
+                if (j0 < upto) {            // two at a time, their reads in flight together
+                    f32x4 pj[2], hj[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        pj[j] = fold[j0 + j][0][lane];
+                        hj[j] = fold[j0 + j][1][lane];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (j0 + j < upto)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                h[i] = fmaf(pj[j][i], h[i], hj[j][i]);
+                }
         if constexpr (FULL) {
             const f32x4 *cw = reinterpret_cast<const f32x4 *>(&cs[TS * w][n0]);
-            float *yw = reinterpret_cast<float *>(&steps[TS * w][lane / LN]);
+            // y of U tokens at a time: lane u of a channel ends with the sum for token u.
+            constexpr int U = LN < 4 ? LN : 4;
+            float *yw = reinterpret_cast<float *>(&steps[TS * w][lane / LN]) + (LN <= 4 || lane % LN < 4 ? lane % U * CH * 2 : 0);
 #pragma unroll
-            for (int s = 0; s < TS; ++s) {
-                const float dx = st[s * CH][1];
-                const f32x4 b = bw[s * LN], ct = cw[s * LN];
-                float y = 0.f;
+            for (int s0 = 0; s0 < TS; s0 += U) {
+                float y[U];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[i] = fmaf(e[s][i], h[i], dx * b[i]);
-                    y = fmaf(h[i], ct[i], y);
+                for (int u = 0; u < U; ++u) {
+                    const int s = s0 + u;
+                    const float dxs = st[s * CH][1];
+                    const f32x4 b = bw[s * LN], ct = cw[s * LN];
+                    y[u] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        h[i] = fmaf(e[s][i], h[i], dxs * b[i]);
+                        y[u] = fmaf(h[i], ct[i], y[u]);
+                    }
                 }
-                y = lanes_sum<LN>(y);
-                if (lane % LN == 0)
-                    yw[s * CH * 2] = y;
+                float sum_u = lanes_scatter<U>(y, lane);
+                if constexpr (LN == 8)
+                    sum_u += lane_moved<0x104>(sum_u);      // of the lane four above
+                if (LN <= 4 || lane % LN < 4)
+                    yw[s0 * CH * 2] = sum_u;
             }
         }
         total += sum;
@@ -268,13 +328,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
             Piece<T, EC> o;
 #pragma unroll
             for (int i = 0; i < EC; ++i) {
-                const int ci = cc + i < end ? cc + i : 0;
-                float y = fmaf(p.skip ? p.skip[ci] : 0.f, x[i], steps[tok][ch0 + i][0]);
+                float y = fmaf(skips[ch0 + i], x[i], steps[tok][ch0 + i][0]);
                 if (p.gate)
                     y *= silu(load_as_f32(&gate.v[i]));
                 store_rne(&o.v[i], y);
             }
-            T *yr = yp + (int64_t)(t * TILE + tok) * p.ys + cc;
+            T *yr = const_cast<T *>(row_of(yp, p.ys, t, tok)) + cc;
             if (there) {
                 if constexpr (VEC) {
                     if (cc < end)
@@ -401,7 +460,9 @@ hipError_t launch(const ScanArgs &a, const Plan &l, hipStream_t s)
     const uintptr_t bc = (uintptr_t)p.b | (uintptr_t)p.c | (uintptr_t)((p.bst | p.bsg | p.cst | p.csg) * sizeof(T)) |
                          (uintptr_t)(p.N * sizeof(T));
     const uintptr_t st = (uintptr_t)p.a | (uintptr_t)p.state_in | (uintptr_t)p.state_out;
-    const bool vec = rows % (ec < 16 ? ec : 16) == 0 && bc % (eb < 16 ? eb : 16) == 0 && st % 16 == 0 && p.N % 4 == 0;
+    const int64_t far = int64_t(1) << 22;       // a row's bytes fit 24 bits
+    const bool vec = p.xs < far && p.dts < far && p.ys < far && (!p.gate || p.gs < far) && p.bst < far && p.cst < far &&
+                     rows % (ec < 16 ? ec : 16) == 0 && bc % (eb < 16 ? eb : 16) == 0 && st % 16 == 0 && p.N % 4 == 0;
     switch (l.ln) {
     case 2: return launch_lanes<T, 2>(a, l.parts, vec, s);
     case 4: return launch_lanes<T, 4>(a, l.parts, vec, s);
