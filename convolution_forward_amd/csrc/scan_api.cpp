@@ -42,7 +42,16 @@ conv_status check_scan_sizes(int64_t tokens, int num_seqs, int channels, int gro
     if (tokens > MAX_ROWS || num_seqs > MAX_ROWS || channels > (1 << 23) || N > 256 || !known_variant(variant))
         return CONV_ERR_UNSUPPORTED;
     const bool can = scan_tiled_supports(tokens, num_seqs, channels, groups, N);
-    *tiled = variant == CONV_VARIANT_TILED || (variant == CONV_VARIANT_AUTO && can && tokens > 24 * (int64_t)num_seqs);
+    // Tokens a sequence, as the host knows them (the mean), from which tiles are
+    // faster. A lone sequence of 8192 channels of 16 states takes 9 us by tiles up
+    // to 64 tokens, and token by token 9 for 16 of them, 14 for 32. Once there
+    // are more workgroups than run at once, 8 such sequences take 51 us by tiles
+    // up to 32 tokens and 54 for 64 (token by token 25 and 48), 64 take 380 and
+    // 423 (146 and 295); tiles are ahead from some 70 and 110 tokens. But one long
+    // sequence among short ones is the time token by token, so less is asked for.
+    const bool alone = (int64_t)num_seqs * channels * N <= 512 * 256;
+    const int least = alone ? 16 : 48;
+    *tiled = variant == CONV_VARIANT_TILED || (variant == CONV_VARIANT_AUTO && can && tokens > least * (int64_t)num_seqs);
     return (*tiled ? can : scan_direct_supports(num_seqs, channels, N)) ? CONV_OK : CONV_ERR_UNSUPPORTED;
 }
 
@@ -58,7 +67,16 @@ conv_status check_heads_sizes(int64_t tokens, int num_seqs, int H, int P, int gr
     if (tokens > MAX_ROWS || num_seqs > MAX_ROWS || H > 65535 || P > 65536 || N > 256 || !known_variant(variant))
         return CONV_ERR_UNSUPPORTED;
     const bool can = heads_chunked_supports(tokens, num_seqs, H, P, groups, N, dtype);
-    *tiled = variant == CONV_VARIANT_TILED || (variant == CONV_VARIANT_AUTO && can && tokens > 12 * (int64_t)num_seqs);
+    // Tokens a sequence, as the host knows them (the mean), from which chunks
+    // are faster. bf16, heads of 64 x 128: a lone sequence of 128 heads takes 13 us
+    // by chunks up to 32 tokens, and token by token 11.5 for 8 of them, 15.8 for
+    // 16; 8 such sequences 22 us (token by token 20 for 4 tokens, 28 for 8), 64 of
+    // them 147 to 156 (149 and 204). fp32, 32 heads of 64 x 64, where a chunk costs
+    // more: 11.5 us alone (24 tokens one by one 10.4, 32 12.0), 64 sequences 94 to
+    // 99 (32 tokens 75, 64 138).
+    const bool alone = (int64_t)num_seqs * H * P <= 16384;
+    const int least = dtype == CONV_F32 ? (alone ? 24 : 44) : alone ? 12 : 6;
+    *tiled = variant == CONV_VARIANT_TILED || (variant == CONV_VARIANT_AUTO && can && tokens > least * (int64_t)num_seqs);
     return (*tiled ? can : heads_direct_supports(num_seqs, H, P, N)) ? CONV_OK : CONV_ERR_UNSUPPORTED;
 }
 

@@ -85,27 +85,30 @@ struct __align__(16) Factors {
 // of the next chunk that are in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Eight values as bf16 parts, the nearest bf16 of what the parts before left.
-// (A remainder is one v_dot2_f32_bf16 with (-1, 0) too, exactly, but those
-// share the matrix cores: beside a wave of matrix instructions one takes 22
-// clocks, a subtraction or mask 8.6.)
+// Eight values as three bf16 parts each, every part what the ones before left,
+// cut to bf16's eight bits: together exactly the value (down to fp32's smallest
+// normal number times 2^16). Masks and subtractions, 2.7 clocks a wave beside
+// others; rounding conversions and shifts would take 4.4. (A remainder is one
+// v_dot2_f32_bf16 too, but those share the matrix cores: beside a wave of matrix
+// instructions one takes 22 clocks.)
 __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&part)[3])
 {
+    u32x4 packed[3];
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
         float a = x[2 * h], b = x[2 * h + 1];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            const bf16x2 t = __builtin_convertvector((f32x2{a, b}), bf16x2);
-            part[i][2 * h] = t[0];
-            part[i][2 * h + 1] = t[1];
+            packed[i][h] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
             if (i < 2) {
-                const uint32_t u = __builtin_bit_cast(uint32_t, t);
-                a -= __uint_as_float(u << 16);
-                b -= __uint_as_float(u & 0xffff0000u);
+                a -= __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+                b -= __uint_as_float(__float_as_uint(b) & 0xffff0000u);
             }
         }
     }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        part[i] = __builtin_bit_cast(bf16x8, packed[i]);
 }
 
 // acc += a b, each of one exact part or three.

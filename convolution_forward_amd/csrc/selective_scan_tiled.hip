@@ -248,79 +248,84 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
         if (t + 1 < tiles)
             load(t + 1);
         // ---- 2.
+        const int waves = (rows + TS - 1) / TS;         // that have tokens; the others have nothing to do here
         const f32x4 before = carry[lane];
         f32x4 e[TS];
         f32x4 h = {0.f, 0.f, 0.f, 0.f};
         float sum = 0.f;
         const f32x2 *st = &steps[TS * w][lane / LN];
         const f32x4 *bw = reinterpret_cast<const f32x4 *>(&bs[TS * w][n0]);
+        if (w < waves) {
 #pragma unroll
-        for (int s = 0; s < TS; ++s) {
-            const f32x2 v = st[s * CH];
-            const f32x4 b = bw[s * LN];
-            sum += v[0];
+            for (int s = 0; s < TS; ++s) {
+                const f32x2 v = st[s * CH];
+                const f32x4 b = bw[s * LN];
+                sum += v[0];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                e[s][i] = __builtin_amdgcn_exp2f(v[0] * rate[i]);
-                h[i] = fmaf(e[s][i], h[i], v[1] * b[i]);
+                for (int i = 0; i < 4; ++i) {
+                    e[s][i] = __builtin_amdgcn_exp2f(v[0] * rate[i]);
+                    h[i] = fmaf(e[s][i], h[i], v[1] * b[i]);
+                }
             }
-        }
-        f32x4 all;
+            f32x4 all;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            all[i] = __builtin_amdgcn_exp2f(sum * rate[i]);
-        fold[w][0][lane] = all;
-        fold[w][1][lane] = h;
+            for (int i = 0; i < 4; ++i)
+                all[i] = __builtin_amdgcn_exp2f(sum * rate[i]);
+            fold[w][0][lane] = all;
+            fold[w][1][lane] = h;
+        }
         lds_barrier();
         // ---- 3.
-        h = before;
-        const int upto = FULL ? w : WAVES;
-        if (FULL || w == WAVES - 1)
+        if (w < waves) {
+            h = before;
+            const int upto = FULL ? w : waves;
+            if (FULL || w == waves - 1)
 #pragma unroll
-            for (int j0 = 0; j0 < (FULL ? WAVES - 1 : WAVES); j0 += 2)
-                if (j0 < upto) {            // two at a time, their reads in flight together
-                    f32x4 pj[2], hj[2];
+                for (int j0 = 0; j0 < (FULL ? WAVES - 1 : WAVES); j0 += 2)
+                    if (j0 < upto) {            // two at a time, their reads in flight together
+                        f32x4 pj[2], hj[2];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        pj[j] = fold[j0 + j][0][lane];
-                        hj[j] = fold[j0 + j][1][lane];
+                        for (int j = 0; j < 2; ++j) {
+                            pj[j] = fold[j0 + j][0][lane];
+                            hj[j] = fold[j0 + j][1][lane];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (j0 + j < upto)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    h[i] = fmaf(pj[j][i], h[i], hj[j][i]);
                     }
+            if constexpr (FULL) {
+                const f32x4 *cw = reinterpret_cast<const f32x4 *>(&cs[TS * w][n0]);
+                // y of U tokens at a time: lane u of a channel ends with the sum for token u.
+                constexpr int U = LN < 4 ? LN : 4;
+                float *yw = reinterpret_cast<float *>(&steps[TS * w][lane / LN]) + (LN <= 4 || lane % LN < 4 ? lane % U * CH * 2 : 0);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        if (j0 + j < upto)
+                for (int s0 = 0; s0 < TS; s0 += U) {
+                    float y[U];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                h[i] = fmaf(pj[j][i], h[i], hj[j][i]);
-                }
-        if constexpr (FULL) {
-            const f32x4 *cw = reinterpret_cast<const f32x4 *>(&cs[TS * w][n0]);
-            // y of U tokens at a time: lane u of a channel ends with the sum for token u.
-            constexpr int U = LN < 4 ? LN : 4;
-            float *yw = reinterpret_cast<float *>(&steps[TS * w][lane / LN]) + (LN <= 4 || lane % LN < 4 ? lane % U * CH * 2 : 0);
+                    for (int u = 0; u < U; ++u) {
+                        const int s = s0 + u;
+                        const float dxs = st[s * CH][1];
+                        const f32x4 b = bw[s * LN], ct = cw[s * LN];
+                        y[u] = 0.f;
 #pragma unroll
-            for (int s0 = 0; s0 < TS; s0 += U) {
-                float y[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int s = s0 + u;
-                    const float dxs = st[s * CH][1];
-                    const f32x4 b = bw[s * LN], ct = cw[s * LN];
-                    y[u] = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        h[i] = fmaf(e[s][i], h[i], dxs * b[i]);
-                        y[u] = fmaf(h[i], ct[i], y[u]);
+                        for (int i = 0; i < 4; ++i) {
+                            h[i] = fmaf(e[s][i], h[i], dxs * b[i]);
+                            y[u] = fmaf(h[i], ct[i], y[u]);
+                        }
                     }
+                    float sum_u = lanes_scatter<U>(y, lane);
+                    if constexpr (LN == 8)
+                        sum_u += lane_moved<0x104>(sum_u);      // of the lane four above
+                    if (LN <= 4 || lane % LN < 4)
+                        yw[s0 * CH * 2] = sum_u;
                 }
-                float sum_u = lanes_scatter<U>(y, lane);
-                if constexpr (LN == 8)
-                    sum_u += lane_moved<0x104>(sum_u);      // of the lane four above
-                if (LN <= 4 || lane % LN < 4)
-                    yw[s0 * CH * 2] = sum_u;
             }
         }
         total += sum;
-        if (w == WAVES - 1)
+        if (w == waves - 1)
             carry[lane] = h;
         lds_barrier();
         // ---- 4.
