@@ -7,7 +7,8 @@
 // The bytes are the time: one pass, a head in the registers of L neighbouring
 // lanes from its load to its store. A lane's unit is two pieces of V values
 // that hold V whole pairs, i and i + R/2 or 2i and 2i + 1, so that no value
-// changes lanes; the norm is an exchange between L lanes.
+// changes lanes; the norm is an exchange between L lanes. V is the most that
+// 16 bytes hold, where the sizes, strides and addresses allow.
 //
 // A workgroup takes `toks` tokens. Its threads first write their cosines and
 // sines to LDS, one angle a thread (a token's 32 to 48 heads would make each of
@@ -108,28 +109,44 @@ __global__ __launch_bounds__(NT) void rotary_kernel(RotaryArgs a)
     const int64_t t = first + tok;
     if (t >= p.tokens)
         return;
-    // A unit's places in a head, and which of its pieces are there.
-    int at0[NU], at1[NU], pair[NU];
-    bool has0[NU], has1[NU], turned[NU];
+    // A unit's places in a head, which of its pieces are there and which of its
+    // pairs (the first and the second half of them) are rotated. Neighbouring
+    // lanes' pieces are neighbours, for the first and for the second pieces.
+    int at0[NU], at1[NU];
+    bool has0[NU], has1[NU], turn0[NU], turn1[NU];
     float cs[NU][V], sn[NU][V];
+    constexpr bool PIECES = INTER && V > 1;     // each piece holds whole pairs
+    const int pieces = p.D / V, across = PIECES ? (pieces + 1) / 2 : ((p.D - p.rotated) / V + 1) / 2;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
         const int unit = l + L * u;
-        pair[u] = unit * V;
-        turned[u] = pair[u] < half;
-        if (turned[u]) {
-            at0[u] = INTER ? 2 * pair[u] : pair[u];
-            at1[u] = INTER ? 2 * pair[u] + V : pair[u] + half;
+        int pair0, pair1;                       // of the first and of the second half of the unit's pairs
+        if (PIECES) {
+            at0[u] = unit * V;
+            at1[u] = at0[u] + across * V;
+            turn0[u] = unit < across && at0[u] < p.rotated;
+            turn1[u] = unit < across && at1[u] < p.rotated;
+            pair0 = at0[u] / 2;
+            pair1 = at1[u] / 2;
+            has0[u] = unit < across;
+            has1[u] = unit < across && at1[u] < p.D;
         } else {
-            at0[u] = 2 * pair[u];
-            at1[u] = 2 * pair[u] + V;
+            pair0 = unit * V;
+            pair1 = pair0 + V / 2;
+            turn0[u] = turn1[u] = pair0 < half;
+            const int rest = unit - half / V;   // of the pieces that are not rotated
+            at0[u] = turn0[u] ? (INTER ? 2 * pair0 : pair0) : p.rotated + rest * V;
+            at1[u] = turn0[u] ? (INTER ? 2 * pair0 + V : pair0 + half) : p.rotated + (rest + across) * V;
+            has0[u] = turn0[u] || rest < across;
+            has1[u] = turn0[u] || (rest < across && at1[u] < p.D);
         }
-        has0[u] = at0[u] < p.D;
-        has1[u] = at1[u] < p.D;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            cs[u][i] = turned[u] ? cosines[tok * half + pair[u] + i] : 1.f;
-            sn[u][i] = turned[u] ? sines[tok * half + pair[u] + i] : 0.f;
+            const bool second = 2 * i >= V && V > 1;
+            const bool on = second ? turn1[u] : turn0[u];
+            const int at = tok * half + (second ? pair1 + i - V / 2 : pair0 + i);
+            cs[u][i] = on ? cosines[at] : 1.f;
+            sn[u][i] = on ? sines[at] : 0.f;
         }
     }
     const bool qnorm = p.qweight != nullptr, knorm = p.kweight != nullptr;
@@ -205,9 +222,9 @@ __global__ __launch_bounds__(NT) void rotary_kernel(RotaryArgs a)
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
                 Piece<T, V> o[2];
-                if (turned[u]) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
+                for (int i = 0; i < V; ++i) {
+                    if (2 * i >= V && V > 1 ? turn1[u] : turn0[u]) {
                         // Pair i: value i of each piece, or values 2i and 2i + 1 of the two as one run.
                         float &x0 = INTER ? f[u][2 * i / V][2 * i % V] : f[u][0][i];
                         float &x1 = INTER ? f[u][(2 * i + 1) / V][(2 * i + 1) % V] : f[u][1][i];
@@ -240,7 +257,11 @@ void launch_units(const RotaryProblem &p, hipStream_t s)
     // that the heads spread over the compute units.
     const bool few = p.tokens * (int64_t)total <= 4096;
     // (Otherwise 4 tokens: 2 take the 16384 tokens below 81 us, 8 take them 69, but 1024 tokens 12.7 against 9.7.)
+    // With few heads more, so that every group has one (3 heads of 128, 109226
+    // tokens: 67 us with 4 tokens, 37 with 8), as far as the table is 16 KB.
     a.toks = few ? 1 : (groups < 4 ? groups : 4);
+    while (!few && a.toks * total < groups && a.toks * 2 * p.rotated <= 4096)
+        a.toks *= 2;
     a.heads = few ? groups : total;
     const dim3 grid((unsigned)((p.tokens + a.toks - 1) / a.toks), (unsigned)((total + a.heads - 1) / a.heads));
     const size_t lds = (size_t)a.toks * p.rotated * sizeof(float);
@@ -268,13 +289,15 @@ bool fits(const RotaryProblem &p, int V, int64_t esize)
                      (uintptr_t)p.qweight | (uintptr_t)p.kweight;
     if (p.Hk)
         bits |= (uintptr_t)p.k | (uintptr_t)p.k_out | (uintptr_t)((p.kst | p.ksh | p.kot | p.koh) * esize);
-    return bits % bytes == 0 && p.D % V == 0 && p.rotated % (2 * V) == 0;
+    return bits % bytes == 0 && p.D % V == 0 && p.rotated % (p.interleaved ? V : 2 * V) == 0;
 }
 
 template <class T, int V>
 void launch_pieces(const RotaryProblem &p, hipStream_t s)
 {
-    const int units = (p.D + 2 * V - 1) / (2 * V);
+    // Pairs of pieces; the pieces that are not rotated make pairs of their own, an odd one a unit alone.
+    const int rotated = p.interleaved && V > 1 ? 0 : p.rotated / (2 * V);
+    const int units = rotated + (p.D - 2 * V * rotated + 2 * V - 1) / (2 * V);
     if constexpr (V == 1) {
         units <= 64 ? launch_units<T, V, 64, 1>(p, s) : launch_units<T, V, 64, 4>(p, s);
     } else {
@@ -301,6 +324,8 @@ void launch(const RotaryProblem &p, hipStream_t s)
         launch_pieces<T, V>(p, s);
     else if (fits(p, V / 2, sizeof(T)))
         launch_pieces<T, V / 2>(p, s);
+    else if (sizeof(T) == 2 && fits(p, 2, sizeof(T)))
+        launch_pieces<T, 2>(p, s);
     else
         launch_pieces<T, 1>(p, s);
 }
