@@ -8,16 +8,18 @@
 // with the skipped input on M's diagonal. Sums and differences of L are taken
 // in 64 bits, so a strong decay early in a chunk costs the later ones nothing.
 //
-// A wave owns 16 CT rows of S (columns of X) of one head and keeps them in its
+// A wave owns 16 rows of S (columns of X) of one head and keeps them in its
 // accumulators from chunk to chunk; as they leave one product they are the
-// operand of the next. Four such waves of one group share the chunk's B and C in
-// LDS, and the c . b of M, which each head in the workgroup turns into its own M.
+// operand of the next. The waves of a workgroup (eight in bf16, four in fp32)
+// are of one group and share the chunk's B and C in LDS, and the c . b of M,
+// which each head in the workgroup turns into its own M.
 //
 // Long sequences are cut into segments of `seg` tokens where there are too few
 // heads to fill the chip: a first kernel makes the state that each segment but
 // a sequence's last leaves of nothing (the first one's: of the sequence's own
-// state), the second one puts together the state before its segment from those
-// of the segments before it.
+// state), the last one goes over all segments and puts together the state before
+// each from those of the segments before it. Where these may be more than
+// FOLDED a kernel between the two has done that.
 //
 // Precision: bf16 operands (B, C, X) are exact; every other operand (S, M, X
 // with its factors) and each fp32 one is split into three bf16 parts, x = hi +
@@ -49,6 +51,10 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int Q = 64;                   // tokens of a chunk
+constexpr int NT_JOIN = 256;
+// Segments of a sequence whose states the last kernel puts together by itself: of 6 sequences of 4095 tokens together,
+// 16 segments, it takes 97 us where a kernel of its own for that makes it 114 us, of 8192 tokens of 128 heads 271 and 278.
+constexpr int FOLDED = 16;
 constexpr int NEVER = 0x7fffffff;
 constexpr int FRAG = 1024;              // 64 lanes x 16 bytes
 constexpr int MFRAGS = 6;               // 16 x 32 blocks of a lower triangle of 64
@@ -59,10 +65,11 @@ struct HeadsArgs {
     float *decays;          // ... and its decay for each head
     int seg;                // tokens of a segment
     int units;              // segment numbers x groups
-    int slices;             // slices of 16 CT columns a head
+    int slices;             // slices of 16 columns a head
     int jobs;               // slices that a workgroup takes (waves past them help with what is shared)
     int wgs;                // workgroups of a segment and group
     int heads;              // most heads a workgroup's jobs belong to
+    bool joined;            // the state before each segment is there, not what each one leaves
 };
 
 // What a chunk's exponents come to for one head: what M needs, and what the
@@ -168,10 +175,10 @@ __device__ __forceinline__ uint32_t not_finite(const u32x4 &v)
            (F32 ? 0x80000000u : 0x80008000u);
 }
 
-// KN steps of 32 states (N up to 32 KN), CT tiles of 16 columns a wave.
+// KN steps of 32 states (N up to 32 KN), CW columns a wave.
 // FULL: outputs and final states; else the states that segments leave. VEC:
 // 16-byte pieces of x, b, c and gate, and of states (a host rule).
-template <class T, int KN, int CT, int WAVES, bool FULL, bool VEC>
+template <class T, int KN, int WAVES, bool FULL, bool VEC>
 struct Chunks {
     static constexpr int NT = 64 * WAVES;
     static constexpr bool F32 = std::is_same<T, float>::value;
@@ -179,7 +186,7 @@ struct Chunks {
     static constexpr int E = 16 / sizeof(T);        // values of a piece
     static constexpr int NP = 32 * KN, RC = 4 * KN; // states of a row in LDS, in pieces of eight
     static constexpr int PB = Q * NP / E / NT;      // pieces of B, and of C, a thread
-    static constexpr int CW = 16 * CT;              // columns of a wave
+    static constexpr int CW = 16;                   // columns of a wave
     static constexpr int PX = Q * CW / E / 64;      // pieces of X a lane
     // LDS: B, C (each XP parts), then X of each wave (XP parts) which M takes the place of, then the factors and notes.
     // Rows of C are a piece longer than their states, so that 16 of them begin in 16 different groups of four banks;
@@ -211,7 +218,7 @@ struct Chunks {
         uint8_t *const after = lds_ + shared_at(a.heads);
         Factors *const factors = reinterpret_cast<Factors *>(after);                    // [heads]
         int *const badcol = reinterpret_cast<int *>(after + a.heads * sizeof(Factors));
-        int *const badb = badcol + WAVES * CW;                                           // [2]
+        int *const badb = badcol + WAVES * CW;                                          // [2]
 
         // Workgroup i runs on XCD i % 8: those of one segment and group, which
         // read the same B and C, go to one XCD and meet in its L2.
@@ -273,9 +280,9 @@ struct Chunks {
         const int cols = p.P - col0;                // columns there are, from the wave's first
 
         // The gate (x in its place where there is none) of the columns V g + .. of tokens 16 it + c.
-        constexpr int V = 4 * CT;
+        constexpr int V = 4;
         struct Gate {
-            T v[V] __attribute__((aligned(V * sizeof(T) < 16 ? V * sizeof(T) : 16)));
+            T v[V] __attribute__((aligned(V * sizeof(T))));
         };
         u32x4 bv[PB], cv[FULL ? PB : 1], xv[PX];
         Gate gate[FULL ? 4 : 1];
@@ -393,7 +400,7 @@ struct Chunks {
             }
         };
         // X of the wave's columns through its own part of LDS, as 8 tokens of a column a lane.
-        bf16x8 xf[2][CT][XP];
+        bf16x8 xf[2][XP];
         auto put_x = [&](int ch) __attribute__((always_inline)) {
             const int rows = min(len - ch * Q, Q);
             uint8_t *const own = xm + w * XP * XBYTES;
@@ -420,13 +427,10 @@ struct Chunks {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int i = 0; i < XP; ++i) {
-                        // Tile ct holds columns 8 q + 4 ct + (0 .. 3) (one tile: 4 q + ..), q = c / 4.
-                        const uint8_t *t = own + i * XBYTES + (32 * s + 8 * g + (c >> 2)) * CW * 2 + (c & 3) * 8 * CT + 8 * ct;
-                        xf[s][ct][i] = join(transposed(t), transposed(t + 4 * CW * 2));
-                    }
+                for (int i = 0; i < XP; ++i) {
+                    const uint8_t *t = own + i * XBYTES + (32 * s + 8 * g + (c >> 2)) * CW * 2 + (c & 3) * 8;
+                    xf[s][i] = join(transposed(t), transposed(t + 4 * CW * 2));
+                }
         };
         double exponent = 0.0;      // of the whole segment, in wave w < heads
         auto make_factors = [&](int ch) __attribute__((always_inline)) {
@@ -477,7 +481,7 @@ struct Chunks {
         // ---- The state before the segment. Column p of a tile (of lane c) is
         // row p of S; a lane has 4 rows n of each of 2 KN tiles, which
         // interleave, so that a pair of them is 8 adjacent n.
-        f32x4 S[2 * KN][CT];
+        f32x4 S[2 * KN];
         // each(S, pointer) for what there is of the state at s, by pieces of four. (The lane's number is made anew, or
         // the addresses of the first visit would be kept through the chunks for the last.)
         auto visit = [&](const float *s, int64_t index, auto each) __attribute__((always_inline)) {
@@ -485,16 +489,13 @@ struct Chunks {
             asm volatile("" : "+v"(l));
             const int gg = l >> 4, cc = l & 15;
             const float *base = s + (index * p.H + h) * p.P * p.N;
+            const int row = col0 + cc;
+            if (row < p.P) {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const int row = col0 + (CT == 2 ? 8 * (cc >> 2) + 4 * ct + (cc & 3) : cc);
-                if (row < p.P) {
-#pragma unroll
-                    for (int nt = 0; nt < 2 * KN; ++nt) {
-                        const int n = 32 * (nt >> 1) + 8 * gg + 4 * (nt & 1);
-                        if (n < p.N)
-                            each(S[nt][ct], base + (int64_t)row * p.N + n, p.N - n);
-                    }
+                for (int nt = 0; nt < 2 * KN; ++nt) {
+                    const int n = 32 * (nt >> 1) + 8 * gg + 4 * (nt & 1);
+                    if (n < p.N)
+                        each(S[nt], base + (int64_t)row * p.N + n, p.N - n);
                 }
             }
         };
@@ -526,27 +527,22 @@ struct Chunks {
             });
         };
         // The workspace's states lie as the lanes hold them: whole lines at a time, nothing to compare.
-        auto kept = [&](int k, int nt, int ct) __attribute__((always_inline)) {
-            const int64_t at0 = (((int64_t)k * p.H + h) * a.slices + job % a.slices) * (2 * KN * CT) + nt * CT + ct;
+        auto kept = [&](int k, int nt) __attribute__((always_inline)) {
+            const int64_t at0 = (((int64_t)k * p.H + h) * a.slices + job % a.slices) * (2 * KN) + nt;
             return reinterpret_cast<f32x4 *>(a.states) + at0 * 64 + lane;
         };
         auto keep = [&](int k) __attribute__((always_inline)) {
             if (mine)
 #pragma unroll
                 for (int nt = 0; nt < 2 * KN; ++nt)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-                        *kept(k, nt, ct) = S[nt][ct];
+                    *kept(k, nt) = S[nt];
         };
         const int slot = p.state_in || p.state_out ? seq_slot(p.seq, tile.n) : -1;
-        const int first_number = number - index;
-        const int last_number = first_number + (whole > 0 ? (whole - 1) / a.seg : 0);
+        const int last_number = number - index + (whole > 0 ? (whole - 1) / a.seg : 0);
         bool held = false;          // whether S may hold anything
 #pragma unroll
         for (int nt = 0; nt < 2 * KN; ++nt)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-                S[nt][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+            S[nt] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (index == 0 && (!FULL || last)) {
             if (p.state_in && slot >= 0) {
                 held = true;
@@ -554,31 +550,27 @@ struct Chunks {
                     v = read4(s, left);
                 });
             }
-            // A sequence of several segments: what its last one may overwrite
-            // before its first one has read it is kept in the place of the
-            // state that the last one does not leave.
+            // A sequence of several segments: its own state, which the call may
+            // overwrite, is kept in the place of the one that the last segment
+            // does not leave.
             if (!FULL)
                 keep(last_number);
         } else if (FULL) {
             held = true;
-            const int from = index == 0 ? last_number : first_number;
+            const int from = a.joined ? number : index == 0 ? last_number : number - index;
 #pragma unroll
             for (int nt = 0; nt < 2 * KN; ++nt)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    S[nt][ct] = *kept(from, nt, ct);
+                S[nt] = *kept(from, nt);
 #pragma unroll 2
-            for (int k = first_number + 1; k < number; ++k) {
+            for (int k = a.joined ? number : number - index + 1; k < number; ++k) {
                 const float by = a.decays[(int64_t)k * p.H + h];
 #pragma unroll
-                for (int nt = 0; nt < 2 * KN; ++nt)
+                for (int nt = 0; nt < 2 * KN; ++nt) {
+                    const f32x4 v = *kept(k, nt);
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        const f32x4 v = *kept(k, nt, ct);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            S[nt][ct][e] = fmaf(by, S[nt][ct][e], v[e]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        S[nt][e] = fmaf(by, S[nt][e], v[e]);
+                }
             }
         }
 
@@ -611,7 +603,7 @@ struct Chunks {
             lds_barrier();
             if (tid == 0)
                 badb[(ch + 1) & 1] = NEVER;     // last read before the barrier that ended the chunk before
-            f32x4 acc[4][CT];
+            f32x4 acc[4];
             if constexpr (FULL) {
                 // M^T's blocks: tokens i of tile `it` as columns, 32 tokens j of step s as rows, two interleaving
                 // tiles, so that a lane has 8 adjacent j of one i: an operand of the product with X.
@@ -671,31 +663,24 @@ struct Chunks {
                 // Y^T: S C^T.
 #pragma unroll
                 for (int it = 0; it < 4; ++it)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-                        acc[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    acc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
                 if (held) {
                     const uint8_t *const c0 = cs + c_place(c, g);
 #pragma unroll
                     for (int ks = 0; ks < KN; ++ks) {
-                        bf16x8 sp[CT][3];
+                        bf16x8 sp[3];
+                        float v[8];
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) {
-                            float v[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                v[e] = S[2 * ks + (e >> 2)][ct][e & 3];
-                            split8(v, sp[ct]);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = S[2 * ks + (e >> 2)][e & 3];
+                        split8(v, sp);
 #pragma unroll
                         for (int it = 0; it < 4; ++it) {
                             bf16x8 cf[XP];
 #pragma unroll
                             for (int i = 0; i < XP; ++i)
                                 cf[i] = *reinterpret_cast<const bf16x8 *>(c0 + i * CBYTES + c_place(16 * it, 4 * ks));
-#pragma unroll
-                            for (int ct = 0; ct < CT; ++ct)
-                                acc[it][ct] = product(sp[ct], cf, acc[it][ct]);
+                            acc[it] = product(sp, cf, acc[it]);
                         }
                     }
                 }
@@ -711,9 +696,7 @@ struct Chunks {
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
                     const float up = f.up[16 * it + c];
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-                        acc[it][ct] *= up;
+                    acc[it] *= up;
 #pragma unroll
                     for (int s = 0; s <= it >> 1; ++s) {
                         // Block (it, s) is number 0 1 2 4 for (1,0) (2,0) (3,0) (3,1), 3 for (0,0) and 5 for (2,1).
@@ -722,9 +705,7 @@ struct Chunks {
 #pragma unroll
                         for (int i = 0; i < 3; ++i)
                             mf[i] = *reinterpret_cast<const bf16x8 *>(ms + (fr * 3 + i) * FRAG);
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
-                            acc[it][ct] = product(xf[s][ct], mf, acc[it][ct]);
+                        acc[it] = product(xf[s], mf, acc[it]);
                     }
                 }
                 if (p.gate) {
@@ -732,7 +713,7 @@ struct Chunks {
                     for (int it = 0; it < 4; ++it)
 #pragma unroll
                         for (int e = 0; e < V; ++e)
-                            acc[it][e >> 2][e & 3] *= silu(load_as_f32(&gate[it].v[e]));
+                            acc[it][e] *= silu(load_as_f32(&gate[it].v[e]));
                 }
                 if (bad) {
 #pragma unroll
@@ -740,7 +721,7 @@ struct Chunks {
 #pragma unroll
                         for (int e = 0; e < V; ++e)
                             if (16 * it + c >= min(bad_all, badcol[w * CW + V * g + e]))
-                                acc[it][e >> 2][e & 3] = NAN;
+                                acc[it][e] = NAN;
                 }
                 T *yb = yp + (int64_t)ch * Q * p.yst;
                 const auto yr = view(yb, p.yst, mine ? rows : 1, mine ? cols : 0);
@@ -751,7 +732,7 @@ struct Chunks {
                     Gate o;
 #pragma unroll
                     for (int e = 0; e < V; ++e)
-                        store_rne(&o.v[e], acc[it][e >> 2][e & 3]);
+                        store_rne(&o.v[e], acc[it][e]);
                     const int t = 16 * it + c;
                     if constexpr (VEC) {
                         const uint32_t at0 = yo + it * (16 * (int)sizeof(T)) * (int)p.yst;
@@ -776,24 +757,19 @@ struct Chunks {
             const uint8_t *const b0 = bs + b_place(8 * g + (c >> 2), c & 3);
 #pragma unroll
             for (int nt = 0; nt < 2 * KN; ++nt)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    S[nt][ct] = held ? S[nt][ct] * total : S[nt][ct];
+                S[nt] = held ? S[nt] * total : S[nt];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                bf16x8 xw[CT][3];
+                bf16x8 xw[3];
+                float v[8];
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float x = (float)xf[s][ct][0][e];
-                        if constexpr (F32)
-                            x = x + (float)xf[s][ct][1][e] + (float)xf[s][ct][2][e];
-                        v[e] = x * f.tail[32 * s + 8 * g + e];
-                    }
-                    split8(v, xw[ct]);
+                for (int e = 0; e < 8; ++e) {
+                    float x = (float)xf[s][0][e];
+                    if constexpr (F32)
+                        x = x + (float)xf[s][1][e] + (float)xf[s][2][e];
+                    v[e] = x * f.tail[32 * s + 8 * g + e];
                 }
+                split8(v, xw);
 #pragma unroll
                 for (int nt = 0; nt < 2 * KN; ++nt) {
                     // The next chunk's loads, spread over these products.
@@ -807,19 +783,15 @@ struct Chunks {
                         const uint8_t *const at0 = b0 + i * BBYTES + b_place(32 * s, 4 * (nt >> 1)) + 8 * (nt & 1);
                         bt[i] = join(transposed(at0), transposed(at0 + b_place(4, 0)));
                     }
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
-                        S[nt][ct] = product(bt, xw[ct], S[nt][ct]);
+                    S[nt] = product(bt, xw, S[nt]);
                 }
             }
             held = true;
             if (bad) {
+                if (bad_all != NEVER || badcol[w * CW + c] != NEVER)
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    if (bad_all != NEVER || badcol[w * CW + (CT == 2 ? 8 * (c >> 2) + 4 * ct + (c & 3) : c)] != NEVER)
-#pragma unroll
-                        for (int nt = 0; nt < 2 * KN; ++nt)
-                            S[nt][ct] = f32x4{NAN, NAN, NAN, NAN};
+                    for (int nt = 0; nt < 2 * KN; ++nt)
+                        S[nt] = f32x4{NAN, NAN, NAN, NAN};
                 if (lane < CW)
                     badcol[w * CW + lane] = NEVER;
             }
@@ -844,7 +816,46 @@ template <class T, int KN, bool FULL, bool VEC>
 __global__ __launch_bounds__(64 * WAVES<T>)
     __attribute__((amdgpu_waves_per_eu(std::is_same<T, float>::value ? 1 : KN > 4 ? 2 : 4))) void heads_chunk_kernel(HeadsArgs a)
 {
-    Chunks<T, KN, 1, WAVES<T>, FULL, VEC>::run(a);
+    Chunks<T, KN, WAVES<T>, FULL, VEC>::run(a);
+}
+
+// From the states that segments leave to those before them, along each sequence
+// of several segments: a thread takes four states of one lane of the kernels
+// above, four segments at a time.
+__global__ __launch_bounds__(NT_JOIN) void heads_join_kernel(HeadsArgs a, int per_head)
+{
+    const int64_t per = (int64_t)a.p.H * per_head;
+    const int64_t i = (int64_t)blockIdx.x * NT_JOIN + threadIdx.x;
+    if (i >= per)
+        return;
+    const int h = (int)(i / per_head);
+    f32x4 *const states = reinterpret_cast<f32x4 *>(a.states) + i;
+    for (int n = blockIdx.y; n < a.p.seq.num_seqs; n += gridDim.y) {
+        const int64_t begin = seq_begin(a.p.seq, n), len = seq_begin(a.p.seq, n + 1) - begin;
+        if (len <= a.seg)
+            continue;
+        const int64_t first = begin / a.seg + n, last = first + (len - 1) / a.seg;
+        f32x4 v = states[first * per];
+        states[first * per] = states[last * per];       // the sequence's own state
+        for (int64_t k = first + 1; k <= last; k += 4) {
+            f32x4 add[4];
+            float by[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t at = k + j < last ? k + j : last;
+                add[j] = states[at * per];
+                by[j] = a.decays[at * a.p.H + h];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (k + j <= last) {
+                    states[(k + j) * per] = v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = fmaf(by[j], v[e], add[j][e]);
+                }
+        }
+    }
 }
 
 constexpr int LDS_MOST = 160 * 1024;
@@ -854,6 +865,7 @@ struct Plan {
     int kn, slices, jobs, wgs, heads, seg;
     int64_t numbers;        // segments, numbered as in sequences.h
     bool parts;             // segments are shorter than a sequence may be
+    bool joined;            // a sequence may have more than FOLDED of them
 };
 
 // Heads that `jobs` slices in a row may belong to, as a power of two.
@@ -869,11 +881,11 @@ int most_heads(int jobs, int slices)
 int lds_bytes(bool f32, int kn, int heads)
 {
     if (f32)
-        return kn == 2 ? Chunks<float, 2, 1, WAVES<float>, true, true>::lds(heads)
-                       : Chunks<float, 4, 1, WAVES<float>, true, true>::lds(heads);
-    return kn == 2   ? Chunks<uint16_t, 2, 1, WAVES<uint16_t>, true, true>::lds(heads)
-           : kn == 4 ? Chunks<uint16_t, 4, 1, WAVES<uint16_t>, true, true>::lds(heads)
-                     : Chunks<uint16_t, 8, 1, WAVES<uint16_t>, true, true>::lds(heads);
+        return kn == 2 ? Chunks<float, 2, WAVES<float>, true, true>::lds(heads)
+                       : Chunks<float, 4, WAVES<float>, true, true>::lds(heads);
+    return kn == 2   ? Chunks<uint16_t, 2, WAVES<uint16_t>, true, true>::lds(heads)
+           : kn == 4 ? Chunks<uint16_t, 4, WAVES<uint16_t>, true, true>::lds(heads)
+                     : Chunks<uint16_t, 8, WAVES<uint16_t>, true, true>::lds(heads);
 }
 
 bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype dtype, Plan *l)
@@ -893,14 +905,15 @@ bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype d
     if (group_jobs > (1 << 22))
         return false;
     l->wgs = (int)((group_jobs + l->jobs - 1) / l->jobs);
-    // Segments such that some 512 workgroups have one, but at most 16 to the longest sequence there can be (a
-    // segment reads the states of all before it), and none of less than 256 tokens.
+    // Segments such that some 512 workgroups have one, but at most 64 to the longest sequence there can be, and none
+    // of less than 256 tokens. (16384 tokens of 32 heads in 64 segments: 123 us, in 16: 150.)
     const int64_t longest = s.offsets ? s.tokens : s.each;
     int64_t seg = s.tokens * l->wgs * groups / 512;
-    seg = seg > longest / 16 ? seg : longest / 16;
+    seg = seg > longest / 64 ? seg : longest / 64;
     seg = seg > 256 ? seg : 256;
     seg = (seg + Q - 1) / Q * Q;
     l->parts = seg < longest;
+    l->joined = (longest + seg - 1) / seg > FOLDED;
     if (!l->parts)
         seg = (longest + Q) / Q * Q;
     if (seg > (1 << 30))
@@ -937,7 +950,7 @@ hipError_t launch_pass(const HeadsArgs &a, hipStream_t s)
     if (e != hipSuccess)
         return e;
     hipLaunchKernelGGL((heads_chunk_kernel<T, KN, FULL, VEC>), dim3((unsigned)((a.units + 7) / 8 * 8 * a.wgs)),
-                       dim3(64 * WAVES<T>), (Chunks<T, KN, 1, WAVES<T>, FULL, VEC>::lds(a.heads)), s, a);
+                       dim3(64 * WAVES<T>), (Chunks<T, KN, WAVES<T>, FULL, VEC>::lds(a.heads)), s, a);
     return hipGetLastError();
 }
 
@@ -946,6 +959,15 @@ hipError_t launch(const HeadsArgs &a, bool parts, bool vec, hipStream_t s)
 {
     if (parts) {
         const hipError_t e = vec ? launch_pass<T, KN, false, true>(a, s) : launch_pass<T, KN, false, false>(a, s);
+        if (e != hipSuccess)
+            return e;
+    }
+    if (a.joined) {
+        const int per_head = a.slices * 2 * KN * 64;
+        const int64_t blocks = ((int64_t)a.p.H * per_head + NT_JOIN - 1) / NT_JOIN;
+        const int seqs = a.p.seq.num_seqs < 64 ? a.p.seq.num_seqs : 64;
+        hipLaunchKernelGGL(heads_join_kernel, dim3((unsigned)blocks, (unsigned)seqs), dim3(NT_JOIN), 0, s, a, per_head);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
     }
@@ -984,6 +1006,7 @@ hipError_t launch_heads_chunked(const HeadScanProblem &p, hipStream_t s)
     a.jobs = l.jobs;
     a.wgs = l.wgs;
     a.heads = l.heads;
+    a.joined = l.joined;
     const int64_t e = p.dtype == CONV_F32 ? 4 : 2;
     const uintptr_t strides = (uintptr_t)((p.xst | p.xsh | p.yst | p.ysh | p.bst | p.bsg | p.cst | p.csg) * e) |
                               (p.gate ? (uintptr_t)((p.gst | p.gsh) * e) : 0);
