@@ -29,7 +29,7 @@
 // Values that are not finite: a zero of M times a NaN would carry it to earlier
 // tokens. So values of X, B and the step sizes that are not finite are read as
 // zeros and their token is noted; outputs from it on, and the state, are set to
-// NaN: a row of a head (X), a head (the step size) or a group (B).
+// NaN: a row of a head (X), a head (the step size or the exponent) or a group (B).
 #include <type_traits>
 
 #include "common.h"
@@ -84,7 +84,7 @@ struct __align__(16) Factors {
         float tail[Q];      // 2^(L_63 - L) d
         float total;        // 2^L_63
         int wide;           // row and col may leave fp32's range
-        int bad;            // first token whose step is not finite
+        int bad;            // first token whose step is not finite, or its exponent no number
     } of[2];
 };
 
@@ -348,18 +348,21 @@ struct Chunks {
             const int64_t t = min(ch * Q + lane, len - 1);
             dv = dp[t * p.dts];
         };
-        // A piece's parts into LDS: in bf16 the piece itself, in fp32 half a piece of each part.
+        // A piece's parts into LDS: in bf16 the piece itself, in fp32 half a piece of each part (cut as in split8;
+        // rounded, values next to fp32's largest would leave bf16's range).
         auto put = [&](uint8_t *at16, int part_bytes, const u32x4 &v, int half) __attribute__((always_inline)) {
             if constexpr (F32) {
-                const f32x4 f = __builtin_bit_cast(f32x4, v);
-                f32x4 left = f;
+                f32x4 left = __builtin_bit_cast(f32x4, v);
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
-                    const bf16x4 t = __builtin_convertvector(left, bf16x4);
-                    *reinterpret_cast<bf16x4 *>(at16 + i * part_bytes + 8 * half) = t;
+                    u32x2 t;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        t[e] = __builtin_amdgcn_perm(__float_as_uint(left[2 * e + 1]), __float_as_uint(left[2 * e]), 0x07060302u);
+                    *reinterpret_cast<u32x2 *>(at16 + i * part_bytes + 8 * half) = t;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        left[e] -= (float)t[e];
+                        left[e] -= __uint_as_float(__float_as_uint(left[e]) & 0xffff0000u);
                 }
             } else {
                 *reinterpret_cast<u32x4 *>(at16) = v;
@@ -440,9 +443,10 @@ struct Chunks {
             auto &of = f.of[ch & 1];
             float d = step_size(load_as_f32(&dv) + bias, p.softplus);
             // Exponents past +-10000 are 0 and infinity either way.
-            double e = fmin(fmax((double)d * rate, -1e4), 1e4);
+            double e = (double)d * rate;
             const bool here = lane < len - ch * Q;
-            const bool bad = here && !(fabsf(d) < INFINITY);
+            const bool bad = here && (!(fabsf(d) < INFINITY) || e != e);
+            e = fmin(fmax(e, -1e4), 1e4);
             const uint64_t bads = __ballot(bad);
             if (!here || bad) {
                 d = 0.f;
