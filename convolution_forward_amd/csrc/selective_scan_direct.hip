@@ -3,14 +3,17 @@
 //   d = step(dt + bias);  h[n] = exp(d a[c,n]) h[n] + d x b[n]
 //   y = (sum_n c[n] h[n] + skip x) silu(gate)
 //
-// A lane holds four states of one channel, LN lanes a channel (four times LN
-// covers the states), a wave 64 / LN neighbouring channels: its states are
-// one run of memory, and y is an exchange between LN lanes. No wave waits for
-// another.
+// A lane holds four states of one channel or two, LN lanes a channel (four times
+// LN covers the states), a wave 64 / LN neighbouring channels or twice as many:
+// its states are one run of memory, and y is an exchange between LN lanes. No
+// wave waits for another.
 //
-// Single tokens: the states' bytes are the time, each read and written once.
+// Single tokens: the states' bytes are the time, each read and written once. 64
+// sequences of 8192 channels of 16 states, bf16: 16.5 us, 4.3 TB/s, where the
+// states lie in the last cache, and 18 where they do not; 256: 61 us, 4.4 TB/s;
+// one: 3 us, a launch.
 // Longer sequences are the chain from token to token; the next token's inputs
-// are loaded a token ahead.
+// are loaded a token ahead (64 of 8 tokens: 41 us).
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"
@@ -21,71 +24,84 @@
 namespace convfwd {
 namespace {
 
-// One token's inputs as they lie in memory.
-template <class T>
+// One token's inputs as they lie in memory, R channels a lane.
+template <class T, int R>
 struct Token {
     T b[4] __attribute__((aligned(16))), c[4] __attribute__((aligned(16)));
-    T x, dt, gate;
+    T x[R], dt[R], gate[R];
 };
 
-// WIDE: states, b and c allow pieces of four (a host rule).
-template <class T, int LN, bool WIDE>
+// WIDE: states, b and c allow pieces of four, which R = 2 needs, as well as groups of whole slices (a host rule).
+template <class T, int LN, int R, bool WIDE>
 __global__ __launch_bounds__(256) void scan_direct_kernel(ScanProblem p, int slices)
 {
     constexpr int CH = 64 / LN;
     const int lane = threadIdx.x & 63;
-    const int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
-    const int n = (int)(job / slices);
+    // (The same in all lanes, which the compiler has to be told; below 2^26.)
+    const uint32_t job = __builtin_amdgcn_readfirstlane(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6));
+    const int n = (int)(job / (uint32_t)slices);
     if (n >= p.seq.num_seqs)
         return;
-    const int c = (int)(job % slices) * CH + lane / LN, at = 4 * (lane % LN);
-    const bool live = c < p.channels;       // lanes past the channels take the last one's inputs and store nothing
-    const int ch = live ? c : p.channels - 1;
-    const int group = ch / (p.channels / p.groups);
+    const int c0 = (int)(job % (uint32_t)slices) * CH * R + lane / LN, at = 4 * (lane % LN);
     const int64_t begin = seq_begin(p.seq, n), end = seq_begin(p.seq, n + 1);
     const int slot = p.state_in || p.state_out ? seq_slot(p.seq, n) : -1;
-    const int64_t sat = ((int64_t)slot * p.channels + ch) * p.N + at;
 
-    float h[4], a[4];
-    const float *ap = p.a + (int64_t)ch * p.N + at;
-    const bool held = p.state_in && slot >= 0;
+    int ch[R];              // lanes past the channels take the last one's inputs and store nothing
+    bool live[R];
+    float h[R][4], a[R][4], skip[R], bias[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        h[i] = a[i] = 0.f;
-    if constexpr (WIDE) {
-        if (at < p.N) {
-            const float4 v = *reinterpret_cast<const float4 *>(ap);
-            a[0] = v.x, a[1] = v.y, a[2] = v.z, a[3] = v.w;
-            if (held) {
-                const float4 s = *reinterpret_cast<const float4 *>(p.state_in + sat);
-                h[0] = s.x, h[1] = s.y, h[2] = s.z, h[3] = s.w;
+    for (int j = 0; j < R; ++j) {
+        live[j] = c0 + j * CH < p.channels;
+        ch[j] = live[j] ? c0 + j * CH : p.channels - 1;
+    }
+    int group = ch[0] / (p.channels / p.groups);
+    if constexpr (R == 2)
+        group = __builtin_amdgcn_readfirstlane(group);
+    auto four = [&](float (&v)[4], const float *s) __attribute__((always_inline)) {
+        if constexpr (WIDE) {
+            if (at < p.N) {
+                const float4 f = *reinterpret_cast<const float4 *>(s);
+                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (at + i < p.N)
+                    v[i] = s[i];
         }
-    } else {
+    };
+    auto place = [&](int j) __attribute__((always_inline)) { return (int64_t)ch[j] * p.N + at; };
+    const int64_t sat = (int64_t)slot * p.channels * p.N;
+#pragma unroll
+    for (int j = 0; j < R; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (at + i < p.N) {
-                a[i] = ap[i];
-                if (held)
-                    h[i] = p.state_in[sat + i];
-            }
-    }
+            h[j][i] = a[j][i] = 0.f;
+    if (p.state_in && slot >= 0)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        a[i] *= LOG2E;
-    const float skip = p.skip ? p.skip[ch] : 0.f, bias = p.bias ? p.bias[ch] : 0.f;
-    const T *xp = static_cast<const T *>(p.x) + begin * p.xs + ch;
-    const T *dp = static_cast<const T *>(p.dt) + begin * p.dts + ch;
-    const T *gp = p.gate ? static_cast<const T *>(p.gate) + begin * p.gs + ch : nullptr;
+        for (int j = 0; j < R; ++j)
+            four(h[j], p.state_in + sat + place(j));
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        four(a[j], p.a + place(j));
+        skip[j] = p.skip ? p.skip[ch[j]] : 0.f;
+        bias[j] = p.bias ? p.bias[ch[j]] : 0.f;
+    }
+    const T *xp = static_cast<const T *>(p.x) + begin * p.xs;
+    const T *dp = static_cast<const T *>(p.dt) + begin * p.dts;
+    const T *gp = p.gate ? static_cast<const T *>(p.gate) + begin * p.gs : nullptr;
     const T *bp = static_cast<const T *>(p.b) + begin * p.bst + group * p.bsg;
     const T *cp = static_cast<const T *>(p.c) + begin * p.cst + group * p.csg;
-    T *yp = static_cast<T *>(p.y) + begin * p.ys + ch;
+    T *yp = static_cast<T *>(p.y) + begin * p.ys;
 
-    auto load = [&](Token<T> &t) __attribute__((always_inline)) {
-        t.x = *xp;
-        t.dt = *dp;
-        if (gp)
-            t.gate = *gp;
+    auto load = [&](Token<T, R> &t) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            t.x[j] = xp[ch[j]];
+            t.dt[j] = dp[ch[j]];
+            if (gp)
+                t.gate[j] = gp[ch[j]];
+        }
         if constexpr (WIDE) {
             const int n0 = at < p.N ? at : 0;
             __builtin_memcpy(t.b, __builtin_assume_aligned(bp + n0, 4 * sizeof(T)), sizeof(t.b));
@@ -107,29 +123,32 @@ __global__ __launch_bounds__(256) void scan_direct_kernel(ScanProblem p, int sli
         bp += p.bst;
         cp += p.cst;
     };
-    auto step = [&](const Token<T> &t) __attribute__((always_inline)) {
-        const float x = load_as_f32(&t.x);
-        const float d = step_size(load_as_f32(&t.dt) + bias, p.softplus);
-        const float dx = d * x;
-        float y = 0.f;
+    auto step = [&](const Token<T, R> &t) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool in = WIDE ? at < p.N : at + i < p.N;
-            // States past the last one stay zeros, whatever x is.
-            h[i] = in ? fmaf(__builtin_amdgcn_exp2f(d * a[i]), h[i], dx * load_as_f32(&t.b[i])) : 0.f;
-            y = in ? fmaf(h[i], load_as_f32(&t.c[i]), y) : y;
+        for (int j = 0; j < R; ++j) {
+            const float x = load_as_f32(&t.x[j]);
+            const float d = step_size(load_as_f32(&t.dt[j]) + bias[j], p.softplus);
+            const float dx = d * x;
+            float y = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool in = WIDE ? at < p.N : at + i < p.N;
+                // States past the last one stay zeros, whatever x is.
+                h[j][i] = in ? fmaf(__builtin_amdgcn_exp2f(d * (a[j][i] * LOG2E)), h[j][i], dx * load_as_f32(&t.b[i])) : 0.f;
+                y = in ? fmaf(h[j][i], load_as_f32(&t.c[i]), y) : y;
+            }
+            y = lanes_sum<LN>(y);
+            y = fmaf(skip[j], x, y);
+            if (gp)
+                y *= silu(load_as_f32(&t.gate[j]));
+            if (live[j] && at == 0)
+                store_rne(yp + ch[j], y);
         }
-        y = lanes_sum<LN>(y);
-        y = fmaf(skip, x, y);
-        if (gp)
-            y *= silu(load_as_f32(&t.gate));
-        if (live && at == 0)
-            store_rne(yp, y);
         yp += p.ys;
     };
     int64_t left = end - begin;
     if (left > 0) {
-        Token<T> t0, t1;
+        Token<T, R> t0, t1;
         load(t0);
         for (; left > 2; left -= 2) {
             advance();
@@ -148,15 +167,21 @@ __global__ __launch_bounds__(256) void scan_direct_kernel(ScanProblem p, int sli
             step(t0);
         }
     }
-    if (p.state_out && slot >= 0 && live) {
-        if constexpr (WIDE) {
-            if (at < p.N)
-                *reinterpret_cast<float4 *>(p.state_out + sat) = make_float4(h[0], h[1], h[2], h[3]);
-        } else {
+    if (p.state_out && slot >= 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (at + i < p.N)
-                    p.state_out[sat + i] = h[i];
+        for (int j = 0; j < R; ++j) {
+            float *const to = p.state_out + sat + place(j);
+            if (!live[j])
+                continue;
+            if constexpr (WIDE) {
+                if (at < p.N)
+                    *reinterpret_cast<float4 *>(to) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (at + i < p.N)
+                        to[i] = h[j][i];
+            }
         }
     }
 }
@@ -172,16 +197,28 @@ int lanes_for(int N)
 template <class T, int LN>
 void launch_lanes(const ScanProblem &p, hipStream_t s)
 {
-    const int slices = (p.channels + 64 / LN - 1) / (64 / LN);
-    const int64_t jobs = (int64_t)p.seq.num_seqs * slices;
-    const int waves = jobs <= 1024 ? 1 : 4;     // few waves: one a workgroup, so that they spread over the compute units
-    const dim3 grid((unsigned)((jobs + waves - 1) / waves)), block(64 * waves);
+    constexpr int CH = 64 / LN;
     const uintptr_t bc = (uintptr_t)p.b | (uintptr_t)p.c | (uintptr_t)((p.bst | p.bsg | p.cst | p.csg) * (int64_t)sizeof(T));
     const uintptr_t st = (uintptr_t)p.state_in | (uintptr_t)p.state_out | (uintptr_t)p.a;
-    if (bc % (4 * sizeof(T)) == 0 && st % 16 == 0 && p.N % 4 == 0)
-        hipLaunchKernelGGL((scan_direct_kernel<T, LN, true>), grid, block, 0, s, p, slices);
+    const bool wide = bc % (4 * sizeof(T)) == 0 && st % 16 == 0 && p.N % 4 == 0;
+    int slices = (p.channels + CH - 1) / CH;
+    int64_t jobs = (int64_t)p.seq.num_seqs * slices;
+    // Two channels a lane from 8192 waves on, as many as run at once: a single token of 8192 channels of 16 states in 256
+    // sequences takes 61 us (one a lane: 73), in 64 18.2 (20.3), in 16 6.7 (7.4), but in 4 3.8 (3.3). Four take 73 us in
+    // 256: 157 registers.
+    const bool two = wide && jobs >= 8192 && p.channels / p.groups % (2 * CH) == 0;
+    if (two) {
+        slices /= 2;
+        jobs /= 2;
+    }
+    const int waves = jobs <= 1024 ? 1 : 4;     // few waves: one a workgroup, so that they spread over the compute units
+    const dim3 grid((unsigned)((jobs + waves - 1) / waves)), block(64 * waves);
+    if (two)
+        hipLaunchKernelGGL((scan_direct_kernel<T, LN, 2, true>), grid, block, 0, s, p, slices);
+    else if (wide)
+        hipLaunchKernelGGL((scan_direct_kernel<T, LN, 1, true>), grid, block, 0, s, p, slices);
     else
-        hipLaunchKernelGGL((scan_direct_kernel<T, LN, false>), grid, block, 0, s, p, slices);
+        hipLaunchKernelGGL((scan_direct_kernel<T, LN, 1, false>), grid, block, 0, s, p, slices);
 }
 
 template <class T>

@@ -33,10 +33,10 @@ __global__ __launch_bounds__(256) void heads_direct_kernel(HeadScanProblem p, in
 {
     const int lane = threadIdx.x & 63;
     const int row = lane >> 3, at = 4 * (lane & 7);
-    const int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
-    const int slice = (int)(job % slices);
-    const int64_t nh = job / slices;
-    const int n = (int)(nh / p.H), h = (int)(nh % p.H);
+    // (The same in all lanes, which the compiler has to be told; below 2^26.)
+    const uint32_t job = __builtin_amdgcn_readfirstlane(blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6));
+    const uint32_t nh = job / (uint32_t)slices;
+    const int slice = (int)(job % (uint32_t)slices), n = (int)(nh / (uint32_t)p.H), h = (int)(nh % (uint32_t)p.H);
     if (n >= p.seq.num_seqs)
         return;
     const int group = h / (p.H / p.groups);
