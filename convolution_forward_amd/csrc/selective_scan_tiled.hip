@@ -26,6 +26,8 @@
 // one begins with the state put together from those before its segment. The
 // first segment's initial state is kept in the place of the last one's, which
 // leaves none, since the call may overwrite it in place.
+#include <float.h>
+
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"
@@ -168,7 +170,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
         }
         return v;
     };
-    const f32x4 rate = four(p.a + sat) * LOG2E;
+    // (A rate of minus infinity, a state forgotten at each token, as the lowest number: times the zero step of a token that
+    // is not there it has to be zero.)
+    f32x4 rate = four(p.a + sat) * LOG2E;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        rate[i] = rate[i] < -FLT_MAX ? -FLT_MAX : rate[i];
     const int64_t state_size = (int64_t)p.channels * p.N;
     const int slot = p.state_in || p.state_out ? seq_slot(p.seq, tile.n) : -1;
     auto kept = [&](f32x4 *base, int k) { return base + ((int64_t)k * a.slices + slice) * 64 + lane; };

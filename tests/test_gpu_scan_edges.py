@@ -195,6 +195,22 @@ def test_decay_that_is_no_number(variant):
 
 @BOTH
 @pytest.mark.parametrize("variant", [DIRECT, TILED])
+def test_decay_without_memory(which, variant):
+    """A rate of minus infinity forgets the state at every token; one at which nothing of it is left gives the same."""
+    fn, ins, shape, _ = case(which, 701)
+    ins = list(ins)
+    lens, st = [70, 1, 630], rnd((3,) + shape, 69)
+    ins[2] = ins[2].clone()
+    both = []
+    for rate in (-float("inf"), -1e30):
+        ins[2][1] = rate
+        both.append(run(fn, ins, lens, st, variant))
+    assert torch.equal(both[0][0], both[1][0]) and torch.equal(both[0][1], both[1][1])
+    assert torch.isfinite(both[0][0]).all() and torch.isfinite(both[0][1]).all()
+
+
+@BOTH
+@pytest.mark.parametrize("variant", [DIRECT, TILED])
 def test_values_at_the_end_of_32_bits(which, variant):
     """The largest finite inputs under steps that make them small."""
     fn, ins, shape, _ = case(which, 70, F32)
