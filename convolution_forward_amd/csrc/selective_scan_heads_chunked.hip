@@ -26,6 +26,11 @@
 // mid + lo, 24 bits together, and the products of parts above 2^-24 are added
 // in fp32: three for an exact operand times a split one, six for two split ones.
 //
+// 8192 tokens of 128 heads of 64 x 128 in 8 groups, bf16: 266 to 278 us, 1.65
+// TB/s, a quarter of it the first kernel. The matrix instructions of
+// both, counting the products of parts, are 148 us at a large product's rate;
+// beside them the splits, two barriers a chunk and the exchange through LDS.
+//
 // Values that are not finite: a zero of M times a NaN would carry it to earlier
 // tokens. So values of X, B and the step sizes that are not finite are read as
 // zeros and their token is noted; outputs from it on, and the state, are set to

@@ -26,6 +26,13 @@
 // one begins with the state put together from those before its segment. The
 // first segment's initial state is kept in the place of the last one's, which
 // leaves none, since the call may overwrite it in place.
+//
+// 8192 tokens of 8192 channels of 16 states, bf16: 436 us, 1.24 TB/s; vector
+// instructions bound it. A token of a wave is 256 states: an exponential (8.3
+// clocks a wave), a product by the rate, and twice a product with b and the two
+// or three of the recurrence and y (2.7 each), 97 clocks, and some 60 of step
+// sizes, gates, conversions and exchanges, of 181 it takes at four waves a SIMD.
+// Four waves and tiles of 64 tokens, with the products d x b kept: 513 us.
 #include <float.h>
 
 #include "common.h"
