@@ -914,10 +914,14 @@ bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype d
     if (group_jobs > (1 << 22))
         return false;
     l->wgs = (int)((group_jobs + l->jobs - 1) / l->jobs);
-    // Segments such that some 512 workgroups have one, but at most 64 to the longest sequence there can be, and none
-    // of less than 256 tokens. (16384 tokens of 32 heads in 64 segments: 123 us, in 16: 150.)
+    // No segments where each compute unit has a workgroup without them: one prompt of 4096 tokens of 256 heads of 128 x
+    // 128 (256 workgroups) takes 397 us whole and 421 in two, 4095 tokens of 512 heads of 64 x 128 in six prompts 370 and
+    // 443. Otherwise segments such that some 512 workgroups have one (16384 tokens of 32 heads of 64 x 64: 107 us, with
+    // 256 131, with 1024 117; 8192 tokens of 128 heads of 64 x 128: 241, 287 and 258), but at most 64 to the longest
+    // sequence there can be (the first of these in 16: 150 us against 123), and none of less than 256 tokens.
     const int64_t longest = s.offsets ? s.tokens : s.each;
-    int64_t seg = s.tokens * l->wgs * groups / 512;
+    const int64_t whole = (int64_t)l->wgs * groups;      // workgroups without segments
+    int64_t seg = whole * (s.offsets ? 1 : s.num_seqs) >= 256 ? longest : s.tokens * whole / 512;
     seg = seg > longest / 64 ? seg : longest / 64;
     seg = seg > 256 ? seg : 256;
     seg = (seg + Q - 1) / Q * Q;

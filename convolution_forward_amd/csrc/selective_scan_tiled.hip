@@ -415,10 +415,13 @@ bool make_plan(const Sequences &s, int channels, int groups, int N, Plan *l)
     if ((int64_t)l->group_slices * groups > (1 << 22))
         return false;
     l->slices = l->group_slices * groups;
-    // Segments such that some 512 workgroups have one, but at most 16 to the longest sequence there can be, and none of
+    // No segments where each compute unit has a workgroup without them: one prompt of 8192 tokens and 4096 channels of 16
+    // (256 workgroups) takes 296 us whole and 301 in two, of 6144 channels 432 and 526, 2047 tokens of 4096 channels in
+    // six prompts 70 and 97. Otherwise segments such that some 1024 workgroups have one (2048 channels: 165 us, with 512
+    // 173, whole 289; 1024 channels 90, 92 and 238), but at most 16 to the longest sequence there can be, and none of
     // less than 256 tokens.
     const int64_t longest = s.offsets ? s.tokens : s.each;
-    int64_t seg = s.tokens * l->slices / 512;
+    int64_t seg = (int64_t)l->slices * (s.offsets ? 1 : s.num_seqs) >= 256 ? longest : s.tokens * l->slices / 1024;
     seg = seg > longest / 16 ? seg : longest / 16;
     seg = seg > 256 ? seg : 256;
     seg = (seg + TILE - 1) / TILE * TILE;

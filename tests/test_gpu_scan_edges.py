@@ -116,6 +116,25 @@ def test_many_segments(lens, dtype):
         mixer_ref.check(pool.flip(0), h0, bh, "equal, state", F32)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_whole_sequences_of_many_channels(dtype):
+    """Channels (heads) enough for a workgroup a compute unit: long sequences are not cut, and ask for no workspace."""
+    lens = [400, 0, 300]
+    assert cf.selective_scan_workspace(700, 3, 4100, 1, 5, dtype=dtype, variant=TILED) > 0
+    assert cf.selective_scan_workspace(700, 3, 8200, 1, 5, dtype=dtype, variant=TILED) == 0
+    ins, st = channel_inputs(700, 8200, 1, 5, dtype, 70), rnd((3, 8200, 5), 71)
+    y, new = run(cf.selective_scan, ins, lens, st, TILED)
+    y0, by, h0, bh = ref.channels(*ins, True, lens, st)
+    mixer_ref.check(y, y0, by, "y", dtype)
+    mixer_ref.check(new, h0, bh, "state", F32)
+    assert cf.selective_scan_heads_workspace(700, 3, 260, 16, 260, 16, dtype=dtype, variant=TILED) == 0
+    ins, st = head_inputs(700, 260, 16, 260, 16, dtype, 72), rnd((3, 260, 16, 16), 73)
+    y, new = run(cf.selective_scan_heads, ins, lens, st, TILED)
+    y0, by, h0, bh = ref.heads(*ins, True, lens, st)
+    mixer_ref.check(y, y0, by, "y", dtype)
+    mixer_ref.check(new, h0, bh, "state", F32)
+
+
 @BOTH
 @pytest.mark.parametrize("variant", [DIRECT, TILED])
 def test_one_slot_read_by_all(which, variant):
