@@ -8,10 +8,10 @@
 // its states are one run of memory, and y is an exchange between LN lanes. No
 // wave waits for another.
 //
-// Single tokens: the states' bytes are the time, each read and written once. 64
-// sequences of 8192 channels of 16 states, bf16: 16.5 us, 4.3 TB/s, where the
-// states lie in the last cache, and 18 where they do not; 256: 61 us, 4.4 TB/s;
-// one: 3 us, a launch.
+// Single tokens: the states' bytes are the time, each read once and written once,
+// past the caches. 64 sequences of 8192 channels of 16 states, bf16: 16.1 us, 4.5
+// TB/s, where the states lie in the last cache (16.9 with stores that stay in the
+// caches), and 18.5 where they do not; 256: 61 us, 4.4 TB/s; one: 3 us, a launch.
 // Longer sequences are the chain from token to token; the next token's inputs
 // are loaded a token ahead (64 of 8 tokens: 41 us).
 #include "common.h"
@@ -23,6 +23,8 @@
 
 namespace convfwd {
 namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // One token's inputs as they lie in memory, R channels a lane.
 template <class T, int R>
@@ -60,8 +62,8 @@ __global__ __launch_bounds__(256) void scan_direct_kernel(ScanProblem p, int sli
     auto four = [&](float (&v)[4], const float *s) __attribute__((always_inline)) {
         if constexpr (WIDE) {
             if (at < p.N) {
-                const float4 f = *reinterpret_cast<const float4 *>(s);
-                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+                const f32x4 f = *reinterpret_cast<const f32x4 *>(s);
+                v[0] = f[0], v[1] = f[1], v[2] = f[2], v[3] = f[3];
             }
         } else {
 #pragma unroll
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(256) void scan_direct_kernel(ScanProblem p, int sli
                 continue;
             if constexpr (WIDE) {
                 if (at < p.N)
-                    *reinterpret_cast<float4 *>(to) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
+                    __builtin_nontemporal_store(f32x4{h[j][0], h[j][1], h[j][2], h[j][3]}, reinterpret_cast<f32x4 *>(to));
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)

@@ -7,8 +7,9 @@
 // eight rows and y is an exchange between eight lanes. A wave owns 8 RL rows
 // and waits for no other.
 //
-// Single tokens: the states' bytes are the time, each read and written once. 128
-// sequences of 128 heads of 64 x 128, bf16: 184 us, 5.8 TB/s; one: 5 us.
+// Single tokens: the states' bytes are the time, each read and written once, past
+// the caches. 128 sequences of 128 heads of 64 x 128, bf16: 170 us, 6.3 TB/s
+// (184 through the caches); 8: 14.2 (15.8); one: 4.2 (4.6).
 // Longer sequences are the chain from token to token; the next token's inputs
 // are loaded a token ahead.
 #include "common.h"
@@ -20,6 +21,8 @@
 
 namespace convfwd {
 namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // One token's inputs as they lie in memory.
 template <class T, int KV, int RL>
@@ -70,8 +73,8 @@ __global__ __launch_bounds__(256) void heads_direct_kernel(HeadScanProblem p, in
             for (int k = 0; k < KV; ++k) {
                 if constexpr (WIDE) {
                     if (32 * k + at < p.N) {
-                        const float4 v = *reinterpret_cast<const float4 *>(p.state_in + sat(j, k));
-                        S[j][k][0] = v.x, S[j][k][1] = v.y, S[j][k][2] = v.z, S[j][k][3] = v.w;
+                        const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p.state_in + sat(j, k)));
+                        S[j][k][0] = v[0], S[j][k][1] = v[1], S[j][k][2] = v[2], S[j][k][3] = v[3];
                     }
                 } else {
 #pragma unroll
@@ -176,8 +179,8 @@ __global__ __launch_bounds__(256) void heads_direct_kernel(HeadScanProblem p, in
                     continue;
                 if constexpr (WIDE) {
                     if (32 * k + at < p.N)
-                        *reinterpret_cast<float4 *>(p.state_out + sat(j, k)) =
-                            make_float4(S[j][k][0], S[j][k][1], S[j][k][2], S[j][k][3]);
+                        __builtin_nontemporal_store(f32x4{S[j][k][0], S[j][k][1], S[j][k][2], S[j][k][3]},
+                                                    reinterpret_cast<f32x4 *>(p.state_out + sat(j, k)));
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -209,7 +212,7 @@ void launch(const HeadScanProblem &p, hipStream_t s)
     // Several rows a lane where their states are short and there are rows enough. A token of 16384 rows of 16 states
     // takes 3.3 us with one row a lane and 4.0 with four, of 32768 4.4 and 4.2, of 2^20 66 and 43; of 16384 rows of 64
     // states 4.7 with one and with two, of 65536 10.4 and 8.8, of 2^20 107 and 100. Of 128 states one is best: 2^20 rows
-    // take 184 us with one and 201 with two.
+    // take 184 us with one and 201 with two. (Before the states went past the caches.)
     const int64_t rows = (int64_t)p.seq.num_seqs * p.H * p.P;
     if (p.N <= 32)
         rows <= 16384 ? launch_rows<T, 1, 1>(p, s) : launch_rows<T, 1, 4>(p, s);
