@@ -56,7 +56,7 @@ typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int Q = 64;                   // tokens of a chunk
-constexpr int NT_JOIN = 256;
+constexpr int NT_JOIN = 64;
 // Segments of a sequence whose states the last kernel puts together by itself: of 6 sequences of 4095 tokens together,
 // 16 segments, it takes 97 us where a kernel of its own for that makes it 114 us, of 8192 tokens of 128 heads 271 and 278.
 constexpr int FOLDED = 16;
@@ -830,7 +830,8 @@ __global__ __launch_bounds__(64 * WAVES<T>)
 
 // From the states that segments leave to those before them, along each sequence
 // of several segments: a thread takes four states of one lane of the kernels
-// above, four segments at a time.
+// above, eight segments at a time, their loads in flight together (32 segments of
+// 32 heads of 64 x 64: 9.8 us, with four at a time and four waves a workgroup 11.7).
 __global__ __launch_bounds__(NT_JOIN) void heads_join_kernel(HeadsArgs a, int per_head)
 {
     const int64_t per = (int64_t)a.p.H * per_head;
@@ -846,17 +847,17 @@ __global__ __launch_bounds__(NT_JOIN) void heads_join_kernel(HeadsArgs a, int pe
         const int64_t first = begin / a.seg + n, last = first + (len - 1) / a.seg;
         f32x4 v = states[first * per];
         states[first * per] = states[last * per];       // the sequence's own state
-        for (int64_t k = first + 1; k <= last; k += 4) {
-            f32x4 add[4];
-            float by[4];
+        for (int64_t k = first + 1; k <= last; k += 8) {
+            f32x4 add[8];
+            float by[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const int64_t at = k + j < last ? k + j : last;
                 add[j] = states[at * per];
                 by[j] = a.decays[at * a.p.H + h];
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 8; ++j)
                 if (k + j <= last) {
                     states[(k + j) * per] = v;
 #pragma unroll
