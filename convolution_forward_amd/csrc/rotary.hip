@@ -253,15 +253,16 @@ void launch_units(const RotaryProblem &p, hipStream_t s)
     RotaryArgs a;
     a.p = p;
     const int total = p.Hq + p.Hk, groups = NT / L;
-    // Few tokens: one a workgroup, and only as many heads as it has groups, so
-    // that the heads spread over the compute units.
+    // Few of both: only as many heads a workgroup as it has groups, so that the
+    // heads spread over the compute units.
     const bool few = p.tokens * (int64_t)total <= 4096;
-    // Otherwise one too up to four workgroups a compute unit (32 + 8 heads of 128, bf16: 512 tokens 6.0 us with one, 6.4
+    // One token a workgroup up to four workgroups a compute unit (32 + 8 heads of 128, bf16: 512 tokens 6.0 us with one, 6.4
     // with two, 7.9 with four, 1024 7.6, 8.3 and 9.2), then two, or four where the groups have less than a batch of heads
     // with two. 16 + 16 heads of 128, fp32, 16 groups: 1111 tokens 9.7, 9.5 and 10.7, 16384 94, 95 and 99; 16 + 2 heads
     // of 256, bf16, 16 groups: 4096 tokens 19.6, 18.3 and 16.2.
     // With few heads more, so that every group has one (3 heads of 128, 109226
-    // tokens: 67 us with 4 tokens, 37 with 8), as far as the table is 16 KB.
+    // tokens: 67 us with 4 tokens, 37 with 8), as far as the table is 16 KB; not
+    // where there are few tokens too (1300 of 3 heads of 64: 3.8 us, so 5.2).
     a.toks = p.tokens <= 1024 ? 1 : 2 * total < BATCH * groups ? 4 : 2;
     while (!few && a.toks * total < groups && a.toks * 2 * p.rotated <= 4096)
         a.toks *= 2;
