@@ -66,12 +66,16 @@ struct ScanArgs {
 // of the next tile that are in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// A thread's piece of a row, loaded and stored as parts of at most 16 bytes: in
+// fp32 eight values are two.
 template <class T, int V>
 struct Piece {
-    T v[V] __attribute__((aligned(V * sizeof(T) < 16 ? V * sizeof(T) : 16)));
+    static constexpr int PART = V * sizeof(T) < 16 ? V : 16 / sizeof(T);
+    T v[V] __attribute__((aligned(PART * sizeof(T))));
 };
 
-// VEC: channels and states lie in whole aligned pieces (a host rule).
+// VEC: channels and states lie in whole aligned parts of pieces (a host rule), of
+// which the last piece of a row may have only some.
 template <class T, int LN, bool FULL, bool VEC>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void scan_tile_kernel(ScanArgs a)
 {
@@ -122,9 +126,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
 
     // Values past the channels (states) are the row's first ones, and are not used.
     auto row_piece = [&](auto &to, const T *row, int at, int width) __attribute__((always_inline)) {
-        constexpr int V = sizeof(to.v) / sizeof(T);
+        constexpr int V = sizeof(to.v) / sizeof(T), PART = Piece<T, V>::PART;
         if constexpr (VEC) {
-            __builtin_memcpy(&to, __builtin_assume_aligned(row + (at < width ? at : 0), alignof(Piece<T, V>)), sizeof(to));
+#pragma unroll
+            for (int i = 0; i < V; i += PART)
+                __builtin_memcpy(to.v + i, __builtin_assume_aligned(row + (at + i < width ? at + i : 0), PART * sizeof(T)),
+                                 PART * sizeof(T));
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -355,8 +362,11 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
             T *yr = const_cast<T *>(row_of(yp, p.ys, t, tok)) + cc;
             if (there) {
                 if constexpr (VEC) {
-                    if (cc < end)
-                        __builtin_memcpy(__builtin_assume_aligned(yr, alignof(Piece<T, EC>)), &o, sizeof(o));
+                    constexpr int PART = Piece<T, EC>::PART;
+#pragma unroll
+                    for (int i = 0; i < EC; i += PART)
+                        if (cc + i < end)
+                            __builtin_memcpy(__builtin_assume_aligned(yr + i, PART * sizeof(T)), o.v + i, PART * sizeof(T));
                 } else {
 #pragma unroll
                     for (int i = 0; i < EC; ++i)
@@ -473,7 +483,7 @@ hipError_t launch_lanes(const ScanArgs &a, bool parts, bool vec, hipStream_t s)
 template <class T>
 hipError_t launch(const ScanArgs &a, const Plan &l, hipStream_t s)
 {
-    // A thread's piece: 16 / LN channels, or LN states of b and of c.
+    // A thread's piece: 16 / LN channels, or LN states of b and of c; of their parts, 16 bytes at most, a row has whole ones.
     const ScanProblem &p = a.p;
     const int64_t ec = 16 / l.ln * sizeof(T), eb = l.ln * sizeof(T);
     const uintptr_t rows = (uintptr_t)p.x | (uintptr_t)p.dt | (uintptr_t)p.gate | (uintptr_t)p.y |
