@@ -934,8 +934,9 @@ bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype d
         return false;
     l->seg = (int)seg;
     l->numbers = seq_tiles(s, l->seg);
-    // Threads of the grid below 2^32.
-    return (l->numbers * groups + 7) / 8 * 8 * l->wgs < (int64_t(1) << 24);
+    // Threads of the grid below 2^32: 512 of them a workgroup in bf16, 256 in fp32.
+    const int64_t threads = 64 * (f32 ? WAVES<float> : WAVES<uint16_t>);
+    return (l->numbers * groups + 7) / 8 * 8 * l->wgs < (int64_t(1) << 32) / threads;
 }
 
 Sequences sequences_of(int64_t tokens, int num_seqs, bool equal)
