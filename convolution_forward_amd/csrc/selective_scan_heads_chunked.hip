@@ -466,7 +466,8 @@ struct Chunks {
             e += moved<0x143, 0xc>(e);
             const double mid = of_lane(e, 31), end = of_lane(e, 63);
             exponent += end;
-            const bool wide = __any(!(fabs(e - mid) <= 60.0));
+            const bool extreme = d != 0.f && !(fabsf(d) >= 0x1p-60f && fabsf(d) <= 0x1p60f);
+            const bool wide = __any(!(fabs(e - mid) <= 60.0) || extreme);
             of.tail[lane] = power2(end - e) * d;
             if constexpr (FULL) {
                 f.L[lane] = e;
@@ -644,16 +645,18 @@ struct Chunks {
                             raw[tj] = product(bf, cf, raw[tj]);
                         }
                     }
+                    // (The factors first: under a decay they come to d_j at most, where c . b times one of them may leave
+                    // fp32's range or fall among its subnormal numbers.)
                     float m[8];
                     if (!wide) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            m[e] = raw[e >> 2][e & 3] * col[e] * r;
+                            m[e] = raw[e >> 2][e & 3] * (col[e] * r);
                     } else {
                         const double Li = fm.L[ti];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            m[e] = raw[e >> 2][e & 3] * fm.step[tj0 + e] * power2(Li - fm.L[tj0 + e]);
+                            m[e] = raw[e >> 2][e & 3] * (fm.step[tj0 + e] * power2(Li - fm.L[tj0 + e]));
                     }
                     if (it >> 1 == s) {
 #pragma unroll

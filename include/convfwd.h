@@ -565,8 +565,10 @@ CONVFWD_API int64_t conv_selective_scan_workspace(int64_t tokens, int num_seqs, 
  *
  * d a <= 0, a decay, is the scan's use. A state may grow too, but where it
  * grows past 2^100 within a chunk the outputs from there on are unspecified.
- * Chunks make the products c . b of their tokens before any step size: where
- * one leaves fp32's range, its token's outputs of the group are unspecified.
+ * Chunks make a token's products with c before x and before the decay of
+ * what came before the chunk: d c . b for each token up to it, and c with the
+ * state's rows. Where c . b, or one of these, leaves fp32's range, the token's
+ * outputs of the head are unspecified.
  * A value that is not finite, or leaves fp32's range, reaches no earlier
  * token, no other group and no other sequence.
  */
