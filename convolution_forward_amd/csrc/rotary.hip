@@ -17,10 +17,11 @@
 // heads of 128, bf16, with norms: 65 us, 0.34 GB at 5.15 TB/s (a plain copy:
 // 5.1). 8 tokens: 5.8 us, a launch.
 //
-// An angle is the exact product (a double holds 29 bits of position times 24
-// of frequency) as turns, reduced in 64 bits to an eighth of a turn round a
-// quarter's multiple, where fp32 holds it to 2^-25 of a radian; the series of
-// sine and cosine there leave out less than 2^-28.
+// An angle is position times frequency, exact where that fits a double (29 bits
+// of position times 24 of frequency, or more of the one and fewer of the other),
+// else rounded to its 53 bits. It is reduced by quarters of a turn, pi / 2 in two
+// parts of 53 bits each, up to 2^48 radians, and then held in fp32 to 2^-25 of a
+// radian; the series of sine and cosine leave out less than 2^-28.
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"
@@ -34,9 +35,11 @@ constexpr int BATCH = 4;        // heads in flight a lane
 
 __device__ __forceinline__ void turn(double position, float frequency, float scale, float &c, float &s)
 {
-    const double t = position * ((double)frequency * 0.15915494309189533577);
-    const double q = rint(4.0 * t);
-    const float x = (float)((t - 0.25 * q) * 6.28318530717958647693), z = x * x;
+    const double t = position * (double)frequency;
+    const double q = rint(t * 0.63661977236758134308);
+    const double r = fma(-q, 6.12323399573676603587e-17, fma(-q, 1.57079632679489661923, t));
+    // (Past 2^48 the quarters are no longer exact: the angle is arbitrary, but no larger than the series are for.)
+    const float x = fabs(r) > 1.0 ? 0.f : (float)r, z = x * x;
     float sn = 1.f / 362880.f;
     sn = fmaf(sn, z, -1.f / 5040.f);
     sn = fmaf(sn, z, 1.f / 120.f);

@@ -465,7 +465,9 @@ CONVFWD_API int64_t conv_delta_rule_workspace(int64_t tokens, int num_seqs, int 
  * for the pairs i < rotated / 2 of n's first `rotated` values: (n_i,
  * n_{i + rotated/2}), or (n_2i, n_{2i+1}) with interleaved != 0. The values
  * from `rotated` on are n_j. The angle is reduced in 64 bits, so that far
- * positions keep their precision; a frequency or position of any sign will do.
+ * positions keep their precision: it is the exact product up to positions of
+ * 2^29 at any frequency, or of 2^48 at a frequency of 1; further away it is
+ * off by 2^-53 of itself. A frequency or position of any sign will do.
  * A head of zeros stays zeros also without an eps.
  *
  *   q          device [tokens, Hq, D], `dtype` (CONV_F32 or CONV_BF16);
