@@ -163,7 +163,8 @@ def rotary_frequencies(rotated: int, base: float = 10000.0, scaling: str | None 
             # The index at which a frequency makes that many turns.
             ends = [half * math.log(trained / (2 * math.pi * turns)) / math.log(base) for turns in (fast, slow)]
             lo, hi = max(math.floor(ends[0]), 0), min(math.ceil(ends[1]), rotated - 1)
-            keep = [1.0 - min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(half)]
+            # hi is past lo unless one was moved into the range: then all make at most `slow` turns, or `fast` and more.
+            keep = [1.0 - min(max((i - lo) / (hi - lo), 0.0), 1.0) if hi > lo else float(i < lo) for i in range(half)]
             scale = 0.1 * math.log(factor) + 1.0
         else:
             keep = [min(max((trained * v / (2 * math.pi) - slow) / (fast - slow), 0.0), 1.0) for v in f]
