@@ -206,7 +206,7 @@ __global__ __launch_bounds__(NT) void rotary_kernel(RotaryArgs a)
                     // Squares that leave fp32's range are made again of values brought near it; zeros stay zeros.
                     by = ms < 1.f ? 0x1p100f : 0x1p-80f;
                     const float again = squares(by) / (float)p.D + p.eps * by * by;
-                    r = again > 0.f ? 1.f / sqrtf(again) : again == 0.f ? 0.f : again;
+                    r = again == 0.f ? 0.f : 1.f / sqrtf(ms < 0.f ? ms : again);     // (a negative eps: NaN)
                 }
                 const T *w = static_cast<const T *>(query ? p.qweight : p.kweight);
 #pragma unroll
