@@ -4,11 +4,22 @@
 // |x| 2^-24 of the value, is that of rounding x itself to fp32.
 #pragma once
 
+#include <float.h>
+
 #include "common.h"
 
 namespace convfwd {
 
 constexpr float LOG2E = 1.44269504088896340736f;
+
+// A rate, in units of log 2. What is below fp32's numbers, minus infinity too, is
+// the lowest of them: it forgets the state at every token but one of step zero,
+// where minus infinity would make a NaN of it.
+__device__ __forceinline__ float rate_of_log2(float a)
+{
+    const float r = a * LOG2E;
+    return r < -FLT_MAX ? -FLT_MAX : r;
+}
 
 // A step size: v, or log(1 + exp(v)). log(1 + e) of 0 <= e <= 1 is
 // 2 atanh(s), s = e / (2 + e) <= 1/3, which keeps the relative precision that

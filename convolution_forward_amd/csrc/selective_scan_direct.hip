@@ -86,6 +86,9 @@ __global__ __launch_bounds__(256) void scan_direct_kernel(ScanProblem p, int sli
 #pragma unroll
     for (int j = 0; j < R; ++j) {
         four(a[j], p.a + place(j));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            a[j][i] = rate_of_log2(a[j][i]);
         skip[j] = p.skip ? p.skip[ch[j]] : 0.f;
         bias[j] = p.bias ? p.bias[ch[j]] : 0.f;
     }
@@ -136,7 +139,7 @@ __global__ __launch_bounds__(256) void scan_direct_kernel(ScanProblem p, int sli
             for (int i = 0; i < 4; ++i) {
                 const bool in = WIDE ? at < p.N : at + i < p.N;
                 // States past the last one stay zeros, whatever x is.
-                h[j][i] = in ? fmaf(__builtin_amdgcn_exp2f(d * (a[j][i] * LOG2E)), h[j][i], dx * load_as_f32(&t.b[i])) : 0.f;
+                h[j][i] = in ? fmaf(__builtin_amdgcn_exp2f(d * a[j][i]), h[j][i], dx * load_as_f32(&t.b[i])) : 0.f;
                 y = in ? fmaf(h[j][i], load_as_f32(&t.c[i]), y) : y;
             }
             y = lanes_sum<LN>(y);

@@ -280,7 +280,7 @@ struct Chunks {
         // Wave w < heads makes the factors of head head0 + w.
         const int fh = group * per + head0 + min(w, heads - 1);
         const T *dp = static_cast<const T *>(p.dt) + first * p.dts + fh;
-        const double rate = (double)p.a[fh] * 1.4426950408889634074;
+        const double rate = (double)(p.a[fh] < -FLT_MAX ? -FLT_MAX : p.a[fh]) * 1.4426950408889634074;   // as rate_of_log2
         const float bias = p.bias ? p.bias[fh] : 0.f;
         const int cols = p.P - col0;                // columns there are, from the wave's first
 

@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) void heads_direct_kernel(HeadScanProblem p, in
                 }
             }
     }
-    const float a = p.a[h] * LOG2E, skip = p.skip ? p.skip[h] : 0.f, bias = p.bias ? p.bias[h] : 0.f;
+    const float a = rate_of_log2(p.a[h]), skip = p.skip ? p.skip[h] : 0.f, bias = p.bias ? p.bias[h] : 0.f;
     const T *xp = static_cast<const T *>(p.x) + begin * p.xst + h * p.xsh;
     const T *dp = static_cast<const T *>(p.dt) + begin * p.dts + h;
     const T *gp = p.gate ? static_cast<const T *>(p.gate) + begin * p.gst + h * p.gsh : nullptr;

@@ -33,8 +33,6 @@
 // or three of the recurrence and y (2.7 each), 97 clocks, and some 60 of step
 // sizes, gates, conversions and exchanges, of 181 it takes at four waves a SIMD.
 // Four waves and tiles of 64 tokens, with the products d x b kept: 513 us.
-#include <float.h>
-
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"
@@ -185,12 +183,11 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(4))) void sc
         }
         return v;
     };
-    // (A rate of minus infinity, a state forgotten at each token, as the lowest number: times the zero step of a token that
-    // is not there it has to be zero.)
-    f32x4 rate = four(p.a + sat) * LOG2E;
+    // (Never minus infinity: times the zero step of a token that is not there it has to be zero.)
+    f32x4 rate = four(p.a + sat);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        rate[i] = rate[i] < -FLT_MAX ? -FLT_MAX : rate[i];
+        rate[i] = rate_of_log2(rate[i]);
     const int64_t state_size = (int64_t)p.channels * p.N;
     const int slot = p.state_in || p.state_out ? seq_slot(p.seq, tile.n) : -1;
     auto kept = [&](f32x4 *base, int k) { return base + ((int64_t)k * a.slices + slice) * 64 + lane; };

@@ -503,7 +503,8 @@ CONVFWD_API conv_status conv_rotary_fwd(const void *q, const int64_t *q_strides,
  * term, and without a gate its factor, is left out.
  *
  *   x, dt, gate, y  device [tokens, channels], `dtype` (CONV_F32 or CONV_BF16), a row stride each. gate may be NULL.
- *   a          device, contiguous [channels, N] fp32; negative for a decay. N <= 256.
+ *   a          device, contiguous [channels, N] fp32; negative for a decay, minus infinity (taken for the lowest
+ *              number) to forget h at each token whose d is not 0. N <= 256.
  *   b, c       device [tokens, groups, N], `dtype`; strides: host arrays
  *              (token, group) in elements, NULL = contiguous.
  *   skip, dt_bias  device [channels] fp32, or NULL.
@@ -552,7 +553,8 @@ CONVFWD_API int64_t conv_selective_scan_workspace(int64_t tokens, int num_seqs, 
  *              strides: host arrays (token, head) in elements, NULL =
  *              contiguous. Channels are adjacent. gate may be NULL.
  *   dt         device [tokens, H], `dtype`, row stride dt_stride.
- *   a, skip, dt_bias  device [H] fp32; skip and dt_bias may be NULL. a is negative for a decay.
+ *   a, skip, dt_bias  device [H] fp32; skip and dt_bias may be NULL. a is negative for a decay, minus infinity (taken
+ *              for the lowest number) to forget S at each token whose d is not 0.
  *   b, c       device [tokens, groups, N], `dtype`, strides likewise (token, group). N <= 256.
  *   state_in, state_out  device, contiguous [num_slots, H, P, N] fp32.
  *   workspace  device memory of at least conv_selective_scan_heads_workspace
