@@ -158,7 +158,7 @@ int64_t row_stride(const Tensor &t, const char *what, int64_t width, int64_t row
 
 int small(int64_t v, const char *what)
 {
-    if (v > INT32_MAX)
+    if (v > INT32_MAX || v < INT32_MIN)
         refuse(what, " of ", v, " is too large");
     return (int)v;
 }
@@ -312,7 +312,7 @@ PyObject *matmul_q8(PyObject *const *a)
         y = fresh(x, sizes, ytype);
     }
     const conv_status st = conv_matmul_q8_fwd(ptr(x), xs, sx, ptr(w), ws, sw, b, ptr(y), ys, M, small(N, "a channel count"),
-                                              small(K, "a K"), qdt, ydt, (int)integer(a[7]), stream_of(x));
+                                              small(K, "a K"), qdt, ydt, small(integer(a[7]), "a variant"), stream_of(x));
     return st != CONV_OK ? status(st) : wrap(std::move(y));
 }
 
@@ -371,7 +371,7 @@ PyObject *gated_delta_rule(PyObject *const *a)
     if (out)
         head_strides(*out, seq.tokens, "out", Hv, Dv, type, st_o);
     const int hk = small(Hk, "a head count"), hv = small(Hv, "a head count"), dk = small(Dk, "a head's width"),
-              dv = small(Dv, "a head's width"), variant = (int)integer(a[13]);
+              dv = small(Dv, "a head's width"), variant = small(integer(a[13]), "a variant");
     const double scale = a[5] == Py_None ? 1.0 / std::sqrt((double)Dk) : number(a[5]);
     const c10::DeviceGuard guard(q.device());
     Tensor o = out ? *out : fresh(v, v.sizes(), type);
@@ -503,7 +503,7 @@ PyObject *selective_scan(PyObject *const *a)
     const int64_t num = state(so, shape, at::kFloat, state(si, shape, at::kFloat, 0));
     const auto *sl = static_cast<const int32_t *>(vector(slots, seq.count, at::kInt, "slots"));
     const int ch = small(channels, "a channel count"), g = small(groups, "a group count"), n = small(N, "a state count"),
-              variant = (int)integer(a[15]);
+              variant = small(integer(a[15]), "a variant");
     const c10::DeviceGuard guard(x.device());
     Tensor y = out ? *out : fresh(x, x.sizes(), type);
     const Space space(work, x, work ? 0 : conv_selective_scan_workspace(seq.tokens, seq.count, ch, g, n, dt, variant));
@@ -546,7 +546,7 @@ PyObject *selective_scan_heads(PyObject *const *a)
     const int64_t num = state(so, shape, at::kFloat, state(si, shape, at::kFloat, 0));
     const auto *sl = static_cast<const int32_t *>(vector(slots, seq.count, at::kInt, "slots"));
     const int h = small(H, "a head count"), p = small(P, "a head's width"), g = small(groups, "a group count"),
-              n = small(N, "a state count"), variant = (int)integer(a[15]);
+              n = small(N, "a state count"), variant = small(integer(a[15]), "a variant");
     const c10::DeviceGuard guard(x.device());
     Tensor y = out ? *out : fresh(x, x.sizes(), type);
     const Space space(work, x,
