@@ -117,8 +117,8 @@ def rotary(q, positions, frequencies, k=None, q_weight=None, k_weight=None, eps:
     """Norms of queries and keys for each head, and their rotation by position (conv_rotary_fwd in include/convfwd.h).
 
     q [tokens, Hq, D] or [batch, length, Hq, D] float32 or bfloat16, k likewise
-    with Hk heads; positions [tokens] int64 or int32 (a value a token, batches
-    one after the other); frequencies [R / 2] float32, as rotary_frequencies
+    with Hk heads; positions [tokens] or [batch, length], contiguous, int64 or
+    int32; frequencies [R / 2] float32, as rotary_frequencies
     makes them: the first R values of a head are rotated, in pairs i and
     i + R/2, or 2i and 2i + 1 with interleaved. q_weight and k_weight [D] of
     q's type: an RMS norm before the rotation; without one the values are

@@ -9,10 +9,10 @@
  * dynamic LDS limit has been raised (hipFuncSetAttribute, done on the first
  * launch there and remembered only once it succeeds); calls are thread-safe.
  *
- * Two convolution operators, and at the end of this file the four operators
- * of a token mixer built round a short causal convolution (norm, 8-bit
- * product, causal convolution, head norms and rotation, gated delta rule,
- * selective scans):
+ * Two convolution operators, and at the end of this file the operators of a
+ * token mixer built round a short causal convolution (norm, 8-bit product,
+ * causal convolution, head norms and rotation, gated delta rule, selective
+ * scans):
  *
  *  - Dense NHWC cross-correlation, as fixed by "CMU DLSys Lecture 14:
  *    Convolutional Network Implementation", section 1 (the index contract):
@@ -472,7 +472,8 @@ CONVFWD_API int64_t conv_delta_rule_workspace(int64_t tokens, int num_seqs, int 
  *
  *   q          device [tokens, Hq, D], `dtype` (CONV_F32 or CONV_BF16);
  *              strides: host arrays (token, head) in elements, NULL =
- *              contiguous. Channels are adjacent. D <= 512.
+ *              contiguous. Channels are adjacent. D <= 512, fewer than 2^24
+ *              tokens, Hq and Hk up to 65535 (CONV_ERR_UNSUPPORTED past them).
  *   k          device [tokens, Hk, D] likewise; Hk == 0: no keys (k, k_out,
  *              their strides and k_weight are then ignored).
  *   positions  device [tokens], int32 or int64 (position_bits 32 or 64).
@@ -481,7 +482,9 @@ CONVFWD_API int64_t conv_delta_rule_workspace(int64_t tokens, int num_seqs, int 
  *   q_out, k_out  device, shapes of q and k. Each may be its input (same
  *              pointer and strides); they may be columns of one buffer of
  *              rows, as q and k may.
- * Errors: CONV_ERR_SHAPE for an odd `rotated` or one past D.
+ * Errors: CONV_ERR_SHAPE for an odd `rotated` or one past D. eps is not
+ * checked: a head whose mean square and a negative eps add up to less than 0
+ * is NaN.
  */
 CONVFWD_API conv_status conv_rotary_fwd(const void *q, const int64_t *q_strides, const void *k,
                                         const int64_t *k_strides, const void *positions, int position_bits,
@@ -502,7 +505,8 @@ CONVFWD_API conv_status conv_rotary_fwd(const void *q, const int64_t *q_strides,
  * Channel i reads b and c of group i / (channels / groups). Without skip its
  * term, and without a gate its factor, is left out.
  *
- *   x, dt, gate, y  device [tokens, channels], `dtype` (CONV_F32 or CONV_BF16), a row stride each. gate may be NULL.
+ *   x, dt, gate, y  device [tokens, channels], `dtype` (CONV_F32 or CONV_BF16), a row stride each. gate may be NULL. At
+ *              most 2^23 channels.
  *   a          device, contiguous [channels, N] fp32; negative for a decay, minus infinity (taken for the lowest
  *              number) to forget h at each token whose d is not 0. N <= 256.
  *   b, c       device [tokens, groups, N], `dtype`; strides: host arrays
@@ -521,7 +525,8 @@ CONVFWD_API conv_status conv_rotary_fwd(const void *q, const int64_t *q_strides,
  * d a <= 0, a decay, is the scan's use. A state may grow too, but where it
  * grows past 2^100 within a tile the outputs from there on are unspecified.
  * A value that is not finite, or leaves fp32's range, reaches no earlier
- * token and no other sequence.
+ * token and no other sequence; what comes of it may be NaN where the formulas
+ * give an infinity.
  */
 CONVFWD_API conv_status conv_selective_scan_fwd(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride,
                                                 const float *a, const void *b, const int64_t *b_strides,
@@ -551,7 +556,8 @@ CONVFWD_API int64_t conv_selective_scan_workspace(int64_t tokens, int num_seqs, 
  *
  *   x, gate, y  device [tokens, H, P], `dtype` (CONV_F32 or CONV_BF16);
  *              strides: host arrays (token, head) in elements, NULL =
- *              contiguous. Channels are adjacent. gate may be NULL.
+ *              contiguous. Channels are adjacent. gate may be NULL. H up to
+ *              65535, P up to 65536.
  *   dt         device [tokens, H], `dtype`, row stride dt_stride.
  *   a, skip, dt_bias  device [H] fp32; skip and dt_bias may be NULL. a is negative for a decay, minus infinity (taken
  *              for the lowest number) to forget S at each token whose d is not 0.
@@ -574,7 +580,8 @@ CONVFWD_API int64_t conv_selective_scan_workspace(int64_t tokens, int num_seqs, 
  * state's rows. Where c . b, or one of these, leaves fp32's range, the token's
  * outputs of the head are unspecified.
  * A value that is not finite, or leaves fp32's range, reaches no earlier
- * token, no other group and no other sequence.
+ * token, no other group and no other sequence; what comes of it may be NaN
+ * where the formulas give an infinity.
  */
 CONVFWD_API conv_status conv_selective_scan_heads_fwd(const void *x, const int64_t *x_strides, const void *dt,
                                                       int64_t dt_stride, const float *a, const void *b,
