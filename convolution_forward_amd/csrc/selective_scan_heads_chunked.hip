@@ -942,17 +942,6 @@ bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype d
     return (l->numbers * groups + 7) / 8 * 8 * l->wgs < (int64_t(1) << 32) / threads;
 }
 
-Sequences sequences_of(int64_t tokens, int num_seqs, bool equal)
-{
-    Sequences s = {};
-    static const int32_t some = 0;
-    s.offsets = equal ? nullptr : &some;        // only whether there are offsets counts here
-    s.num_seqs = num_seqs;
-    s.tokens = tokens;
-    s.each = tokens / num_seqs;
-    return s;
-}
-
 // Floats of the workspace's states, as the lanes hold them.
 int64_t state_floats(const Plan &l, int H) { return l.numbers * H * l.slices * 16 * (32 * l.kn); }
 

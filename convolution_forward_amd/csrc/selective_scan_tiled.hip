@@ -444,17 +444,6 @@ bool make_plan(const Sequences &s, int channels, int groups, int N, Plan *l)
     return l->numbers * ((l->slices + 7) / 8 * 8) < (int64_t(1) << 23);
 }
 
-Sequences sequences_of(int64_t tokens, int num_seqs, bool equal)
-{
-    Sequences s = {};
-    static const int32_t some = 0;
-    s.offsets = equal ? nullptr : &some;        // only whether there are offsets counts here
-    s.num_seqs = num_seqs;
-    s.tokens = tokens;
-    s.each = tokens / num_seqs;
-    return s;
-}
-
 // Bytes of the workspace's states, and of its decays.
 int64_t half_space(const Plan &l) { return l.parts ? l.numbers * l.slices * 64 * 16 : 0; }
 

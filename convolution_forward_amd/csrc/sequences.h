@@ -39,6 +39,19 @@ struct SeqTile {
 
 inline int64_t seq_tiles(const Sequences &s, int tile) { return s.tokens / tile + s.num_seqs; }
 
+// Sequences as a plan of sizes alone sees them: equally long, or with offsets,
+// of which it only asks whether there are any.
+inline Sequences sequences_of(int64_t tokens, int num_seqs, bool equal)
+{
+    static const int32_t some = 0;
+    Sequences s = {};
+    s.offsets = equal ? nullptr : &some;
+    s.num_seqs = num_seqs;
+    s.tokens = tokens;
+    s.each = tokens / num_seqs;
+    return s;
+}
+
 // Called by whole waves with a uniform number: 64 lanes probe 64 sequences at
 // a time, so up to 64 sequences cost one memory round trip, 4096 two.
 __device__ __forceinline__ SeqTile seq_tile(const Sequences &s, int tile, int number)
