@@ -15,7 +15,9 @@
 // them as often, at some 60 instructions), then groups of L lanes go over the
 // heads, `toks` groups side by side on one token each. 16384 tokens of 32 and 8
 // heads of 128, bf16, with norms: 65 us, 0.34 GB at 5.15 TB/s (a plain copy:
-// 5.1). 8 tokens: 5.8 us, a launch.
+// 5.1). 8 tokens: 5.2 to 5.9 us, of which a launch is 3: a thread's position, its
+// frequency, the heads behind the barrier and the weights behind the norm's sum
+// come one after the other.
 //
 // An angle is position times frequency, exact where that fits a double (29 bits
 // of position times 24 of frequency, or more of the one and fewer of the other),

@@ -43,13 +43,13 @@ conv_status check_scan_sizes(int64_t tokens, int num_seqs, int channels, int gro
         return CONV_ERR_UNSUPPORTED;
     const bool can = scan_tiled_supports(tokens, num_seqs, channels, groups, N);
     // Tokens a sequence, as the host knows them (the mean), from which tiles are
-    // faster. A lone sequence of 8192 channels of 16 states takes 9 us by tiles up
-    // to 64 tokens, and token by token 9 for 16 of them, 13 for 32. Once there
-    // are more workgroups than run at once, 8 such sequences take 51 us by tiles
-    // up to 32 tokens and 56 for 64 (token by token 25 and 48), 64 take 380 and
-    // 425 (132 and 254); tiles are ahead from some 85 and 140 tokens. But one long
-    // sequence among short ones is the time token by token (one of 4033 tokens
-    // with 63 of one: 2670 us, by tiles 570), so less is asked for.
+    // faster. A lone sequence of 8192 channels of 16 states takes 8.8 to 9.8 us by
+    // tiles up to 64 tokens, and token by token 8.2 for 16 of them, 13.4 for 32.
+    // Once there are more workgroups than run at once, 8 such sequences take 55 us
+    // by tiles for 32 tokens and 57 for 64 (token by token 25 and 44), 64 take 426
+    // and 452 (127 and 243); tiles are ahead from some 100 and 220 tokens. But one
+    // long sequence among short ones is the time token by token (one of 4033 tokens
+    // with 63 of one: 2110 us, by tiles 514), so less is asked for.
     const bool alone = (int64_t)num_seqs * channels * N <= 512 * 256;
     const int least = alone ? 16 : 48;
     *tiled = variant == CONV_VARIANT_TILED || (variant == CONV_VARIANT_AUTO && can && tokens > least * (int64_t)num_seqs);
@@ -69,12 +69,13 @@ conv_status check_heads_sizes(int64_t tokens, int num_seqs, int H, int P, int gr
         return CONV_ERR_UNSUPPORTED;
     const bool can = heads_chunked_supports(tokens, num_seqs, H, P, groups, N, dtype);
     // Tokens a sequence, as the host knows them (the mean), from which chunks
-    // are faster. bf16, heads of 64 x 128: a lone sequence of 128 heads takes 13 us
-    // by chunks up to 32 tokens, and token by token 9.9 for 8 of them, 15.2 for
-    // 16; 8 such sequences 22 us (token by token 20 for 4 tokens, 29 for 8), 64 of
-    // them 148 to 158 (126 and 196). fp32, 32 heads of 64 x 64, where a chunk costs
-    // more: 11.6 us alone (24 tokens one by one 10.7, 32 13.0), 64 sequences 94 to
-    // 97 (32 tokens 68, 64 125).
+    // are faster. bf16, heads of 64 x 128: a lone sequence of 128 heads takes 13.2
+    // us by chunks up to 32 tokens, and token by token 11.6 for 12 of them, 14.2
+    // for 16; 8 such sequences 22 us (token by token 20 for 4 tokens, 24 for 6), 64
+    // of them 147 and 157 (123 and 158). fp32, 32 heads of 64 x 64, where a chunk
+    // costs more: 11.5 us alone (24 tokens one by one 9.8, 32 12.0), 64 sequences
+    // 95 for 32 tokens and 111 for 64 (67 and 118, level at 58; a long sequence
+    // among short ones gains by chunks, so less is asked for).
     const bool alone = (int64_t)num_seqs * H * P <= 16384;
     const int least = dtype == CONV_F32 ? (alone ? 24 : 44) : alone ? 12 : 6;
     *tiled = variant == CONV_VARIANT_TILED || (variant == CONV_VARIANT_AUTO && can && tokens > least * (int64_t)num_seqs);

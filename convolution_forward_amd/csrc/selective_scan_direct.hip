@@ -11,9 +11,12 @@
 // Single tokens: the states' bytes are the time, each read once and written once,
 // past the caches. 64 sequences of 8192 channels of 16 states, bf16: 16.1 us, 4.5
 // TB/s, where the states lie in the last cache (16.9 with stores that stay in the
-// caches), and 18.5 where they do not; 256: 61 us, 4.4 TB/s; one: 3 us, a launch.
+// caches), and 18.5 where they do not; 256: 62.5 us, 4.6 TB/s; one: 3.2 us, a
+// launch. The offsets come first, one after the other, then the state and the
+// rates, and the token's inputs last: that chain is what 64 sequences do not hide.
 // Longer sequences are the chain from token to token; the next token's inputs
-// are loaded a token ahead (64 of 8 tokens: 41 us).
+// are loaded a token ahead (64 of 8 tokens: 41 us; one of 1000 tokens of 2048
+// channels of 64 states, more than tiles take: 419).
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"
@@ -209,8 +212,8 @@ void launch_lanes(const ScanProblem &p, hipStream_t s)
     int slices = (p.channels + CH - 1) / CH;
     int64_t jobs = (int64_t)p.seq.num_seqs * slices;
     // Two channels a lane from 8192 waves on, as many as run at once: a single token of 8192 channels of 16 states in 256
-    // sequences takes 61 us (one a lane: 73), in 64 18.2 (20.3), in 16 6.7 (7.4), but in 4 3.8 (3.3). Four take 73 us in
-    // 256: 157 registers.
+    // sequences takes 62.5 us (one a lane: 66.3), in 64 17 (17), in 16 5.5 (6.0), but in 4 4.1 (3.6). Four a lane were
+    // slower than one in 256: 157 registers.
     const bool two = wide && jobs >= 8192 && p.channels / p.groups % (2 * CH) == 0;
     if (two) {
         slices /= 2;

@@ -11,8 +11,9 @@
 // A wave owns 16 rows of S (columns of X) of one head and keeps them in its
 // accumulators from chunk to chunk; as they leave one product they are the
 // operand of the next. The waves of a workgroup (eight in bf16, four in fp32)
-// are of one group and share the chunk's B and C in LDS, and the c . b of M,
-// which each head in the workgroup turns into its own M.
+// are of one group and share the chunk's B and C in LDS. M's six blocks of 16 x
+// 32 go round the waves of its head, which make c . b and the factors for them,
+// each head's anew.
 //
 // Long sequences are cut into segments of `seg` tokens where there are too few
 // heads to fill the chip: a first kernel makes the state that each segment but
@@ -26,10 +27,14 @@
 // mid + lo, 24 bits together, and the products of parts above 2^-24 are added
 // in fp32: three for an exact operand times a split one, six for two split ones.
 //
-// 8192 tokens of 128 heads of 64 x 128 in 8 groups, bf16: 266 to 278 us, 1.65
-// TB/s, a quarter of it the first kernel. The matrix instructions of
-// both, counting the products of parts, are 148 us at a large product's rate;
-// beside them the splits, two barriers a chunk and the exchange through LDS.
+// 8192 tokens of 128 heads of 64 x 128 in 8 groups, bf16: 264 to 281 us, 1.65
+// TB/s, a quarter of it the first kernel. The matrix instructions of both,
+// counting the products of parts, are 133 us at a large product's rate. By the
+// counters they run in 25 % of the first kernel's clocks and 28 % of the last
+// one's, vector instructions (splits, factors, gates) are issued in 46 and 58
+// %, and LDS is busy in 28 and 37 %; what keeps these from overlapping more is
+// that a chunk's phases follow each other, two barriers in the first kernel and
+// three in the last, with 2.6 and 3 waves a SIMD.
 //
 // Values that are not finite: a zero of M times a NaN would carry it to earlier
 // tokens. So values of X, B and the step sizes that are not finite are read as
@@ -57,8 +62,9 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int Q = 64;                   // tokens of a chunk
 constexpr int NT_JOIN = 64;
-// Segments of a sequence whose states the last kernel puts together by itself: of 6 sequences of 4095 tokens together,
-// 16 segments, it takes 97 us where a kernel of its own for that makes it 114 us, of 8192 tokens of 128 heads 271 and 278.
+// Segments of a sequence whose states the last kernel puts together by itself. Whole calls: 6 sequences of 4095 tokens
+// together, 16 segments, 95 us, with a kernel of its own for that 112; 8192 tokens of 128 heads, 8 segments, 264 and 275;
+// 16384 tokens of 32 heads, 64 segments, 129 and 122.
 constexpr int FOLDED = 16;
 constexpr int NEVER = 0x7fffffff;
 constexpr int FRAG = 1024;              // 64 lanes x 16 bytes
@@ -904,6 +910,8 @@ int lds_bytes(bool f32, int kn, int heads)
 bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype dtype, Plan *l)
 {
     const bool f32 = dtype == CONV_F32;
+    // (64 rows of B and C of 256 states in three parts each would be 200 KB of LDS. Such prompts in fp32 go token by token:
+    // 4096 tokens of 32 heads of 64 x 256 in 2410 us, in bf16 by chunks in 85.)
     if (N > (f32 ? 128 : 256))
         return false;
     l->kn = N <= 64 ? 2 : N <= 128 ? 4 : 8;
@@ -919,10 +927,10 @@ bool make_plan(const Sequences &s, int H, int P, int groups, int N, conv_dtype d
         return false;
     l->wgs = (int)((group_jobs + l->jobs - 1) / l->jobs);
     // No segments where each compute unit has a workgroup without them: one prompt of 4096 tokens of 256 heads of 128 x
-    // 128 (256 workgroups) takes 397 us whole and 421 in two, 4095 tokens of 512 heads of 64 x 128 in six prompts 370 and
-    // 443. Otherwise segments such that some 512 workgroups have one (16384 tokens of 32 heads of 64 x 64: 107 us, with
-    // 256 131, with 1024 117; 8192 tokens of 128 heads of 64 x 128: 241, 287 and 258), but at most 64 to the longest
-    // sequence there can be (the first of these in 16: 150 us against 123), and none of less than 256 tokens.
+    // 128 (256 workgroups) takes 449 us whole and 456 in two, 4095 tokens of 512 heads of 64 x 128 in six prompts 415 and
+    // 419. Otherwise segments such that some 512 workgroups have one (16384 tokens of 32 heads of 64 x 64: 122 us, with
+    // 256 148, with 1024 135; 8192 tokens of 128 heads of 64 x 128: 264, 341 and 287), but at most 64 to the longest
+    // sequence there can be (the first of these in 16: 148), and none of less than 256 tokens. (Whole calls.)
     const int64_t longest = s.offsets ? s.tokens : s.each;
     const int64_t whole = (int64_t)l->wgs * groups;      // workgroups without segments
     int64_t seg = whole * (s.offsets ? 1 : s.num_seqs) >= 256 ? longest : s.tokens * whole / 512;

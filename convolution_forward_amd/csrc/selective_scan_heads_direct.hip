@@ -8,8 +8,11 @@
 // and waits for no other.
 //
 // Single tokens: the states' bytes are the time, each read and written once, past
-// the caches. 128 sequences of 128 heads of 64 x 128, bf16: 170 us, 6.3 TB/s
-// (184 through the caches); 8: 14.2 (15.8); one: 4.2 (4.6).
+// the caches. 128 sequences of 128 heads of 64 x 128, bf16: 173 us, 6.25 TB/s
+// (through the caches 181); 8: 13.7; one: 4.3. fp32, where two tokens of b and c
+// leave room for three waves a SIMD instead of four: 188. 129 to 256 states take
+// 216 registers in bf16, two waves (64 sequences of 128 heads of 64 x 256, as
+// many states: 187 us), and 278 in fp32, one wave (236).
 // Longer sequences are the chain from token to token; the next token's inputs
 // are loaded a token ahead.
 #include "common.h"
@@ -210,9 +213,9 @@ template <class T>
 void launch(const HeadScanProblem &p, hipStream_t s)
 {
     // Several rows a lane where their states are short and there are rows enough. A token of 16384 rows of 16 states
-    // takes 3.3 us with one row a lane and 4.0 with four, of 32768 4.4 and 4.2, of 2^20 66 and 43; of 16384 rows of 64
-    // states 4.7 with one and with two, of 65536 10.4 and 8.8, of 2^20 107 and 100. Of 128 states one is best: 2^20 rows
-    // take 184 us with one and 201 with two. (Before the states went past the caches.)
+    // takes 3.5 us with one row a lane and 4.1 with four, of 32768 4.5 and 4.3, of 2^20 64 and 40; of 16384 rows of 64
+    // states 4.2 with one and 4.4 with two, of 32768 5.9 and 5.3, of 2^20 99 and 91. Of 128 states one is best: 2^20 rows
+    // take 173 us with one and 178 with two.
     const int64_t rows = (int64_t)p.seq.num_seqs * p.H * p.P;
     if (p.N <= 32)
         rows <= 16384 ? launch_rows<T, 1, 1>(p, s) : launch_rows<T, 1, 4>(p, s);

@@ -27,12 +27,20 @@
 // first segment's initial state is kept in the place of the last one's, which
 // leaves none, since the call may overwrite it in place.
 //
-// 8192 tokens of 8192 channels of 16 states, bf16: 436 us, 1.24 TB/s; vector
-// instructions bound it. A token of a wave is 256 states: an exponential (8.3
-// clocks a wave), a product by the rate, and twice a product with b and the two
-// or three of the recurrence and y (2.7 each), 97 clocks, and some 60 of step
-// sizes, gates, conversions and exchanges, of 181 it takes at four waves a SIMD.
-// Four waves and tiles of 64 tokens, with the products d x b kept: 513 us.
+// 8192 tokens of 8192 channels of 16 states, bf16: 439 us, 1.23 TB/s; vector
+// instructions bound it. A token of a wave is 256 states, and takes a SIMD 257
+// clocks. By the counters it is 46 vector instructions, issued in 206 of them:
+// for each of a lane's four states an exponential, a product by the rate, twice
+// a product with b, and three of the recurrence and y, 28 together; the other 18
+// are step sizes, gates, conversions, sums over lanes and addresses. LDS is busy
+// in half of the clocks, 6 % of them bank conflicts; the rest is the three
+// barriers of a tile. Four waves and tiles of 64 tokens, with the products d x b
+// kept, took 513 us.
+//
+// With 8 states and fewer a thread has eight channels in steps 1 and 4 beside the
+// 64 decays, which then do not all stay in registers (10 go to memory in bf16, 24
+// in fp32): 409 us for 8192 channels of 8 states in bf16, 705 in fp32, against
+// 412 in fp32 for 16 states.
 #include "common.h"
 #include "eight_bit.h"
 #include "internal.h"
@@ -416,18 +424,18 @@ struct Plan {
 
 bool make_plan(const Sequences &s, int channels, int groups, int N, Plan *l)
 {
-    if (N > 32)
+    if (N > 32)         // more go token by token: 4096 tokens of 2048 channels of 64 states in 1700 us
         return false;
     l->ln = N <= 8 ? 2 : N <= 16 ? 4 : 8;
     l->group_slices = (channels / groups + 64 / l->ln - 1) / (64 / l->ln);
     if ((int64_t)l->group_slices * groups > (1 << 22))
         return false;
     l->slices = l->group_slices * groups;
-    // No segments where each compute unit has a workgroup without them: one prompt of 8192 tokens and 4096 channels of 16
-    // (256 workgroups) takes 296 us whole and 301 in two, of 6144 channels 432 and 526, 2047 tokens of 4096 channels in
-    // six prompts 70 and 97. Otherwise segments such that some 1024 workgroups have one (2048 channels: 165 us, with 512
-    // 173, whole 289; 1024 channels 90, 92 and 238), but at most 16 to the longest sequence there can be, and none of
-    // less than 256 tokens.
+    // No segments where each compute unit has a workgroup without them: one prompt of 8192 tokens and 6144 channels of 16
+    // takes 439 us whole and 491 in segments, 2047 tokens of 4096 channels in six prompts 75 and 100; the least such
+    // prompt, 4096 channels (256 workgroups), is the exception, 331 and 310. Otherwise segments such that some 1024
+    // workgroups have one (2048 channels: 171 us, with 512 176, whole 304; 1024 channels 92, 92 and 298), but at most 16
+    // to the longest sequence there can be, and none of less than 256 tokens.
     const int64_t longest = s.offsets ? s.tokens : s.each;
     int64_t seg = (int64_t)l->slices * (s.offsets ? 1 : s.num_seqs) >= 256 ? longest : s.tokens * l->slices / 1024;
     seg = seg > longest / 16 ? seg : longest / 16;
