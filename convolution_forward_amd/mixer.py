@@ -184,6 +184,10 @@ def selective_scan(x, dt, a, b, c, skip=None, gate=None, dt_bias=None, dt_softpl
     the same tensor. workspace: a uint8 tensor of at least
     selective_scan_workspace(...) bytes; without it one is taken from torch's
     allocator for the call. Returns y like x.
+
+    VARIANT_AUTO chooses between tiles (up to 32 states) and single steps for
+    the whole call, by its mean length: a prompt is best kept apart from many
+    single tokens.
     """
     r = (_binding or _load()).selective_scan(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, seq_offsets, initial_state,
                                              final_state, slots, out, workspace, variant)
@@ -203,6 +207,9 @@ def selective_scan_heads(x, dt, a, b, c, skip=None, gate=None, dt_bias=None, dt_
     [slots, H, P, states] float32, possibly the same tensor. workspace: a uint8
     tensor of at least selective_scan_heads_workspace(...) bytes; without it one
     is taken from torch's allocator for the call. Returns y like x.
+
+    VARIANT_AUTO chooses between chunks (float32: up to 128 states) and single
+    steps for the whole call, by its mean length, as in selective_scan.
     """
     r = (_binding or _load()).selective_scan_heads(x, dt, a, b, c, skip, gate, dt_bias, dt_softplus, seq_offsets,
                                                    initial_state, final_state, slots, out, workspace, variant)
