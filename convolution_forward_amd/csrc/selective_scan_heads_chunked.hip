@@ -24,8 +24,12 @@
 //
 // Precision: bf16 operands (B, C, X) are exact; every other operand (S, M, X
 // with its factors) and each fp32 one is split into three bf16 parts, x = hi +
-// mid + lo, 24 bits together, and the products of parts above 2^-24 are added
-// in fp32: three for an exact operand times a split one, six for two split ones.
+// mid + lo, 24 bits together, and the products of parts are added in fp32: three
+// for an exact operand times a split one, eight for two split ones. (Parts are
+// cut, so mid may be 2^-7 of x and lo 2^-15; lo lo is left out, 2^-30. Without
+// mid lo and lo mid, 2^-21 together, 8192 tokens of 128 heads in fp32 take 919 us
+// instead of 966; parts rounded to nearest, whose mid lo is 2^-25, 953, but hi
+// hi may then leave fp32's range where the product does not.)
 //
 // 8192 tokens of 128 heads of 64 x 128 in 8 groups, bf16: 264 to 281 us, 1.65
 // TB/s, a quarter of it the first kernel. The matrix instructions of both,
@@ -129,12 +133,12 @@ __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&part)[3])
         part[i] = __builtin_bit_cast(bf16x8, packed[i]);
 }
 
-// acc += a b, each of one exact part or three.
+// acc += a b, each of one exact part or three: small products first.
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 product(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 acc)
 {
 #pragma unroll
-    for (int k = 2; k >= 0; --k)
+    for (int k = NA + NB > 4 ? 3 : 2; k >= 0; --k)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
             if (k - i >= 0 && k - i < NB)
