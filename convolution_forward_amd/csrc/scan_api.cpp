@@ -73,8 +73,8 @@ conv_status check_heads_sizes(int64_t tokens, int num_seqs, int H, int P, int gr
     // us by chunks up to 32 tokens, and token by token 11.6 for 12 of them, 14.2
     // for 16; 8 such sequences 22 us (token by token 20 for 4 tokens, 24 for 6), 64
     // of them 147 and 157 (123 and 158). fp32, 32 heads of 64 x 64, where a chunk
-    // costs more: 11.5 us alone (24 tokens one by one 9.8, 32 12.0), 64 sequences
-    // 95 for 32 tokens and 111 for 64 (67 and 118, level at 58; a long sequence
+    // costs more: 11.9 us alone (24 tokens one by one 9.9, 32 12.1), 64 sequences
+    // 98 for 32 tokens and 114 for 64 (69 and 118, level at 60; a long sequence
     // among short ones gains by chunks, so less is asked for).
     const bool alone = (int64_t)num_seqs * H * P <= 16384;
     const int least = dtype == CONV_F32 ? (alone ? 24 : 44) : alone ? 12 : 6;
